@@ -281,6 +281,111 @@ int moe_mxfp4_forward_noalloc(const mxfp4_moe_dims* d, const void* packed_gfx950
                               int64_t ldx, const float* router_logits, int32_t top_k, int32_t renormalize,
                               void* y_bf16, int32_t* topk_ids, float* topk_w, void* stream);
 
+/* ------------------------------------------------------------------------------------------------
+ * Balance loss of the router, with the per-expert counts it is made of and its gradient.  [DEF]
+ *   p_t   = softmax of token t's logits over the E experts;
+ *   n_e   = number of pairs (t, j) with topk_ids[t, j] = e over the tokens that count;
+ *   loss  = E / (k V^2) * sum_e n_e * sum_t p_{t,e},  V = number of tokens that count
+ *           (1 when pairs and probabilities are spread evenly; 0 when V = 0);
+ *   dloss/dlogits_{t,e} = p_{t,e} * (d_e - sum_e' d_e' p_{t,e'}),  d_e = E / (k V^2) * (n_e - mean n).
+ * The counts are constants of the gradient.  d_e is taken less its mean, which drops out of the bracket.
+ * router_logits device fp32 [T, ldl], ldl >= E; E, top_k and T as in moe_mxfp4_route.  topk_ids device
+ *   int32 [T, top_k] contiguous; an id outside [0, E) is a dropped pair and is not counted.
+ * token_mask device uint8 [T] or NULL: a token counts when its byte is not 0.  The logits and ids of
+ *   other tokens are not looked at (any bits), and their gradient is 0.  A logit of -inf has p = 0; a
+ *   token whose logits are all -inf has p = 0 throughout and a gradient of 0.
+ * loss device fp32 [1], counts device int32 [E], coef device fp32 [E] (d_e, for the backward pass).
+ * workspace device, >= moe_balance_workspace_bytes(T, E), 256-byte aligned; nothing in it is kept
+ * between calls.  Sums over tokens run in binary32 inside a workgroup and in binary64 across
+ * workgroups, in a fixed order: repeated calls give the same bits.  T == 0 writes loss 0 and counts 0.
+ * moe_balance_backward: grad_loss device fp32 [1]; grad_logits device fp32 [T, E] contiguous, every
+ * element written.  Pointers of both need 4-byte alignment only (workspace aside).
+ */
+size_t moe_balance_workspace_bytes(int64_t T, int32_t E);
+int moe_balance_forward(const float* router_logits, int64_t T, int32_t E, int64_t ldl, const int32_t* topk_ids,
+                        int32_t top_k, const uint8_t* token_mask, float* loss, int32_t* counts, float* coef,
+                        void* workspace, size_t workspace_bytes, void* stream);
+int moe_balance_backward(const float* router_logits, int64_t T, int32_t E, int64_t ldl, const uint8_t* token_mask,
+                         const float* coef, const float* grad_loss, float* grad_logits, void* stream);
+
+/* Block formats of the entry points below. */
+enum {
+  MXFP4_FMT_MXFP4 = 0, /* E2M1, an E8M0 scale per 32 elements, as mxfp4_quantize writes it */
+  MXFP4_FMT_NVFP4 = 1, /* E2M1, an E4M3 scale per 16 elements and a global scale, as nvfp4_quantize */
+  MXFP4_FMT_MXFP8 = 2  /* E4M3, an E8M0 scale per 32 elements, as MXFP4_ACT_MXFP8 (the cache only) */
+};
+
+/* ------------------------------------------------------------------------------------------------
+ * Matrix-vector products with 4-bit weights: y = x W^T (/ global_scale) + b for one or a few rows of x.
+ * [DEF: the W4A16 linear layer, for NVFP4 weights too, in the form that decoding a token needs]
+ * Weights in the standard layout, as the quantizers write them (no pack): w_q uint8 [N, K/2] (16-byte
+ * aligned), w_s uint8 [N, K/32] E8M0 (MXFP4) or [N, K/16] E4M3 (NVFP4).  K is a multiple of the block
+ * (32 or 16), 1 <= N, K <= 2^20.  global_scale host, positive and finite (NVFP4; MXFP4 ignores it).
+ * bias [N] fp32 or bf16 or NULL.  x_bf16 device bf16 [M, ldx], ldx >= K, ldx % 8 == 0, 0 <= M <= 2^20.
+ * y device [M, ldy], ldy >= N, bf16 or fp32 (out_is_fp32).
+ * Arithmetic: a weight times its scale is exact in bf16 (at most six significant bits), the products
+ * accumulate in fp32, the global scale divides and the bias is added in fp32, one rounding to bf16.
+ * Weights of 2^128 and more, or of less than 2^-126, are outside the contract.
+ * Deterministic, and a row's result does not depend on the other rows.  The weights are read once per 16 rows
+ * of x: for many rows mxfp4_linear_forward is the faster layer. */
+int fp4_matvec(int32_t fmt, const void* w_q, const void* w_s, float global_scale, int64_t N, int64_t K,
+               const void* bias, int32_t bias_is_fp32, const void* x_bf16, int64_t M, int64_t ldx, void* y,
+               int64_t ldy, int32_t out_is_fp32, void* stream);
+
+/* The same product of every routed pair with its expert's matrix.  [DEF: the experts' products of the MoE
+ * layer, on weights in the standard layout]
+ *   y[p] = W_e x[p / top_k] / global_scales[e] + b_e   for p in sorted_pairs[offsets[e], offsets[e+1]);
+ *   swiglu != 0: the first N/2 rows of W_e are the gate, the others the up projection, and
+ *   y[p] = silu(gate) * up has N/2 columns (rows [w1; w3], as in the MoE layer).
+ * w_q [E, N, K/2], w_s [E, N, K/B], bias [E, N] or NULL, global_scales device fp32 [E] (NVFP4).
+ * expert_offsets device int32 [E + 1] and sorted_pairs device int32 [n_pairs]: moe_mxfp4_route's outputs
+ *   (offsets outside [0, n_pairs] are clamped, pairs outside it passed over; a pair that is not
+ *   listed keeps its row of y).  x has n_pairs / top_k rows: top_k as routed when the pairs of a token
+ *   share its row, 1 when every pair has a row of its own (the second product).
+ * y device [n_pairs, N or N/2] contiguous.  1 <= E, top_k <= 1024. */
+int fp4_expert_matvec(int32_t fmt, const void* w_q, const void* w_s, const float* global_scales, int32_t E, int64_t N,
+                      int64_t K, const void* bias, int32_t bias_is_fp32, const void* x_bf16, int64_t ldx,
+                      int32_t top_k, const int32_t* expert_offsets, const int32_t* sorted_pairs, int64_t n_pairs,
+                      int32_t swiglu, void* y, int32_t out_is_fp32, void* stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * Paged cache in a block format: rows are quantized as they are written and read back as bf16.
+ * [DEF: the quantizers' element and scale rules, applied to the cached rows of an attention layer]
+ * A cache holds num_pages pages of page_size tokens; a token has `heads` vectors of k_dim elements, and
+ * of v_dim elements in a second plane (v_dim = 0: one plane).  Caller-owned memory, per plane:
+ *   q uint8 [num_pages, page_size, heads, dim/2] (MXFP8: dim), 8-byte aligned;
+ *   s uint8 [num_pages, page_size, heads, dim/B], B the format's block (32; NVFP4: 16), dim % B == 0.
+ * Rows are ragged: rows [cu_rows[b], cu_rows[b + 1]) belong to sequence b and hold its positions
+ * start[b], start[b] + 1, ... (start NULL: from 0).  Position i lives in page page_table[b][i / page_size],
+ * slot i % page_size.  cu_rows device int32 [n_seqs + 1], non-decreasing; start device int32 [n_seqs] or
+ * NULL; page_table device int32 [n_seqs, ld_table], max_pages <= ld_table columns used.
+ * `rows` is the number of rows that k and v hold; rows before cu_rows[0] or from cu_rows[n_seqs] on are not
+ * read by the write and are left as they were by the read.  A position below 0, past max_pages or in a
+ * page outside [0, num_pages) is not written, and is read as zeros.
+ * The write quantizes each block of each row: MXFP4 and NVFP4 bit for bit as mxfp4_quantize and
+ * nvfp4_quantize, MXFP8 as MXFP4_ACT_MXFP8 quantizes activations.  Two rows of one call must not share a
+ * slot: what such a slot then holds is not specified.  The read returns code * scale (NVFP4: divided by the
+ * plane's global scale in binary32), rounded once to bf16.
+ * k / v device bf16, element (row, head, i) at row * ldt + head * ldh + i; ldt, ldh multiples of 8, ldh >= dim,
+ * ldt >= dim.  heads * dim <= 2^20.  Neither call uses a workspace.  The cache's pointers may be NULL when
+ * num_pages is 0, the table when max_pages is 0. */
+typedef struct {
+  int32_t fmt, heads, k_dim, v_dim, page_size;
+  int64_t num_pages;
+  float k_global_scale, v_global_scale; /* NVFP4: host, positive and finite */
+} mxfp4_cache_dims;
+
+/* Bytes of the four cache tensors, in the order k_q, k_s, v_q, v_s. */
+int mxfp4_cache_bytes(const mxfp4_cache_dims* d, size_t bytes_out[4]);
+int mxfp4_cache_write(const mxfp4_cache_dims* d, const void* k_bf16, int64_t k_ldt, int64_t k_ldh, const void* v_bf16,
+                      int64_t v_ldt, int64_t v_ldh, int64_t rows, const int32_t* cu_rows, const int32_t* start,
+                      const int32_t* page_table, int64_t ld_table, int32_t n_seqs, int32_t max_pages, void* k_q,
+                      void* k_s, void* v_q, void* v_s, void* stream);
+int mxfp4_cache_read(const mxfp4_cache_dims* d, const void* k_q, const void* k_s, const void* v_q, const void* v_s,
+                     int64_t rows, const int32_t* cu_rows, const int32_t* start, const int32_t* page_table,
+                     int64_t ld_table, int32_t n_seqs, int32_t max_pages, void* k_bf16, int64_t k_ldt, int64_t k_ldh,
+                     void* v_bf16, int64_t v_ldt, int64_t v_ldh, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

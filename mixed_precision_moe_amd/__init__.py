@@ -11,6 +11,7 @@ import torch
 
 from . import _lib
 from ._lib import MoeDims, Mxfp4Error, check
+from .ops import FMT_MXFP4, FMT_MXFP8, FMT_NVFP4, PagedCache, balance_loss, fp4_expert_matvec, fp4_matvec
 
 LAYOUT_GFX950 = 0
 LAYOUT_STD_W31 = 1
@@ -22,6 +23,7 @@ ACT_MXFP4 = 2  # both GEMM inputs quantized to MXFP4 (E2M1 + E8M0 per 32)
 
 __all__ = ["quantize", "tiled_scale_shape", "nvfp4_quantize", "nvfp4_tiled_scale_shape", "repack_weights", "unpack_weights", "check_packed", "route",
            "moe_forward", "moe_forward_noalloc", "NOALLOC_SCRATCH_BYTES", "MoE", "Linear", "MoeDims", "Mxfp4Error",
+           "balance_loss", "fp4_matvec", "fp4_expert_matvec", "PagedCache", "FMT_MXFP4", "FMT_NVFP4", "FMT_MXFP8",
            "LAYOUT_GFX950", "LAYOUT_STD_W31", "LAYOUT_SCALE_TILED", "ACT_BF16", "ACT_MXFP8", "ACT_MXFP4"]
 
 

@@ -16,6 +16,14 @@ class MoeDims(ctypes.Structure):
     _fields_ = [("E", c_i32), ("H", c_i32), ("I", c_i32), ("has_bias", c_i32)]
 
 
+class CacheDims(ctypes.Structure):
+    _fields_ = [("fmt", c_i32), ("heads", c_i32), ("k_dim", c_i32), ("v_dim", c_i32), ("page_size", c_i32),
+                ("num_pages", c_i64), ("k_global_scale", ctypes.c_float), ("v_global_scale", ctypes.c_float)]
+
+
+_CACHE_INDEX = [c_i64, c_p, c_p, c_p, c_i64, c_i32, c_i32]  # rows, cu_rows, start, page_table, ld_table, n_seqs, max_pages
+_CACHE_ROWS = [c_p, c_i64, c_i64, c_p, c_i64, c_i64]        # k, k_ldt, k_ldh, v, v_ldt, v_ldh
+
 _SIGS = {
     "mxfp4_status_str": (ctypes.c_char_p, [ctypes.c_int]),
     "mxfp4_version": (c_u32, []),
@@ -44,6 +52,16 @@ _SIGS = {
                                              c_i32, c_p, c_p, c_p, c_p, c_sz, c_p]),
     "moe_mxfp4_forward_profiled": (ctypes.c_int, [ctypes.POINTER(MoeDims), c_i32, c_p, c_p, c_i64, c_i64, c_p, c_i32,
                                                   c_i32, c_p, c_p, c_p, c_p, c_sz, c_p, ctypes.POINTER(c_p), c_i32]),
+    "moe_balance_workspace_bytes": (c_sz, [c_i64, c_i32]),
+    "moe_balance_forward": (ctypes.c_int, [c_p, c_i64, c_i32, c_i64, c_p, c_i32, c_p, c_p, c_p, c_p, c_p, c_sz, c_p]),
+    "moe_balance_backward": (ctypes.c_int, [c_p, c_i64, c_i32, c_i64, c_p, c_p, c_p, c_p, c_p]),
+    "fp4_matvec": (ctypes.c_int, [c_i32, c_p, c_p, ctypes.c_float, c_i64, c_i64, c_p, c_i32, c_p, c_i64, c_i64, c_p,
+                                  c_i64, c_i32, c_p]),
+    "fp4_expert_matvec": (ctypes.c_int, [c_i32, c_p, c_p, c_p, c_i32, c_i64, c_i64, c_p, c_i32, c_p, c_i64, c_i32, c_p,
+                                         c_p, c_i64, c_i32, c_p, c_i32, c_p]),
+    "mxfp4_cache_bytes": (ctypes.c_int, [ctypes.POINTER(CacheDims), ctypes.POINTER(c_sz)]),
+    "mxfp4_cache_write": (ctypes.c_int, [ctypes.POINTER(CacheDims)] + _CACHE_ROWS + _CACHE_INDEX + [c_p] * 5),
+    "mxfp4_cache_read": (ctypes.c_int, [ctypes.POINTER(CacheDims)] + [c_p] * 4 + _CACHE_INDEX + _CACHE_ROWS + [c_p]),
 }
 
 EXPORTED = tuple(_SIGS)

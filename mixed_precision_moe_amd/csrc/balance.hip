@@ -1,0 +1,365 @@
+// Balance loss of the router: per-expert counts, the loss and its gradient.
+//
+//   p_t = softmax(l_t),  S_e = sum_t p_te,  n_e = pairs of expert e,  V = tokens that count
+//   loss = E / (k V^2) * sum_e n_e S_e
+//   dl_te = g p_te (d_e - sum_e' d_e' p_te'),  d_e = E / (k V^2) (n_e - mean n)
+//
+// Both passes stream the logits once and are bound by that; everything about a token stays in registers.
+// A token's row lies across LPR lanes with VPL values each, so a wave holds 64 / LPR rows and a lane keeps
+// the same columns from row to row: S_e needs no exchange inside the loop.  The forward pass runs as
+// partial sums per workgroup and a second launch that joins them (32 columns a workgroup, binary64, fixed
+// order); the workgroup that is last to finish adds up the loss.  Few logits take one workgroup and one launch.
+#include <hip/hip_runtime.h>
+
+#include "ops.h"
+
+#define MX_DEV __device__ __forceinline__
+
+namespace {
+
+constexpr int kThreads = 256;  // of the first launch and the backward pass
+constexpr int kWaves = kThreads / 64;
+constexpr int kJoin = 1024;  // threads of the second launch
+constexpr int kJoinCols = 32;
+// The largest T * E that one workgroup takes by itself.
+constexpr int64_t kSingle = 8192;
+constexpr int kMaxBlocks = 512;
+
+typedef float f4_t __attribute__((ext_vector_type(4)));
+
+// ---------------------------------------------------------------------------------------------
+// Reductions over the LPR consecutive lanes of a row (4 <= LPR <= 64): every lane gets the same bits,
+// since each step adds a pair of values that both partners hold.
+template <int CTRL>
+MX_DEV float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+template <int LPR, typename F>
+MX_DEV float across(float v, F f) {
+  v = f(v, dpp<0xB1>(v));                    // lane ^ 1
+  v = f(v, dpp<0x4E>(v));                    // lane ^ 2
+  if (LPR == 8) v = f(v, __shfl_xor(v, 4));  // an 8-lane rotation is no DPP move
+  if (LPR >= 16) {
+    v = f(v, dpp<0x128>(v));  // rotate by 8 within 16 lanes
+    v = f(v, dpp<0x124>(v));  // rotate by 4
+  }
+  if (LPR >= 32) v = f(v, __shfl_xor(v, 16));
+  if (LPR >= 64) v = f(v, __shfl_xor(v, 32));
+  return v;
+}
+struct Add { MX_DEV float operator()(float a, float b) const { return a + b; } };
+struct Max { MX_DEV float operator()(float a, float b) const { return fmaxf(a, b); } };
+
+// Column of value i of the lane lr of its row.
+template <int LPR, int VPL, int VEC>
+MX_DEV int column(int lr, int i) {
+  return VEC == 4 ? ((i / 4) * LPR + lr) * 4 + (i & 3) : i * LPR + lr;
+}
+
+// One row's softmax in place: v holds the logits (-inf past E), then the probabilities.
+template <int LPR, int VPL>
+MX_DEV void softmax_row(float* v) {
+  float m = v[0];
+#pragma unroll
+  for (int i = 1; i < VPL; i++) m = fmaxf(m, v[i]);
+  m = across<LPR>(m, Max());
+  const bool any = m > -INFINITY;  // no logit but -inf: nothing to share out
+  if (!any) m = 0.0f;
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPL; i++) {
+    v[i] = __expf(v[i] - m);
+    s += v[i];
+  }
+  s = across<LPR>(s, Add());
+  const float r = any ? 1.0f / s : 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPL; i++) v[i] *= r;
+}
+
+template <int LPR, int VPL, int VEC>
+MX_DEV void load_row(const float* __restrict__ l, int E, int lr, float* v) {
+  if (VEC == 4) {
+#pragma unroll
+    for (int c = 0; c < VPL / 4; c++) {
+      const int col = (c * LPR + lr) * 4;
+      f4_t x = f4_t{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      if (col < E) x = *reinterpret_cast<const f4_t*>(l + col);
+#pragma unroll
+      for (int j = 0; j < 4; j++) v[4 * c + j] = x[j];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; i++) {
+      const int col = i * LPR + lr;
+      v[i] = -INFINITY;
+      if (col < E) v[i] = l[col];
+    }
+  }
+}
+
+// loss and coef from the joined sums; one workgroup, all threads.  n and S may be global or LDS.
+MX_DEV void finish(int E, int k, const int32_t* n, const double* S, int64_t V, float* loss, float* coef, double* red) {
+  const int t = threadIdx.x, nt = blockDim.x;
+  double dot = 0.0, pairs = 0.0;
+  for (int e = t; e < E; e += nt) {
+    dot += (double)n[e] * S[e];
+    pairs += (double)n[e];
+  }
+  red[t] = dot;
+  red[nt + t] = pairs;
+  __syncthreads();
+  for (int h = nt / 2; h > 0; h >>= 1) {
+    if (t < h) {
+      red[t] += red[t + h];
+      red[nt + t] += red[nt + t + h];
+    }
+    __syncthreads();
+  }
+  const double each = V > 0 ? (double)E / ((double)k * (double)V * (double)V) : 0.0;
+  const double mean = red[nt] / (double)E;
+  if (t == 0) *loss = (float)(each * red[0]);
+  for (int e = t; e < E; e += nt) coef[e] = (float)(each * ((double)n[e] - mean));
+}
+
+template <int LPR, int VPL, int VEC>
+__global__ __launch_bounds__(kThreads) void balance_forward_kernel(BalanceArgs a, float* __restrict__ part_p,
+                                                                   int32_t* __restrict__ part_n,
+                                                                   int32_t* __restrict__ part_v, uint32_t* ticket) {
+  constexpr int RPW = 64 / LPR;
+  constexpr int GROUPS = kWaves * RPW;  // rows in flight in the workgroup
+  constexpr int COLS = LPR * VPL;
+  __shared__ float cols[GROUPS * COLS];  // 16 bytes * kThreads * VPL / 4: 16 KB at VPL = 16
+  __shared__ int32_t hist[COLS];
+  __shared__ int32_t live_in[GROUPS];
+  const int t = threadIdx.x, E = a.E;
+  const int lr = t & (LPR - 1), group = t / LPR;
+  for (int e = t; e < E; e += kThreads) hist[e] = 0;
+  __syncthreads();
+
+  // the pairs' experts: a contiguous range of pairs a workgroup
+  const int64_t pairs = a.T * a.k, per = (pairs + gridDim.x - 1) / gridDim.x;
+  const int64_t p1 = min(pairs, (int64_t)(blockIdx.x + 1) * per);
+  for (int64_t p = (int64_t)blockIdx.x * per + t; p < p1; p += kThreads) {
+    const int32_t e = a.ids[p];
+    const bool counts = !a.mask || a.mask[(uint32_t)p / (uint32_t)a.k];  // T * k < 2^31
+    if (counts && e >= 0 && e < E) atomicAdd(&hist[e], 1);
+  }
+
+  float acc[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; i++) acc[i] = 0.0f;
+  int32_t live = 0;
+  for (int64_t r = (int64_t)blockIdx.x * GROUPS + group; r < a.T; r += (int64_t)gridDim.x * GROUPS) {
+    if (a.mask && !a.mask[r]) continue;  // uniform over the row's lanes, which exchange among themselves alone
+    float v[VPL];
+    load_row<LPR, VPL, VEC>(a.logits + r * a.ldl, E, lr, v);
+    softmax_row<LPR, VPL>(v);
+#pragma unroll
+    for (int i = 0; i < VPL; i++) acc[i] += v[i];
+    live++;
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; i++) cols[group * COLS + column<LPR, VPL, VEC>(lr, i)] = acc[i];
+  if (lr == 0) live_in[group] = live;
+  __syncthreads();
+
+  if (gridDim.x > 1) {
+    for (int e = t; e < E; e += kThreads) {
+      float s = 0.0f;
+      for (int g = 0; g < GROUPS; g++) s += cols[g * COLS + e];
+      part_p[(int64_t)blockIdx.x * E + e] = s;
+      part_n[(int64_t)blockIdx.x * E + e] = hist[e];
+    }
+    if (t == 0) {
+      int32_t v = 0;
+      for (int g = 0; g < GROUPS; g++) v += live_in[g];
+      part_v[blockIdx.x] = v;
+      if (blockIdx.x == 0) *ticket = 0;  // for the second launch
+    }
+    return;
+  }
+  __shared__ double sums[COLS];
+  __shared__ double red[2 * kThreads];
+  for (int e = t; e < E; e += kThreads) {
+    double s = 0.0;
+    for (int g = 0; g < GROUPS; g++) s += (double)cols[g * COLS + e];
+    sums[e] = s;
+    a.counts[e] = hist[e];
+  }
+  int64_t V = 0;
+  for (int g = 0; g < GROUPS; g++) V += live_in[g];
+  __syncthreads();
+  finish(E, a.k, hist, sums, V, a.loss, a.coef, red);
+}
+
+// Joins the partial sums of `blocks` workgroups: kJoinCols columns a workgroup, 32 threads a column.
+__global__ __launch_bounds__(kJoin) void balance_join_kernel(BalanceArgs a, int32_t blocks,
+                                                             const float* __restrict__ part_p,
+                                                             const int32_t* __restrict__ part_n,
+                                                             const int32_t* __restrict__ part_v, double* sums,
+                                                             uint32_t* ticket) {
+  constexpr int SPLIT = kJoin / kJoinCols;
+  __shared__ double red[2 * kJoin];
+  __shared__ int32_t redn[kJoin];
+  __shared__ bool last;
+  const int t = threadIdx.x, E = a.E;
+  const int c = t % kJoinCols, part = t / kJoinCols, e = blockIdx.x * kJoinCols + c;
+  double s = 0.0;
+  int32_t n = 0;
+  if (e < E) {
+#pragma unroll 4
+    for (int b = part; b < blocks; b += SPLIT) {
+      s += (double)part_p[(int64_t)b * E + e];
+      n += part_n[(int64_t)b * E + e];
+    }
+  }
+  red[t] = s;
+  redn[t] = n;
+  __syncthreads();
+  if (t < kJoinCols && e < E) {
+    for (int q = 1; q < SPLIT; q++) {
+      s += red[q * kJoinCols + c];
+      n += redn[q * kJoinCols + c];
+    }
+    sums[e] = s;
+    a.counts[e] = n;
+  }
+  __threadfence();
+  __syncthreads();
+  if (t == 0) last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  // the tokens that count: every thread a few workgroups' numbers, then a tree
+  int32_t v = 0;
+  for (int b = t; b < blocks; b += kJoin) v += part_v[b];
+  redn[t] = v;
+  __syncthreads();
+  for (int h = kJoin / 2; h > 0; h >>= 1) {
+    if (t < h) redn[t] += redn[t + h];
+    __syncthreads();
+  }
+  finish(E, a.k, a.counts, sums, redn[0], a.loss, a.coef, red);
+}
+
+template <int LPR, int VPL, int VEC>
+__global__ __launch_bounds__(kThreads) void balance_backward_kernel(const float* __restrict__ logits, int64_t T, int E,
+                                                                    int64_t ldl, const uint8_t* __restrict__ mask,
+                                                                    const float* __restrict__ coef,
+                                                                    const float* __restrict__ grad_loss,
+                                                                    float* __restrict__ grad) {
+  constexpr int GROUPS = kWaves * (64 / LPR);
+  const int lr = threadIdx.x & (LPR - 1), group = threadIdx.x / LPR;
+  const float g = *grad_loss;
+  float d[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; i++) {
+    const int col = column<LPR, VPL, VEC>(lr, i);
+    d[i] = col < E ? coef[col] : 0.0f;
+  }
+  for (int64_t r = (int64_t)blockIdx.x * GROUPS + group; r < T; r += (int64_t)gridDim.x * GROUPS) {
+    float v[VPL];
+    if (!mask || mask[r]) {
+      load_row<LPR, VPL, VEC>(logits + r * ldl, E, lr, v);
+      softmax_row<LPR, VPL>(v);
+      // the weighted mean of d, taken off twice: where one expert holds nearly all of the row, its own d
+      // less the mean is small, and what the first mean's rounding left would be all of it
+      float mean = 0.0f, rest = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VPL; i++) mean += v[i] * d[i];
+      mean = across<LPR>(mean, Add());
+#pragma unroll
+      for (int i = 0; i < VPL; i++) rest += v[i] * (d[i] - mean);
+      rest = across<LPR>(rest, Add());
+#pragma unroll
+      for (int i = 0; i < VPL; i++) v[i] = g * v[i] * ((d[i] - mean) - rest);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; i++) v[i] = 0.0f;
+    }
+    float* out = grad + r * E;
+    if (VEC == 4) {
+#pragma unroll
+      for (int c = 0; c < VPL / 4; c++) {
+        const int col = (c * LPR + lr) * 4;
+        if (col < E) *reinterpret_cast<f4_t*>(out + col) = f4_t{v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]};
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; i++) {
+        const int col = i * LPR + lr;
+        if (col < E) out[col] = v[i];
+      }
+    }
+  }
+}
+
+// Lanes and values per row: VPL * LPR >= E, short reductions for few experts, at most 16 values a lane.
+// f is called with the constants of the variant.
+template <int L, int V>
+struct RowShape { static constexpr int LPR = L, VPL = V; };
+template <typename F>
+int with_shape(int E, F f) {
+  if (E <= 16) return f(RowShape<4, 4>());
+  if (E <= 32) return f(RowShape<8, 4>());
+  if (E <= 64) return f(RowShape<16, 4>());
+  if (E <= 128) return f(RowShape<16, 8>());
+  if (E <= 256) return f(RowShape<32, 8>());
+  if (E <= 384) return f(RowShape<32, 12>());
+  if (E <= 512) return f(RowShape<32, 16>());
+  if (E <= 768) return f(RowShape<64, 12>());
+  return f(RowShape<64, 16>());
+}
+template <typename R>
+constexpr int rows_in_flight() { return kWaves * (64 / R::LPR); }
+
+bool vec4(const void* p, int64_t ld, int E) { return E % 4 == 0 && ld % 4 == 0 && ((uintptr_t)p & 15) == 0; }
+
+int status() { return hipGetLastError() == hipSuccess ? MXFP4_OK : MXFP4_ERR_DEVICE; }
+
+}  // namespace
+
+int32_t balance_blocks(int64_t T, int32_t E) {
+  if (T * E <= kSingle) return 1;
+  return with_shape(E, [&](auto r) {
+    const int64_t n = (T + rows_in_flight<decltype(r)>() - 1) / rows_in_flight<decltype(r)>();
+    return (int)(n < kMaxBlocks ? n : kMaxBlocks);
+  });
+}
+
+int launch_balance_forward(const BalanceArgs& a, const BalanceWs& w, uint8_t* ws, hipStream_t stream) {
+  float* pp = (float*)(ws + w.part_p);
+  int32_t *pn = (int32_t*)(ws + w.part_n), *pv = (int32_t*)(ws + w.part_v);
+  uint32_t* ticket = (uint32_t*)(ws + w.ticket);
+  const int st = with_shape(a.E, [&](auto r) {
+    using R = decltype(r);
+    if (vec4(a.logits, a.ldl, a.E))
+      hipLaunchKernelGGL((balance_forward_kernel<R::LPR, R::VPL, 4>), dim3(w.blocks), dim3(kThreads), 0, stream, a, pp,
+                         pn, pv, ticket);
+    else
+      hipLaunchKernelGGL((balance_forward_kernel<R::LPR, R::VPL, 1>), dim3(w.blocks), dim3(kThreads), 0, stream, a, pp,
+                         pn, pv, ticket);
+    return status();
+  });
+  if (st || w.blocks == 1) return st;
+  hipLaunchKernelGGL(balance_join_kernel, dim3((a.E + kJoinCols - 1) / kJoinCols), dim3(kJoin), 0, stream, a, w.blocks,
+                     pp, pn, pv, (double*)(ws + w.sums), ticket);
+  return status();
+}
+
+int launch_balance_backward(const float* logits, int64_t T, int32_t E, int64_t ldl, const uint8_t* mask,
+                            const float* coef, const float* grad_loss, float* grad, hipStream_t stream) {
+  return with_shape(E, [&](auto r) {
+    using R = decltype(r);
+    const int64_t n = (T + rows_in_flight<R>() - 1) / rows_in_flight<R>();
+    const dim3 grid((unsigned)(n < 2048 ? n : 2048));
+    if (vec4(logits, ldl, E) && vec4(grad, E, E))
+      hipLaunchKernelGGL((balance_backward_kernel<R::LPR, R::VPL, 4>), grid, dim3(kThreads), 0, stream, logits, T, E,
+                         ldl, mask, coef, grad_loss, grad);
+    else
+      hipLaunchKernelGGL((balance_backward_kernel<R::LPR, R::VPL, 1>), grid, dim3(kThreads), 0, stream, logits, T, E,
+                         ldl, mask, coef, grad_loss, grad);
+    return status();
+  });
+}

@@ -1,0 +1,276 @@
+"""The balance loss, the 4-bit matrix-vector products and the block-quantized paged cache: the torch binding of
+their C entry points.  Like the rest of the binding it checks dtypes, shapes and devices, allocates
+outputs and passes raw pointers; the work runs on the current stream of the tensors' device."""
+
+import ctypes
+
+import torch
+
+from . import _lib
+from ._lib import CacheDims, check
+
+FMT_MXFP4 = 0  # E2M1, an E8M0 scale per 32 elements (quantize)
+FMT_NVFP4 = 1  # E2M1, an E4M3 scale per 16 elements and a global scale (nvfp4_quantize)
+FMT_MXFP8 = 2  # E4M3, an E8M0 scale per 32 elements (the cache only)
+
+_GROUP = {FMT_MXFP4: 32, FMT_NVFP4: 16, FMT_MXFP8: 32}
+
+
+def _need(cond, msg):
+    if not cond:
+        raise ValueError(msg)
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _same_device(first, name, **others):
+    """Every tensor on the GPU that holds `first`."""
+    _need(first.is_cuda, f"{name} must be a GPU tensor")
+    for n, t in others.items():
+        _need(t is None or t.device == first.device, f"{n} must be on {name}'s device")
+
+
+def _call(device, fn, *args):
+    """fn(*args, stream) on the current stream of `device`, which need not be the current device."""
+    if device.index == torch.cuda.current_device():
+        check(fn, getattr(_lib.lib(), fn)(*args, torch.cuda.current_stream(device).cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            check(fn, getattr(_lib.lib(), fn)(*args, torch.cuda.current_stream(device).cuda_stream))
+
+
+# ------------------------------------------------------------------------------------------------
+# Balance loss.
+
+
+def _row_step(t):
+    """Elements from row to row; the stride of a single row says nothing."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+class _BalanceLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, topk_ids, mask):
+        T, E = logits.shape
+        dev = logits.device
+        nws = _lib.lib().moe_balance_workspace_bytes(T, E)
+        _need(nws > 0, "invalid balance loss arguments")
+        ws = torch.empty(nws, dtype=torch.uint8, device=dev)
+        loss = torch.empty((), dtype=torch.float32, device=dev)
+        coef = torch.empty(E, dtype=torch.float32, device=dev)
+        counts = torch.empty(E, dtype=torch.int32, device=dev)
+        _call(dev, "moe_balance_forward", _ptr(logits), T, E, _row_step(logits), _ptr(topk_ids), topk_ids.shape[1],
+              _ptr(mask), _ptr(loss), _ptr(counts), _ptr(coef), _ptr(ws), nws)
+        ctx.save_for_backward(logits, coef, mask)
+        ctx.mark_non_differentiable(counts)
+        ctx.set_materialize_grads(False)
+        return loss, counts
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g, _):
+        if g is None:
+            return None, None, None
+        logits, coef, mask = ctx.saved_tensors
+        T, E = logits.shape
+        grad = torch.empty((T, E), dtype=torch.float32, device=logits.device)
+        _call(logits.device, "moe_balance_backward", _ptr(logits), T, E, _row_step(logits), _ptr(mask), _ptr(coef),
+              _ptr(g), _ptr(grad))
+        return grad, None, None
+
+
+def balance_loss(logits, topk_ids, token_mask=None):
+    """The router's balance loss and per-expert counts.
+
+    logits fp32 [T, E] (rows may be strided), topk_ids int32 [T, k] as `route` returns them (an id outside
+    [0, E) is a dropped pair), token_mask bool or uint8 [T] or None: tokens that count.  Returns (loss, counts):
+    loss fp32, 0-dim, differentiable in the logits: E / (k V^2) * sum_e counts_e * sum_t softmax(logits_t)_e
+    over the V tokens that count (0 without any); counts int32 [E], constants of the gradient."""
+    _same_device(logits, "logits", topk_ids=topk_ids, token_mask=token_mask)
+    _need(logits.dtype == torch.float32 and logits.dim() == 2, "logits: fp32 [T, E]")
+    _need(logits.stride(1) == 1 or logits.shape[1] == 1, "logits' last dimension must be contiguous")
+    T, E = logits.shape
+    _need(T <= 1 or logits.stride(0) >= E, "logits' rows must not overlap")
+    _need(topk_ids.dtype == torch.int32 and topk_ids.dim() == 2 and topk_ids.shape[0] == T and topk_ids.is_contiguous(),
+          "topk_ids: contiguous int32 [T, k]")
+    if token_mask is not None:
+        _need(token_mask.dtype in (torch.bool, torch.uint8) and token_mask.shape == (T,) and token_mask.is_contiguous(),
+              "token_mask: contiguous bool or uint8 [T]")
+    return _BalanceLoss.apply(logits, topk_ids, token_mask)
+
+
+# ------------------------------------------------------------------------------------------------
+# Matrix-vector products.
+
+
+def _check_weights(w_q, w_s, fmt, dims):
+    _need(fmt in (FMT_MXFP4, FMT_NVFP4), "fmt must be FMT_MXFP4 or FMT_NVFP4")
+    for n, t in (("w_q", w_q), ("w_s", w_s)):
+        _need(t.dtype == torch.uint8 and t.is_contiguous() and t.dim() == dims, f"{n} must be contiguous uint8 {dims}-D")
+    K = 2 * w_q.shape[-1]
+    _need(K % _GROUP[fmt] == 0 and w_s.shape == (*w_q.shape[:-1], K // _GROUP[fmt]), "w_s shape")
+    return K
+
+
+def _check_bias(bias, shape):
+    if bias is not None:
+        _need(bias.dtype in (torch.float32, torch.bfloat16) and bias.shape == shape and bias.is_contiguous(),
+              f"bias: contiguous fp32 or bf16 {list(shape)}")
+    return 1 if bias is not None and bias.dtype == torch.float32 else 0
+
+
+def _check_out(out_dtype):
+    _need(out_dtype in (torch.bfloat16, torch.float32), "out_dtype must be bfloat16 or float32")
+    return 1 if out_dtype == torch.float32 else 0
+
+
+def _row_stride(x, K):
+    _need(x.dtype == torch.bfloat16 and x.dim() == 2 and x.shape[1] == K and (x.stride(1) == 1 or K == 1), "x: bf16 rows [*, K]")
+    _need(x.shape[0] <= 1 or x.stride(0) >= K, "x's rows must not overlap")
+    return x.stride(0) if x.shape[0] > 1 else K + -K % 8
+
+
+def fp4_matvec(x, w_q, w_s, bias=None, *, fmt=FMT_MXFP4, global_scale=None, out_dtype=torch.bfloat16):
+    """y = x W^T (/ global_scale) + b for one or a few rows of x: the decoding form of the W4A16 linear layer,
+    on weights as `quantize` (FMT_MXFP4) or `nvfp4_quantize` (FMT_NVFP4, with its global_scale) returns them.
+
+    x bf16 [M, K] (rows may be strided), w_q uint8 [N, K/2], w_s uint8 flat scales [N, K/32] or [N, K/16], bias fp32
+    or bf16 [N] or None.  Returns y [M, N] in out_dtype (bfloat16 or float32)."""
+    _same_device(x, "x", w_q=w_q, w_s=w_s, bias=bias)
+    K = _check_weights(w_q, w_s, fmt, 2)
+    N, M = w_q.shape[0], x.shape[0]
+    ldx = _row_stride(x, K)
+    _need((global_scale is not None) == (fmt == FMT_NVFP4), "global_scale goes with FMT_NVFP4, and only with it")
+    is_fp32 = _check_bias(bias, (N,))
+    out_fp32 = _check_out(out_dtype)
+    y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+    _call(x.device, "fp4_matvec", fmt, _ptr(w_q), _ptr(w_s), 1.0 if global_scale is None else float(global_scale), N, K,
+          _ptr(bias), is_fp32, _ptr(x), M, ldx, _ptr(y), N, out_fp32)
+    return y
+
+
+def fp4_expert_matvec(x, w_q, w_s, expert_offsets, sorted_pairs, bias=None, *, fmt=FMT_MXFP4, global_scales=None,
+                      top_k=1, swiglu=False, out_dtype=torch.bfloat16, y=None):
+    """Every routed pair's product with its expert's matrix, on weights in the standard layout.
+
+    x bf16 [P / top_k, K]: row p // top_k is the input of pair p (top_k as routed for the first product, 1 where
+    every pair has its own row).  w_q uint8 [E, N, K/2], w_s uint8 [E, N, K/32] (NVFP4: [E, N, K/16]), bias [E, N]
+    or None, global_scales fp32 [E] (NVFP4).  expert_offsets int32 [E + 1] and sorted_pairs int32 [P] as `route`
+    returns them.  Returns y [P, N], or [P, N/2] = silu(gate rows) * up rows with swiglu (rows [w1; w3]).  A pair
+    that sorted_pairs does not list keeps what its row of `y` held."""
+    _same_device(x, "x", w_q=w_q, w_s=w_s, bias=bias, expert_offsets=expert_offsets, sorted_pairs=sorted_pairs,
+                 global_scales=global_scales, y=y)
+    K = _check_weights(w_q, w_s, fmt, 3)
+    E, N = w_q.shape[:2]
+    ldx = _row_stride(x, K)
+    for n, t in (("expert_offsets", expert_offsets), ("sorted_pairs", sorted_pairs)):
+        _need(t.dtype == torch.int32 and t.dim() == 1 and t.is_contiguous(), f"{n}: contiguous int32 1-D")
+    _need(expert_offsets.shape[0] == E + 1, "expert_offsets: E + 1 entries")
+    P = sorted_pairs.shape[0]
+    _need(top_k >= 1 and x.shape[0] * top_k == P, "x must have one row for every top_k pairs")
+    _need((global_scales is not None) == (fmt == FMT_NVFP4), "global_scales goes with FMT_NVFP4, and only with it")
+    if global_scales is not None:
+        _need(global_scales.dtype == torch.float32 and global_scales.shape == (E,) and global_scales.is_contiguous(),
+              "global_scales: contiguous fp32 [E]")
+    _need(not swiglu or N % 2 == 0, "swiglu needs an even number of rows")
+    is_fp32 = _check_bias(bias, (E, N))
+    width = N // 2 if swiglu else N
+    if y is None:
+        out_fp32 = _check_out(out_dtype)
+        y = torch.empty((P, width), dtype=out_dtype, device=x.device)
+    else:
+        out_fp32 = _check_out(y.dtype)
+        _need(y.shape == (P, width) and y.is_contiguous(), "y: contiguous [P, N] (swiglu: [P, N/2])")
+    _call(x.device, "fp4_expert_matvec", fmt, _ptr(w_q), _ptr(w_s), _ptr(global_scales), E, N, K, _ptr(bias), is_fp32,
+          _ptr(x), ldx, top_k, _ptr(expert_offsets), _ptr(sorted_pairs), P, 1 if swiglu else 0, _ptr(y), out_fp32)
+    return y
+
+
+# ------------------------------------------------------------------------------------------------
+# Paged cache.
+
+
+class PagedCache:
+    """A paged cache of keys and values (or one plane, v_dim=0) held in a block format.
+
+    A token has `heads` vectors of k_dim (and v_dim; None: k_dim) elements; page_size tokens make a page.
+    The memory is four uint8 tensors k_q, k_s, v_q, v_s (codes [num_pages, page_size, heads, dim/2], MXFP8: dim;
+    scales [num_pages, page_size, heads, dim/32], NVFP4: dim/16), allocated as zeros or given as `storage`."""
+
+    def __init__(self, num_pages, page_size, heads, k_dim, v_dim=None, fmt=FMT_MXFP8, k_global_scale=1.0,
+                 v_global_scale=1.0, storage=None, device=None):
+        v_dim = k_dim if v_dim is None else v_dim
+        self.dims = CacheDims(fmt, heads, k_dim, v_dim, page_size, num_pages, k_global_scale, v_global_scale)
+        sizes = (ctypes.c_size_t * 4)()
+        check("mxfp4_cache_bytes", _lib.lib().mxfp4_cache_bytes(ctypes.byref(self.dims), sizes))
+        per = 1 if fmt == FMT_MXFP8 else 2
+        shapes = [(num_pages, page_size, heads, d // by) for d in (k_dim, v_dim) for by in (per, _GROUP[fmt])]
+        if storage is None:
+            device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+            storage = [torch.zeros(s, dtype=torch.uint8, device=device) if s[-1] else None for s in shapes]
+        _need(len(storage) == 4, "storage: (k_q, k_s, v_q, v_s)")
+        for n, t, s in zip(("k_q", "k_s", "v_q", "v_s"), storage, shapes):
+            if s[-1] == 0:
+                _need(t is None, f"{n} must be None when v_dim is 0")
+                continue
+            _need(t is not None and t.dtype == torch.uint8 and t.shape == s and t.is_contiguous(),
+                  f"{n}: contiguous uint8 {list(s)}")
+        self.k_q, self.k_s, self.v_q, self.v_s = storage
+        _same_device(self.k_q, "k_q", k_s=self.k_s, v_q=self.v_q, v_s=self.v_s)
+        self._dref = ctypes.byref(self.dims)
+
+    def _index(self, page_table, cu_rows, start):
+        _same_device(self.k_q, "the cache", page_table=page_table, cu_rows=cu_rows, start=start)
+        _need(page_table.dtype == torch.int32 and page_table.dim() == 2 and
+              (page_table.stride(1) == 1 or page_table.shape[1] <= 1), "page_table: int32 [B, pages]")
+        B, P = page_table.shape
+        _need(cu_rows.dtype == torch.int32 and cu_rows.shape == (B + 1,) and cu_rows.is_contiguous(),
+              "cu_rows: contiguous int32 [B + 1]")
+        if start is not None:
+            _need(start.dtype == torch.int32 and start.shape == (B,) and start.is_contiguous(), "start: contiguous int32 [B]")
+        _need(B <= 1 or page_table.stride(0) >= P, "page_table's rows must not overlap")
+        return _ptr(cu_rows), _ptr(start), _ptr(page_table), page_table.stride(0) if B > 1 else P, B, P
+
+    def _rows(self, t, name, dim):
+        _need(t.dtype == torch.bfloat16 and t.dim() == 3 and t.shape[1:] == (self.dims.heads, dim) and t.stride(2) == 1,
+              f"{name}: bf16 [rows, {self.dims.heads}, {dim}], last dimension contiguous")
+        # the stride of a dimension of one entry says nothing
+        return (_ptr(t), t.stride(0) if t.shape[0] > 1 else self.dims.heads * dim + -self.dims.heads * dim % 8,
+                t.stride(1) if self.dims.heads > 1 else dim + -dim % 8)
+
+    def _planes(self, k, v):
+        d = self.dims
+        _need((v is None) == (d.v_dim == 0), "v goes with v_dim > 0, and only with it")
+        _same_device(self.k_q, "the cache", k=k, v=v)
+        _need(v is None or v.shape[0] == k.shape[0], "k and v must have the same number of rows")
+        return (*self._rows(k, "k", d.k_dim), *((None, 0, 0) if v is None else self._rows(v, "v", d.v_dim)))
+
+    def write(self, k, v, page_table, cu_rows, start=None):
+        """Quantizes the rows of k [rows, heads, k_dim] and v (None with v_dim=0) into the cache.  Rows
+        [cu_rows[b], cu_rows[b+1]) are sequence b's positions start[b], start[b]+1, ... (start None: from 0);
+        position i lives in page page_table[b, i // page_size].  Rows outside every sequence, and positions without
+        a page (past the table, or a page number outside the cache), are passed over.  Two rows of one call must not
+        share a slot."""
+        index = self._index(page_table, cu_rows, start)
+        planes = self._planes(k, v)
+        _call(self.k_q.device, "mxfp4_cache_write", self._dref, *planes, k.shape[0], *index, _ptr(self.k_q),
+              _ptr(self.k_s), _ptr(self.v_q), _ptr(self.v_s))
+
+    def read(self, page_table, cu_rows, start=None, rows=None, k_out=None, v_out=None):
+        """Reads rows back as bf16: (k [rows, heads, k_dim], v or None), rows and positions as in `write`.  Give
+        `rows` (the outputs are allocated; rows outside every sequence are then undefined) or the outputs, whose
+        rows outside every sequence are left as they were.  Positions without a page read as zeros."""
+        index = self._index(page_table, cu_rows, start)
+        d = self.dims
+        if k_out is None:
+            _need(rows is not None and rows >= 0 and v_out is None, "give rows, or the outputs")
+            k_out = torch.empty((rows, d.heads, d.k_dim), dtype=torch.bfloat16, device=self.k_q.device)
+            if d.v_dim:
+                v_out = torch.empty((rows, d.heads, d.v_dim), dtype=torch.bfloat16, device=self.k_q.device)
+        planes = self._planes(k_out, v_out)
+        _need(rows is None or rows == k_out.shape[0], "rows must be the outputs' rows")
+        _call(self.k_q.device, "mxfp4_cache_read", self._dref, _ptr(self.k_q), _ptr(self.k_s), _ptr(self.v_q),
+              _ptr(self.v_s), k_out.shape[0], *index, *planes)
+        return k_out, v_out

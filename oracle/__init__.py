@@ -40,4 +40,4 @@ sign kept on codes that round to zero.  Those two are "parity unpinned" with res
 they are fixed by this library's ABI and tested only for internal consistency.
 """
 
-from . import quant, convert, route, moe, linear  # noqa: F401
+from . import quant, convert, route, moe, linear, balance, matvec, cache  # noqa: F401

@@ -1,0 +1,50 @@
+"""Oracle: the paged cache in a block format.
+
+Test infrastructure only (see the package docstring).  Rows are quantized with the quantizers' rules (MXFP4 and
+NVFP4 as the matrix quantizers, MXFP8 as the quantized activations) and placed through a page table [DEF].
+"""
+
+import numpy as np
+
+from . import quant as Q
+
+
+def slots_ref(rows, cu, start, table, page_size, num_pages):
+    """Row by row, in plain Python: the slot of each row, -1 where its position has no page, None where the row
+    belongs to no sequence."""
+    out = [None] * rows
+    for b in range(len(cu) - 1):
+        for t in range(max(0, int(cu[b])), min(rows, int(cu[b + 1]))):
+            pos = t - int(cu[b]) + (0 if start is None else int(start[b]))
+            page = int(table[b][pos // page_size]) if 0 <= pos < len(table[b]) * page_size else -1
+            out[t] = page * page_size + pos % page_size if 0 <= page < num_pages else -1
+    return out
+
+
+def encode_ref(x_bits, fmt, gs):
+    """x_bits uint16 [..., D] -> (codes, scales) as the cache holds them."""
+    D = x_bits.shape[-1]
+    flat = np.ascontiguousarray(x_bits).reshape(-1, D)
+    if fmt == "mxfp4":
+        q, s = Q.quantize_ref(flat)
+    elif fmt == "nvfp4":
+        q, s = Q.nvfp4_quantize_ref(flat, gs)
+    else:
+        q, s = Q.mxfp8_quantize_values_ref(Q.bf16_to_f64(flat).astype(np.float32))
+    return q.reshape(*x_bits.shape[:-1], -1), s.reshape(*x_bits.shape[:-1], -1)
+
+
+def decode_ref(q, s, fmt, gs):
+    """The cached values as binary32 numbers, one rounding from bf16: the MX formats' are exact, NVFP4's are a
+    binary32 quotient."""
+    if fmt == "mxfp4":
+        return Q.dequant_ref(q, s).astype(np.float32)
+    if fmt == "mxfp8":
+        return Q.mxfp8_dequant_ref(q, s).astype(np.float32)
+    return (Q.nvfp4_dequant_ref(q, s, 1.0).astype(np.float32) / np.float32(gs)).astype(np.float32)
+
+
+def bf16_bits(v):
+    """binary32 -> bf16 bits, nearest even; infinities stay."""
+    u = np.asarray(v, dtype=np.float32).view(np.uint32).astype(np.uint64)
+    return ((u + 0x7FFF + ((u >> np.uint64(16)) & np.uint64(1))) >> np.uint64(16)).astype(np.uint16)

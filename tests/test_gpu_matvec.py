@@ -1,0 +1,283 @@
+"""GPU parity of the 4-bit matrix-vector products, dense and per routed pair, with the float64 oracle.
+
+Tolerance, from the arithmetic (u = 2^-24).  Weights times their scales are exact in bf16 and so are the products
+in binary32; an output is a sum of K products, of which at most 32 inside one matrix instruction, then K / 128
+accumulations in sequence and 16 partial sums add a rounding each (counted twice, whichever way the matrix unit
+rounds): 2 (K / 128 + 48) u of sum |x W|.  The global scale's division and the bias add 2 u each of what they give, and
+the result is rounded once: 2^-9 of itself to bf16 and half an ulp (2^-8 bounds it at every place of a binade) or u.
+SwiGLU: silu has a slope of at most 1.1, its own evaluation errs by (|g| + 8) u.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import mixed_precision_moe_amd as mx
+from mixed_precision_moe_amd import synth
+from oracle import matvec as V
+from oracle import quant as Q
+from tests.gpu_common import bf16_dev
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+FMTS = {"mxfp4": mx.FMT_MXFP4, "nvfp4": mx.FMT_NVFP4}
+
+
+def host(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def weights(g, shape, fmt, sigma=0.02):
+    """Quantized weights [..., N, K]: (q, s, global scale or None) on the host."""
+    N, K = shape[-2:]
+    gs = float(np.float32(448.0 / sigma)) if fmt == "nvfp4" else None
+    q, s = [], []
+    for _ in range(int(np.prod(shape[:-2]))):
+        w = synth.to_bf16_bits(g.standard_normal((N, K), dtype=np.float32) * np.float32(sigma))
+        a, b = Q.nvfp4_quantize_ref(w, gs) if fmt == "nvfp4" else Q.quantize_ref(w)
+        q.append(a)
+        s.append(b)
+    return np.stack(q).reshape(*shape[:-1], -1), np.stack(s).reshape(*shape[:-1], -1), gs
+
+
+def linear_bound(y, mag, K, b=None):
+    base = mag if b is None else mag + np.abs(b)
+    return 2 * (K / 128 + 48) * U * mag + 4 * U * base
+
+
+def assert_dense(y, x_bits, q, s, gs, b, out):
+    ref, mag = V.matvec_ref(x_bits, q, s, b, gs)
+    K = x_bits.shape[1]
+    err = np.abs(host(y) - ref)
+    bound = linear_bound(ref, mag, K, b) + (2.0 ** -8 if out == torch.bfloat16 else U) * np.abs(ref) + 2.0 ** -133
+    assert y.shape == ref.shape and np.all(err <= bound), float((err / bound).max())
+
+
+def dense(M, N, K, fmt, bias, out=torch.bfloat16, pad=0, seed=0):
+    print(f"matvec {fmt} M={M} N={N} K={K} bias={bias} out={out} pad={pad}", flush=True)
+    g = synth.rng(310, seed, M, N, K)
+    q, s, gs = weights(g, (N, K), fmt)
+    x = synth.to_bf16_bits(g.standard_normal((M, K), dtype=np.float32))
+    bt, b = None, None
+    if bias:
+        bt = torch.from_numpy(g.normal(0, 0.5, N).astype(np.float32)).cuda()
+        bt = bt.bfloat16() if bias == "bf16" else bt
+        b = host(bt)
+    buf = np.full((M, K + pad), 0x7FC0, np.uint16)  # NaN between the rows
+    buf[:, :K] = x
+    xd = bf16_dev(buf)[:, :K]
+    qd, sd = torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda()
+    y = mx.fp4_matvec(xd, qd, sd, bt, fmt=FMTS[fmt], global_scale=gs, out_dtype=out)
+    assert y.dtype == out
+    assert_dense(y, x, q, s, gs, b, out)
+    assert torch.equal(y, mx.fp4_matvec(xd, qd, sd, bt, fmt=FMTS[fmt], global_scale=gs, out_dtype=out))
+    return xd, qd, sd, gs, y
+
+
+# rows below, at and past a tile of 16; outputs that fill no tile; K of one block, below a step, ragged, long
+@pytest.mark.parametrize("fmt,M,N,K,bias", [
+    ("mxfp4", 1, 1, 32, None), ("mxfp4", 1, 16, 32, "bf16"), ("mxfp4", 2, 17, 96, "fp32"), ("mxfp4", 1, 256, 256, "bf16"),
+    ("mxfp4", 16, 33, 128, None), ("mxfp4", 17, 40, 160, "fp32"), ("mxfp4", 5, 64, 1056, None), ("mxfp4", 3, 48, 7168, None),
+    ("mxfp4", 33, 100, 2048, "bf16"), ("mxfp4", 70, 31, 544, None),
+    ("nvfp4", 1, 1, 16, None), ("nvfp4", 1, 5, 48, "fp32"), ("nvfp4", 4, 16, 112, None), ("nvfp4", 16, 65, 128, "bf16"),
+    ("nvfp4", 21, 99, 2032, "bf16"), ("nvfp4", 2, 48, 7168, None), ("nvfp4", 8, 50, 1040, "fp32"), ("nvfp4", 34, 20, 272, None)])
+def test_shapes(fmt, M, N, K, bias):
+    dense(M, N, K, fmt, bias)
+
+
+@pytest.mark.parametrize("fmt", list(FMTS))
+@pytest.mark.parametrize("M", [1, 2, 4, 5, 8, 9, 16, 32])
+def test_fp32_output_and_padded_rows(fmt, M):
+    dense(M, 70, 384, fmt, "fp32", torch.float32, pad=40, seed=1)
+
+
+@pytest.mark.parametrize("fmt", list(FMTS))
+def test_a_rows_result_does_not_depend_on_the_others(fmt):
+    xd, qd, sd, gs, y = dense(40, 130, 1088, fmt, None, torch.float32, seed=2)
+    for rows in (slice(0, 1), slice(3, 7), slice(15, 18), slice(20, 40)):
+        assert torch.equal(mx.fp4_matvec(xd[rows], qd, sd, fmt=FMTS[fmt], global_scale=gs, out_dtype=torch.float32), y[rows])
+    # not even where the others are not finite
+    bad = xd.clone()
+    bad[1] = float("nan")
+    bad[5] = float("inf")
+    z = mx.fp4_matvec(bad, qd, sd, fmt=FMTS[fmt], global_scale=gs, out_dtype=torch.float32)
+    keep = [i for i in range(40) if i not in (1, 5)]
+    assert torch.equal(z[keep], y[keep]) and not torch.isfinite(z[1]).any()
+
+
+def test_every_code_and_scale():
+    """Each E2M1 code under scales over the formats' normal ranges, one at a time against a unit vector: exact."""
+    K, N = 64, 120
+    g = synth.rng(311)
+    x = np.zeros((16, K), np.uint16)
+    x[np.arange(16), np.arange(0, 64, 4)] = 0x3F80
+    q = g.integers(0, 256, (N, K // 2), dtype=np.uint8)
+    s = g.integers(3, 252, (N, 2), dtype=np.uint8)  # 0.5 * 2^-124 .. 6 * 2^124
+    y = mx.fp4_matvec(bf16_dev(x), torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda(), out_dtype=torch.float32)
+    np.testing.assert_array_equal(host(y), V.matvec_ref(x, q, s)[0])
+    s = np.arange(N * 4, dtype=np.uint16).reshape(N, 4) % 127  # every finite, non-negative E4M3 value
+    s = s.astype(np.uint8)
+    y = mx.fp4_matvec(bf16_dev(x), torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda(), fmt=mx.FMT_NVFP4, global_scale=1.0,
+                      out_dtype=torch.float32)
+    np.testing.assert_array_equal(host(y), V.matvec_ref(x, q, s, None, 1.0)[0])
+
+
+def test_equals_the_linear_layer():
+    """Against mx.Linear on the same weights, within both layers' tolerances."""
+    g = synth.rng(312)
+    w = synth.to_bf16_bits(g.standard_normal((192, 256), dtype=np.float32) * np.float32(0.02))
+    q, s, _ = mx.quantize(bf16_dev(w), flat=True, tiled=False)
+    x = synth.to_bf16_bits(g.standard_normal((7, 256), dtype=np.float32))
+    a, b = host(mx.Linear(q, s)(bf16_dev(x))), host(mx.fp4_matvec(bf16_dev(x), q, s))
+    rms = np.sqrt(np.mean(b ** 2))
+    assert np.abs(a - b).max() <= 2e-2 * rms + 1e-3 + 2.0 ** -8 * np.abs(b).max()
+
+
+def pairs_of(ids, E):
+    flat = ids.reshape(-1)
+    order = np.argsort(flat, kind="stable")
+    offs = np.concatenate([[0], np.cumsum(np.bincount(flat, minlength=E))])
+    return torch.from_numpy(offs.astype(np.int32)).cuda(), torch.from_numpy(order.astype(np.int32)).cuda()
+
+
+def expert(T, E, k, N, K, fmt, swiglu, shared, bias, out=torch.bfloat16, seed=0, crowd=False):
+    print(f"expert {fmt} T={T} E={E} k={k} N={N} K={K} swiglu={swiglu} shared={shared} bias={bias}", flush=True)
+    g = synth.rng(313, seed, T, E, N)
+    q, s, gs = weights(g, (E, N, K), fmt)
+    gsv = None if gs is None else (gs * (0.5 + np.arange(E) / E)).astype(np.float32)
+    x = synth.to_bf16_bits(g.standard_normal((T if shared else T * k, K), dtype=np.float32))
+    ids = np.stack([g.permutation(E)[:k] for _ in range(T)])
+    if crowd:
+        ids[:] = ids[0]
+    b = g.normal(0, 0.1, (E, N)).astype(np.float32) if bias else None
+    offs, sp = pairs_of(ids, E)
+    args = (bf16_dev(x), torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda(), offs, sp,
+            None if b is None else torch.from_numpy(b).cuda())
+    kw = dict(fmt=FMTS[fmt], global_scales=None if gsv is None else torch.from_numpy(gsv).cuda(), top_k=k if shared else 1,
+              swiglu=swiglu, out_dtype=out)
+    y = mx.fp4_expert_matvec(*args, **kw)
+    h, mag = V.expert_matvec_ref(x, q, s, ids, shared, b, gsv)
+    tol = linear_bound(h, mag, K, None if b is None else b[ids.reshape(-1)])
+    ref = h
+    if swiglu:
+        ref = V.swiglu_ref(h)
+        gate, up = np.split(h, 2, 1)
+        tg, tu = np.split(tol, 2, 1)
+        silu = gate / (1 + np.exp(-gate))
+        tol = 1.1 * tg * (np.abs(up) + tu) + np.abs(silu) * tu + (np.abs(gate) + 8) * U * np.abs(ref)
+    tol = tol + (2.0 ** -8 if out == torch.bfloat16 else U) * np.abs(ref) + 2.0 ** -133
+    err = np.abs(host(y) - ref)
+    assert y.shape == ref.shape and y.dtype == out and np.all(err <= tol), float((err / tol).max())
+    assert torch.equal(y, mx.fp4_expert_matvec(*args, **kw))
+    return args, kw, y
+
+
+@pytest.mark.parametrize("fmt", list(FMTS))
+@pytest.mark.parametrize("T,E,k,N,K,swiglu,shared,bias", [
+    (1, 1, 1, 16, 32, False, True, False), (1, 8, 3, 34, 96, True, True, True), (5, 4, 2, 50, 160, False, False, True),
+    (16, 70, 4, 32, 64, True, True, False), (33, 5, 5, 30, 224, True, False, True), (3, 200, 8, 18, 544, False, True, False)])
+def test_experts(fmt, T, E, k, N, K, swiglu, shared, bias):
+    expert(T, E, k, N, K, fmt, swiglu, shared, bias)
+
+
+@pytest.mark.parametrize("fmt", list(FMTS))
+def test_more_pairs_than_a_tile_on_one_expert(fmt):
+    expert(37, 9, 2, 40, 128, fmt, True, True, True, torch.float32, 1, crowd=True)
+    expert(37, 9, 2, 40, 128, fmt, False, False, False, torch.float32, 1, crowd=True)
+
+
+def test_last_expert_of_many_and_half_filled_groups():
+    expert(2, 1024, 2, 16, 48, "nvfp4", False, True, True, torch.float32, 2)
+
+
+def test_pairs_that_are_not_listed_keep_their_rows():
+    args, kw, y = expert(6, 4, 2, 24, 64, "mxfp4", False, True, False, torch.float32, 3)
+    offs, sp = args[3].clone(), args[4].clone()
+    gone = sp[-1].item()
+    offs[-1] -= 1  # the last pair is dropped
+    if offs[-2] > offs[-1]:
+        offs[-2] = offs[-1]
+    out = torch.full_like(y, 7.0)
+    z = mx.fp4_expert_matvec(*args[:3], offs, sp, **{k: v for k, v in kw.items() if k != "out_dtype"}, y=out)
+    assert z is out
+    keep = [p for p in range(12) if p != gone]
+    assert torch.equal(z[keep], y[keep]) and bool((z[gone] == 7.0).all())
+
+
+def test_bad_offsets_and_pairs_stay_inside():
+    """Clamped or passed over: the kernel's own bounds, which the header states."""
+    args, kw, y = expert(6, 4, 2, 24, 64, "mxfp4", False, True, False, torch.float32, 3)
+    kw.pop("out_dtype")
+    offs, sp = args[3], args[4].clone()
+    sp[2], sp[5] = -1, 12
+    dropped = sorted({args[4][2].item(), args[4][5].item()})
+    keep = [p for p in range(12) if p not in dropped]
+    z = mx.fp4_expert_matvec(*args[:3], offs, sp, **kw, y=torch.full_like(y, 7.0))
+    assert torch.equal(z[keep], y[keep]) and bool((z[dropped] == 7.0).all())
+    wide = offs.clone()
+    wide[0], wide[-1] = -5, 1 << 30
+    assert torch.equal(mx.fp4_expert_matvec(*args[:3], wide, args[4], **kw, y=torch.full_like(y, 7.0)), y)
+    none = torch.zeros_like(offs)
+    assert bool((mx.fp4_expert_matvec(*args[:3], none, sp, **kw, y=torch.full_like(y, 7.0)) == 7.0).all())
+
+
+def test_no_rows():
+    q, s = torch.zeros(16, 32, dtype=torch.uint8, device="cuda"), torch.zeros(16, 2, dtype=torch.uint8, device="cuda")
+    assert mx.fp4_matvec(torch.zeros(0, 64, dtype=torch.bfloat16, device="cuda"), q, s).shape == (0, 16)
+    i = torch.zeros(2, dtype=torch.int32, device="cuda")
+    y = mx.fp4_expert_matvec(torch.zeros(0, 64, dtype=torch.bfloat16, device="cuda"), q[None], s[None], i, i[:0], top_k=4)
+    assert y.shape == (0, 16)
+
+
+def test_another_stream_and_a_graph():
+    xd, qd, sd, gs, y = dense(3, 200, 1024, "nvfp4", None, seed=5)
+    args, kw, ye = expert(4, 16, 2, 64, 256, "mxfp4", True, True, True, seed=5)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        a = mx.fp4_matvec(xd, qd, sd, fmt=mx.FMT_NVFP4, global_scale=gs)
+        b = mx.fp4_expert_matvec(*args, **kw)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(a, y) and torch.equal(b, ye)
+    graphs = []
+    for _ in range(2):  # two graphs share nothing but their inputs
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = (mx.fp4_matvec(xd, qd, sd, fmt=mx.FMT_NVFP4, global_scale=gs), mx.fp4_expert_matvec(*args, **kw))
+        graphs.append((graph, out))
+    x0, x1 = xd.clone(), -xd
+    for i in range(4):
+        xd.copy_(x1 if i % 2 else x0)
+        eager = mx.fp4_matvec(xd, qd, sd, fmt=mx.FMT_NVFP4, global_scale=gs)
+        for graph, out in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, out in graphs:
+            assert torch.equal(out[0], eager) and torch.equal(out[1], ye)
+
+
+def test_refusals():
+    z = lambda *s, d=torch.uint8: torch.zeros(*s, dtype=d, device="cuda")  # noqa: E731
+    bf = torch.bfloat16
+    x, q, s = z(2, 64, d=bf), z(16, 32), z(16, 2)
+    i2, p = z(2, d=torch.int32), z(2, d=torch.int32)
+    bad = [lambda: mx.fp4_matvec(x.half(), q, s), lambda: mx.fp4_matvec(x[:, :32], q, s),
+           lambda: mx.fp4_matvec(x, q, z(16, 4)), lambda: mx.fp4_matvec(x, q.cpu(), s),
+           lambda: mx.fp4_matvec(x, q, s, fmt=mx.FMT_MXFP8), lambda: mx.fp4_matvec(x, q, s, global_scale=1.0),
+           lambda: mx.fp4_matvec(x, q, z(16, 4), fmt=mx.FMT_NVFP4), lambda: mx.fp4_matvec(x, q, s, z(15, d=bf)),
+           lambda: mx.fp4_matvec(x, q, s, z(16, d=torch.half)), lambda: mx.fp4_matvec(x, q, s, out_dtype=torch.half),
+           lambda: mx.fp4_matvec(x[:1].expand(2, 64), q, s), lambda: mx.fp4_matvec(z(64, 2, d=bf).t(), q, s),
+           lambda: mx.fp4_matvec(x, z(16, 64)[:, :32], s),
+           lambda: mx.fp4_expert_matvec(x, q, s, i2, p), lambda: mx.fp4_expert_matvec(x, q[None], s[None], z(3, d=torch.int32), p),
+           lambda: mx.fp4_expert_matvec(x, q[None], s[None], i2, p, top_k=2),
+           lambda: mx.fp4_expert_matvec(x, q[None], s[None], i2.long(), p),
+           lambda: mx.fp4_expert_matvec(x, z(1, 15, 32), z(1, 15, 2), i2, p, swiglu=True),
+           lambda: mx.fp4_expert_matvec(x, q[None], s[None], i2, p, y=z(2, 15, d=bf)),
+           lambda: mx.fp4_expert_matvec(x, q[None], z(1, 16, 4), i2, p, fmt=mx.FMT_NVFP4)]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
+    with pytest.raises(mx.Mxfp4Error):  # rows 8-byte aligned
+        mx.fp4_matvec(z(2, 68, d=bf)[:, 4:], q, s)
+    with pytest.raises(mx.Mxfp4Error):
+        mx.fp4_matvec(x, q, z(16, 4), fmt=mx.FMT_NVFP4, global_scale=-1.0)
