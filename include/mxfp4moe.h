@@ -319,15 +319,15 @@ enum {
  * Matrix-vector products with 4-bit weights: y = x W^T (/ global_scale) + b for one or a few rows of x.
  * [DEF: the W4A16 linear layer, for NVFP4 weights too, in the form that decoding a token needs]
  * Weights in the standard layout, as the quantizers write them (no pack): w_q uint8 [N, K/2] (16-byte
- * aligned), w_s uint8 [N, K/32] E8M0 (MXFP4) or [N, K/16] E4M3 (NVFP4).  K is a multiple of the block
- * (32 or 16), 1 <= N, K <= 2^20.  global_scale host, positive and finite (NVFP4; MXFP4 ignores it).
+ * aligned), w_s uint8 [N, K/32] E8M0 (MXFP4) or [N, K/16] E4M3 (NVFP4), any alignment.  K is a multiple of the block
+ * (32 or 16), 32 <= K <= 2^20, 1 <= N <= 2^20.  global_scale host, positive and finite (NVFP4; MXFP4 ignores it).
  * bias [N] fp32 or bf16 or NULL.  x_bf16 device bf16 [M, ldx], ldx >= K, ldx % 8 == 0, 0 <= M <= 2^20.
  * y device [M, ldy], ldy >= N, bf16 or fp32 (out_is_fp32).
  * Arithmetic: a weight times its scale is exact in bf16 (at most six significant bits), the products
  * accumulate in fp32, the global scale divides and the bias is added in fp32, one rounding to bf16.
  * Weights of 2^128 and more, or of less than 2^-126, are outside the contract.
- * Deterministic, and a row's result does not depend on the other rows.  The weights are read once per 16 rows
- * of x: for many rows mxfp4_linear_forward is the faster layer. */
+ * Deterministic: repeated calls give the same bits (other numbers of rows may sum in another order).  The weights
+ * are read once per 16 rows of x: for many rows mxfp4_linear_forward is the faster layer. */
 int fp4_matvec(int32_t fmt, const void* w_q, const void* w_s, float global_scale, int64_t N, int64_t K,
                const void* bias, int32_t bias_is_fp32, const void* x_bf16, int64_t M, int64_t ldx, void* y,
                int64_t ldy, int32_t out_is_fp32, void* stream);

@@ -17,9 +17,12 @@ typedef unsigned u32x2_t __attribute__((ext_vector_type(2)));
 // rows of NVFP4 weights start on 8-byte boundaries
 typedef u32x4_t u32x4_a8 __attribute__((aligned(8)));
 
-constexpr int kWaves = 8;
-constexpr int kThreads = 64 * kWaves;
-constexpr int kStep = 128;  // K elements of one step: 32 for each quarter of the wave
+constexpr int kStep = 128;     // K elements of one step: 32 for each quarter of the wave
+constexpr int64_t kFull = 2048;  // waves that fill the chip
+template <int CTRL>
+MX_DEV float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
 
 // Eight weights (one dword of codes) as bf16, times their scale: exact.
 template <int FMT>
@@ -43,38 +46,22 @@ MX_DEV bf16x8_t dequant8(uint32_t codes, float scale) {
   return __builtin_bit_cast(bf16x8_t, out);
 }
 
-// What a lane holds of one row for one step: 32 codes and their scale bytes.
-struct Chunk {
-  u32x4_t q;
-  uint32_t s;
-};
-
-// k: first of the lane's 32 elements; K - k elements are there (K % 16 == 0).
+// The codes of the 32 elements from k on of a row of K elements.  Past the row's end it loads the row's last 32 again
+// (no branch, nothing out of bounds): x is zero there.  NVFP4 rows may end inside the 32 (K % 32 == 16): then
+// what is loaded starts 16 elements early, and settle() moves it.
 template <int FMT>
-MX_DEV Chunk load_chunk(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s, int64_t k, int64_t K) {
-  Chunk c = {u32x4_t{0, 0, 0, 0}, 0};
-  if (FMT == MXFP4_FMT_MXFP4) {
-    if (k < K) {
-      c.q = *reinterpret_cast<const u32x4_t*>(q + k / 2);
-      c.s = s[k / 32];
-    }
-  } else {
-    if (k + 32 <= K) {
-      c.q = *reinterpret_cast<const u32x4_a8*>(q + k / 2);
-      c.s = (uint32_t)s[k / 16] | ((uint32_t)s[k / 16 + 1] << 8);
-    } else if (k < K) {
-      const u32x2_t h = *reinterpret_cast<const u32x2_t*>(q + k / 2);
-      c.q = u32x4_t{h[0], h[1], 0, 0};
-      c.s = s[k / 16];
-    }
-  }
-  return c;
+MX_DEV u32x4_t load_codes(const uint8_t* q, int k, int K) {
+  const int at = min(k, K - 32);
+  if (FMT == MXFP4_FMT_MXFP4) return *reinterpret_cast<const u32x4_t*>(q + at / 2);
+  return *reinterpret_cast<const u32x4_a8*>(q + at / 2);
 }
 
 template <int FMT>
-MX_DEV float chunk_scale(uint32_t s, int half) {
-  if (FMT == MXFP4_FMT_MXFP4) return __uint_as_float(s << 23);  // the conversion reads the exponent field
-  return half ? __builtin_amdgcn_cvt_f32_fp8((int)s, 1) : __builtin_amdgcn_cvt_f32_fp8((int)s, 0);
+MX_DEV void settle(u32x4_t& q, int k, int K) {
+  if (FMT == MXFP4_FMT_MXFP4 || K % 32 == 0) return;
+  const bool early = k == K - 16;
+  q[0] = early ? q[2] : q[0];
+  q[1] = early ? q[3] : q[1];
 }
 
 MX_DEV float bias_at(const void* b, int fp32, int64_t i) {
@@ -87,132 +74,290 @@ MX_DEV uint16_t to_bf16(float f) {  // round to nearest even; infinities pass, N
   return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
 }
 
-// One workgroup: 16 rows of W (SWIGLU: 16 gate rows and the 16 up rows), up to 16 rows of x at a time, the
-// whole of K split over the waves, which join through LDS.
-template <int FMT, bool EXPERT, bool SWIGLU>
-__global__ __launch_bounds__(kThreads) void matvec_kernel(MatvecArgs a) {
-  constexpr int R = SWIGLU ? 2 : 1;
-  constexpr int B = FMT == MXFP4_FMT_NVFP4 ? 16 : 32;
-  __shared__ float part[kWaves][R][256];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int rc = lane & 15, quarter = lane >> 4;
+template <int FMT>
+constexpr int kBlock = FMT == MXFP4_FMT_NVFP4 ? 16 : 32;
+
+// The weights of 16 rows (the lane's is row rc): codes and scales, and where the scale tensor ends.
+struct Rows {
+  const uint8_t* q;        // codes of the lane's row of the first tile
+  const uint8_t* s0;       // scales: the tensor
+  int64_t s_at, s_bytes;   // the lane's row of the first tile in it; its length
+  int64_t q_tile, s_tile;  // bytes from tile to tile
+};
+
+// DW dwords from byte `at` on of a tensor of `bytes` bytes (at < bytes); bytes past its end read as zeros.  near_end:
+// they may reach past it (the same for the whole wave).
+template <int DW>
+MX_DEV void load_bytes(const uint8_t* t, int64_t at, int64_t bytes, bool near_end, uint32_t* v) {
+  typedef unsigned vec_t __attribute__((ext_vector_type(DW)));
+  typedef vec_t vec_a1 __attribute__((aligned(1)));
+  if (near_end && bytes < 4 * DW) {  // the whole tensor is shorter than a load
+#pragma unroll 1
+    for (int i = 0; i < DW; i++) {
+      uint32_t d = 0;
+#pragma unroll 1
+      for (int b = 0; b < 4; b++) d |= at + 4 * i + b < bytes ? (uint32_t)t[at + 4 * i + b] << (8 * b) : 0;
+#pragma unroll
+      for (int j = 0; j < DW; j++) v[j] = i == j ? d : v[j];
+    }
+    return;
+  }
+  const int64_t from = near_end ? min(at, bytes - 4 * DW) : at;
+  const vec_t w = *reinterpret_cast<const vec_a1*>(t + from);
+#pragma unroll
+  for (int i = 0; i < DW; i++) v[i] = w[i];
+  if (near_end) {
+    const int d = (int)(at - from);  // the bytes from d < 4 DW on move to the front
+#pragma unroll
+    for (int h = DW / 2; h > 0; h >>= 1)
+#pragma unroll
+      for (int i = 0; i < DW; i++) v[i] = d / (4 * h) % 2 ? (i + h < DW ? v[i + h] : 0) : v[i];
+#pragma unroll
+    for (int i = 0; i < DW; i++) v[i] = __builtin_amdgcn_alignbyte(i + 1 < DW ? v[i + 1] : 0, v[i], d & 3);
+  }
+}
+
+// Sums over the 16 rows of R tiles against XR rows of x, over this wave's blocks of K, to `part` [R][16 columns][16].
+//
+// A step is 128 elements of K: each quarter of the wave holds 32 of them, 16 bytes of codes a lane (a 64-byte piece of
+// 16 rows), which make four operands of the matrix instruction.  A block is SB steps that one load each of a row's
+// scales and one or a few loads of x serve (a byte of scales at a time beside the codes took a third of the
+// kernel's time); the next block's loads are on their way while a block is worked on.  x goes through a piece of LDS
+// of the wave's own (xs), which turns whole rows as they are loaded into the instruction's other operand.
+// That operand has 16 columns.  For XR <= 4 four columns belong to a row of x and hold different eighths of the
+// quarter's 32 elements, so that one 16-byte read serves all four operands of W.  Operand j's product is wanted in
+// the columns that hold the eighth j alone: each j has sums of its own, and a row's four columns are added up at
+// the end.  What the other columns sum up is dropped, also where it is not finite.
+template <int FMT, int R, int XR, int SB, typename RowX>
+MX_DEV void tile_sums(const Rows& w, int K, int wave, int waves, RowX row_of, uint16_t* xs, float* part) {
+  constexpr bool FEW = XR <= 4;
+  constexpr int kB = SB * kStep, DW = SB * (FMT == MXFP4_FMT_NVFP4 ? 2 : 1);
+  constexpr int PR = kB / 8, RPL = 64 / PR;              // 16-byte pieces of a row's block; rows of one load
+  constexpr int XL = XR > RPL ? XR / RPL : 1;            // loads of x
+  constexpr int kPitch = kB + 8;                         // 16 bytes more than the row: no two columns in a bank
+  const int lane = threadIdx.x & 63, rc = lane & 15, quarter = lane >> 4;
+  const int k_lane = quarter * 32, k_x = lane % PR * 8;
+  const uint16_t* x[XL];
+#pragma unroll
+  for (int l = 0; l < XL; l++) x[l] = row_of(l * RPL + lane / PR);
+  uint16_t* xput = xs + lane / PR * kPitch + k_x;
+  const uint16_t* xget = xs + (FEW ? (rc >> 2) % XR * kPitch + (rc & 3) * 8 : rc * kPitch) + k_lane;
+  struct Block {
+    u32x4_t q[R][SB], x[XL];
+    uint32_t s[R][DW];
+  };
+  auto load = [&](Block& b, int k0) {
+#pragma unroll
+    for (int l = 0; l < XL; l++) b.x[l] = *reinterpret_cast<const u32x4_t*>(x[l] + min(k0 + k_x, K - 8));
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+      const int64_t at = w.s_at + r * w.s_tile + k0 / kBlock<FMT>;
+      load_bytes<DW>(w.s0, at, w.s_bytes, k0 + kB > K, b.s[r]);
+#pragma unroll
+      for (int i = 0; i < SB; i++) b.q[r][i] = load_codes<FMT>(w.q + r * w.q_tile, k0 + i * kStep + k_lane, K);
+    }
+    __builtin_amdgcn_sched_barrier(0);  // the loads go out before the other block is worked on
+  };
+  f32x4_t acc[R][FEW ? 4 : 1] = {};
+  auto work = [&](Block& b, int k0) {
+#pragma unroll
+    for (int l = 0; l < XL; l++) {  // past K: zeros
+#pragma unroll
+      for (int i = 0; i < 4; i++) b.x[l][i] = k0 + k_x < K ? b.x[l][i] : 0;
+      if (XR >= RPL || lane / PR < XR) *reinterpret_cast<u32x4_t*>(xput + l * RPL * kPitch) = b.x[l];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < SB; i++) {
+      u32x4_t xv[FEW ? 1 : 4];
+#pragma unroll
+      for (int j = 0; j < (FEW ? 1 : 4); j++) xv[j] = *reinterpret_cast<const u32x4_t*>(xget + i * kStep + j * 8);
+#pragma unroll
+      for (int r = 0; r < R; r++) {
+        float s0, s1;
+        if (FMT == MXFP4_FMT_MXFP4) {  // the conversion reads the exponent field
+          s0 = s1 = __uint_as_float(__builtin_amdgcn_ubfe(b.s[r][i], 8 * quarter, 8) << 23);
+        } else {
+          const uint32_t two = (quarter & 2 ? b.s[r][2 * i + 1 < DW ? 2 * i + 1 : 0] : b.s[r][2 * i < DW ? 2 * i : 0]) >>
+                               (16 * (quarter & 1));
+          s0 = __builtin_amdgcn_cvt_f32_fp8((int)two, 0);
+          s1 = __builtin_amdgcn_cvt_f32_fp8((int)two, 1);
+        }
+        settle<FMT>(b.q[r][i], k0 + i * kStep + k_lane, K);
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+          acc[r][FEW ? j : 0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              dequant8<FMT>(b.q[r][i][j], j < 2 ? s0 : s1), __builtin_bit_cast(bf16x8_t, xv[FEW ? 0 : j]),
+              acc[r][FEW ? j : 0], 0, 0, 0);
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
+  const int stride = waves * kB;
+  int k0 = wave * kB;
+  for (; k0 < K; k0 += stride) {
+    Block b;
+    load(b, k0);
+    work(b, k0);
+  }
+  // lane: column rc, rows quarter * 4 + i of the tile
+#pragma unroll
+  for (int r = 0; r < R; r++) {
+    f32x4_t v = acc[r][0];
+    if (FEW) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+#pragma unroll
+        for (int f = 1; f < 4; f++) v[i] = (rc & 3) == f ? acc[r][FEW ? f : 0][i] : v[i];
+        v[i] += dpp<0xB1>(v[i]);  // lane ^ 1
+        v[i] += dpp<0x4E>(v[i]);  // lane ^ 2
+      }
+    }
+    const int col = FEW ? rc >> 2 : rc;
+    if (!FEW || (rc & 3) == 0) *reinterpret_cast<f32x4_t*>(part + r * 256 + col * 16 + quarter * 4) = v;
+  }
+}
+
+constexpr int kFew = 4;
+constexpr int kManySteps = 2;  // steps of a block for more rows: their x takes registers and LDS
+// LDS of a wave: its piece of x, then its sums.
+constexpr int wave_bytes(int R, int xr, int few_steps) {
+  const int few = (xr < kFew ? xr : kFew) * (few_steps * kStep + 8) * 2;
+  const int many = xr > kFew ? xr * (kManySteps * kStep + 8) * 2 : 0;
+  const int x = few > many ? few : many, sums = R * 1024;
+  return x > sums ? x : sums;
+}
+
+// One workgroup: a tile of 16 outputs (SWIGLU: 16 gate rows and the 16 up rows), its waves sharing the blocks of K,
+// against up to 16 rows of x at a time.  XR: the most rows there are (1, 4 or 16); SB: steps of a block for up to four.
+// R: tiles of 16 rows of W (SWIGLU: the gate's and the up projection's).
+template <int FMT, bool EXPERT, bool SWIGLU, int XR, int R, int SB>
+__global__ __launch_bounds__(1024, 4) void matvec_kernel(MatvecArgs a) {
+  constexpr int kWave = wave_bytes(R, XR, SB);
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
+  const int K = (int)a.K;
   const int64_t n_out = SWIGLU ? a.N / 2 : a.N;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int64_t n0 = (int64_t)blockIdx.x * (SWIGLU ? 16 : 16 * R);
   int64_t e = 0, first = 0, count = a.M;
   if (EXPERT) {
-    // the blockIdx.y-th expert that has pairs
-    int seen = 0;
-    e = -1;
-    for (int base = 0; base < a.E && e < 0; base += 64) {
-      const int i = base + lane;
-      const bool has = i < a.E && a.offsets[i + 1] > a.offsets[i];
-      uint64_t m = __ballot(has);
-      const int n = __popcll(m);
-      if (seen + n > (int)blockIdx.y) {
-        for (int s = seen; s < (int)blockIdx.y; s++) m &= m - 1;
-        e = base + __ffsll((unsigned long long)m) - 1;
+    e = blockIdx.y;
+    if (gridDim.y < (unsigned)a.E) {  // fewer pairs than experts: the blockIdx.y-th expert that has any
+      int seen = 0;
+      e = -1;
+      for (int base = 0; base < a.E && e < 0; base += 64) {
+        const int i = base + lane;
+        const bool has = i < a.E && a.offsets[i + 1] > a.offsets[i];
+        uint64_t m = __ballot(has);
+        const int n = __popcll(m);
+        if (seen + n > (int)blockIdx.y) {
+          for (int s = seen; s < (int)blockIdx.y; s++) m &= m - 1;
+          e = base + __ffsll((unsigned long long)m) - 1;
+        }
+        seen += n;
       }
-      seen += n;
+      if (e < 0) return;
     }
-    if (e < 0) return;
     const int64_t lo = a.offsets[e], hi = a.offsets[e + 1];
     first = lo < 0 ? 0 : lo;
     count = (hi > a.M ? a.M : hi) - first;
+    if (count <= 0) return;
   }
-  const int64_t KQ = a.K / 2, KS = a.K / B;
-  const uint8_t* wq = a.wq + e * a.N * KQ;
-  const uint8_t* ws = a.ws + e * a.N * KS;
-  const int64_t row = min(n0 + rc, n_out - 1);  // rows past the last repeat it and are not stored
   const float gs = EXPERT && FMT == MXFP4_FMT_NVFP4 ? a.gscales[e] : a.gscale;
-
+  const int KQ = K / 2, KS = K / kBlock<FMT>;
+  const int64_t row = e * a.N + min(n0 + (lane & 15), n_out - 1);  // past the last row: repeats it, not stored
+  const int64_t apart = SWIGLU ? n_out : R > 1 ? e * a.N + min(n0 + 16 + (lane & 15), n_out - 1) - row : 0;
+  const Rows w = {a.wq + row * KQ, a.ws, row * KS, (int64_t)a.E * a.N * KS, apart * KQ, apart * KS};
+  uint8_t* mine = smem + wave * kWave;
   const int64_t m_step = EXPERT ? 16 : (int64_t)gridDim.y * 16;
   for (int64_t m0 = EXPERT ? 0 : (int64_t)blockIdx.y * 16; m0 < count; m0 += m_step) {
-    // the row of x of this lane's column
-    int64_t m = m0 + rc;
-    bool have = m < count;
-    if (EXPERT && have) {
-      const int64_t p = a.pairs[first + m];
-      have = p >= 0 && p < a.M;
-      m = p / a.top_k;
-    }
-    const uint16_t* x = a.x + m * a.ldx;
-    f32x4_t acc[R] = {};
-    for (int64_t k0 = (int64_t)wave * kStep; k0 < a.K; k0 += kWaves * kStep) {
-      const int64_t k = k0 + quarter * 32;
-      Chunk c[R];
-#pragma unroll
-      for (int r = 0; r < R; r++)
-        c[r] = load_chunk<FMT>(wq + (row + r * n_out) * KQ, ws + (row + r * n_out) * KS, k, a.K);
-      u32x4_t xv[4];
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        xv[j] = u32x4_t{0, 0, 0, 0};
-        if (have && k + j * 8 < a.K) xv[j] = *reinterpret_cast<const u32x4_t*>(x + k + j * 8);
-      }
-#pragma unroll
-      for (int r = 0; r < R; r++)
-#pragma unroll
-        for (int j = 0; j < 4; j++)
-          acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dequant8<FMT>(c[r].q[j], chunk_scale<FMT>(c[r].s, j / 2)),
-                                                           __builtin_bit_cast(bf16x8_t, xv[j]), acc[r], 0, 0, 0);
-    }
-    // lane: column rc of x, rows quarter * 4 + i of W
-#pragma unroll
-    for (int r = 0; r < R; r++)
-#pragma unroll
-      for (int i = 0; i < 4; i++) part[wave][r][rc * 16 + quarter * 4 + i] = acc[r][i];
+    const int cols = (int)min((int64_t)16, count - m0);
+    auto pair_of = [&](int c) -> int64_t {  // column c's row of y, -1: none
+      if (!EXPERT) return m0 + c;
+      const int64_t p = a.pairs[first + m0 + c];
+      return p < a.M ? p : -1;
+    };
+    auto row_of = [&](int c) {
+      const int64_t p = pair_of(min(c, cols - 1));
+      return a.x + (p < 0 ? 0 : EXPERT ? (int64_t)((uint32_t)p / (uint32_t)a.top_k) : p) * a.ldx;
+    };
+    if (XR == 1 || (EXPERT && cols == 1))
+      tile_sums<FMT, R, 1, SB>(w, K, wave, waves, row_of, (uint16_t*)mine, (float*)mine);
+    else if (XR == 4 || cols <= kFew)
+      tile_sums<FMT, R, 4, SB>(w, K, wave, waves, row_of, (uint16_t*)mine, (float*)mine);
+    else
+      tile_sums<FMT, R, 16, kManySteps>(w, K, wave, waves, row_of, (uint16_t*)mine, (float*)mine);
     __syncthreads();
-    const int t = threadIdx.x;
-    if (t < 256) {
-      float v[R];
+    constexpr int kOuts = SWIGLU ? 1 : R;  // tiles of outputs
+    for (int o = tid; o < cols * 16 * kOuts; o += blockDim.x) {
+      const int at = o & 15, tile = (o >> 4) % kOuts, col = (o >> 4) / kOuts;
+      float v[SWIGLU ? 2 : 1];
 #pragma unroll
-      for (int r = 0; r < R; r++) {
+      for (int r = 0; r < (SWIGLU ? 2 : 1); r++) {
         v[r] = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; w++) v[r] += part[w][r][t];
+        for (int g = 0; g < waves; g++)
+          v[r] += reinterpret_cast<const float*>(smem + g * kWave)[(tile + r) * 256 + col * 16 + at];
       }
-      const int64_t n = n0 + (t & 15), mm = m0 + (t >> 4);
-      if (n < n_out && mm < count) {
-        int64_t out_row = mm;
-        bool store = true;
-        if (EXPERT) {
-          out_row = a.pairs[first + mm];
-          store = out_row >= 0 && out_row < a.M;
-        }
-        if (store) {
+      const int64_t n = n0 + tile * 16 + at, out_row = pair_of(col);
+      if (n < n_out && out_row >= 0) {
 #pragma unroll
-          for (int r = 0; r < R; r++) {
-            if (FMT == MXFP4_FMT_NVFP4) v[r] /= gs;
-            if (a.bias) v[r] += bias_at(a.bias, a.bias_fp32, e * a.N + n + r * n_out);
-          }
-          const float y = SWIGLU ? v[0] / (1.0f + __expf(-v[0])) * v[R - 1] : v[0];
-          if (a.out_fp32)
-            ((float*)a.y)[out_row * a.ldy + n] = y;
-          else
-            ((uint16_t*)a.y)[out_row * a.ldy + n] = to_bf16(y);
+        for (int r = 0; r < (SWIGLU ? 2 : 1); r++) {
+          if (FMT == MXFP4_FMT_NVFP4) v[r] /= gs;
+          if (a.bias) v[r] += bias_at(a.bias, a.bias_fp32, e * a.N + n + r * n_out);
         }
+        const float y = SWIGLU ? v[0] / (1.0f + __expf(-v[0])) * v[SWIGLU ? 1 : 0] : v[0];
+        if (a.out_fp32)
+          ((float*)a.y)[out_row * a.ldy + n] = y;
+        else
+          ((uint16_t*)a.y)[out_row * a.ldy + n] = to_bf16(y);
       }
     }
     __syncthreads();
   }
 }
 
+template <int FMT, bool EXPERT, bool SWIGLU, int XR, int SB>
+int launch_rows(const MatvecArgs& a, hipStream_t stream) {
+  constexpr int R = SWIGLU || XR > kFew ? 2 : 1, kRows = SWIGLU ? 16 : 16 * R;
+  const int64_t n_out = SWIGLU ? a.N / 2 : a.N;
+  const int64_t groups = EXPERT ? (a.M < a.E ? a.M : a.E) : (a.M + 15) / 16;
+  const int64_t tiles = (n_out + kRows - 1) / kRows;
+  const int kB = (XR > kFew ? kManySteps : SB) * kStep;
+  const int64_t blocks = (a.K + kB - 1) / kB;
+  // blocks of K a wave works through: as few as leave waves to fill the chip, and 16 waves a workgroup
+  int64_t each = tiles * groups * blocks / kFull;
+  each = each < 1 ? 1 : each;
+  const int64_t most = XR > kFew ? 8 : 16;
+  if ((blocks + each - 1) / each > most) each = (blocks + most - 1) / most;
+  const int waves = (int)((blocks + each - 1) / each);
+  const dim3 grid((unsigned)tiles, (unsigned)(groups < 65535 ? groups : 65535));
+  const int lds = waves * wave_bytes(R, XR, SB);
+  hipLaunchKernelGGL((matvec_kernel<FMT, EXPERT, SWIGLU, XR, R, SB>), grid, dim3(64 * waves), lds, stream, a);
+  return hipGetLastError() == hipSuccess ? MXFP4_OK : MXFP4_ERR_DEVICE;
+}
+
+template <int FMT, bool EXPERT, bool SWIGLU, int SB>
+int launch_steps(const MatvecArgs& a, hipStream_t stream) {
+  if (a.M == 1) return launch_rows<FMT, EXPERT, SWIGLU, 1, SB>(a, stream);
+  return a.M <= kFew ? launch_rows<FMT, EXPERT, SWIGLU, 4, SB>(a, stream)
+                     : launch_rows<FMT, EXPERT, SWIGLU, 16, SB>(a, stream);
+}
+
+template <int FMT, bool EXPERT, bool SWIGLU>
+int launch_waves(const MatvecArgs& a, hipStream_t stream) {
+  // blocks of four steps, or of two where those would be more than a fifth padding
+  const int64_t padded = (a.K + 4 * kStep - 1) / (4 * kStep) * (4 * kStep);
+  return padded * 4 > a.K * 5 ? launch_steps<FMT, EXPERT, SWIGLU, 2>(a, stream)
+                              : launch_steps<FMT, EXPERT, SWIGLU, 4>(a, stream);
+}
+
 template <int FMT>
 int launch_fmt(const MatvecArgs& a, hipStream_t stream) {
-  const int64_t n_out = a.swiglu ? a.N / 2 : a.N;
-  const unsigned gx = (unsigned)((n_out + 15) / 16);
-  if (a.offsets) {
-    const dim3 grid(gx, (unsigned)(a.M < a.E ? a.M : a.E));
-    if (a.swiglu)
-      hipLaunchKernelGGL((matvec_kernel<FMT, true, true>), grid, dim3(kThreads), 0, stream, a);
-    else
-      hipLaunchKernelGGL((matvec_kernel<FMT, true, false>), grid, dim3(kThreads), 0, stream, a);
-  } else {
-    const int64_t gy = (a.M + 15) / 16;
-    hipLaunchKernelGGL((matvec_kernel<FMT, false, false>), dim3(gx, (unsigned)(gy < 65535 ? gy : 65535)),
-                       dim3(kThreads), 0, stream, a);
-  }
-  return hipGetLastError() == hipSuccess ? MXFP4_OK : MXFP4_ERR_DEVICE;
+  if (!a.offsets) return launch_waves<FMT, false, false>(a, stream);
+  return a.swiglu ? launch_waves<FMT, true, true>(a, stream) : launch_waves<FMT, true, false>(a, stream);
 }
 
 }  // namespace

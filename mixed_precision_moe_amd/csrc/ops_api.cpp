@@ -49,7 +49,7 @@ int group_of(int32_t fmt) {
 
 int check_matvec(int32_t fmt, int64_t N, int64_t K) {
   if (fmt != MXFP4_FMT_MXFP4 && fmt != MXFP4_FMT_NVFP4) return MXFP4_ERR_LAYOUT;
-  if (N < 1 || N > kMaxWidth || K < group_of(fmt) || K > kMaxWidth || K % group_of(fmt)) return MXFP4_ERR_SHAPE;
+  if (N < 1 || N > kMaxWidth || K < 32 || K > kMaxWidth || K % group_of(fmt)) return MXFP4_ERR_SHAPE;
   return MXFP4_OK;
 }
 

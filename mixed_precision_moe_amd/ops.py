@@ -16,29 +16,40 @@ FMT_MXFP8 = 2  # E4M3, an E8M0 scale per 32 elements (the cache only)
 _GROUP = {FMT_MXFP4: 32, FMT_NVFP4: 16, FMT_MXFP8: 32}
 
 
+# The stream's handle without the object around it: about 2 us of a call that a small kernel does not hide.
+_stream_of = torch._C._cuda_getCurrentRawStream
+
+
 def _need(cond, msg):
     if not cond:
         raise ValueError(msg)
 
 
 def _ptr(t):
-    return t.data_ptr() if t is not None else None
+    return None if t is None else t.data_ptr()
 
 
 def _same_device(first, name, **others):
     """Every tensor on the GPU that holds `first`."""
-    _need(first.is_cuda, f"{name} must be a GPU tensor")
+    if not first.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    device = first.device
     for n, t in others.items():
-        _need(t is None or t.device == first.device, f"{n} must be on {name}'s device")
+        if t is not None and t.device != device:
+            raise ValueError(f"{n} must be on {name}'s device")
+    return device
 
 
 def _call(device, fn, *args):
     """fn(*args, stream) on the current stream of `device`, which need not be the current device."""
-    if device.index == torch.cuda.current_device():
-        check(fn, getattr(_lib.lib(), fn)(*args, torch.cuda.current_stream(device).cuda_stream))
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = getattr(_lib.lib(), fn)(*args, _stream_of(index))
     else:
         with torch.cuda.device(device):
-            check(fn, getattr(_lib.lib(), fn)(*args, torch.cuda.current_stream(device).cuda_stream))
+            status = getattr(_lib.lib(), fn)(*args, _stream_of(index))
+    if status:
+        check(fn, status)
 
 
 # ------------------------------------------------------------------------------------------------
@@ -56,28 +67,33 @@ class _BalanceLoss(torch.autograd.Function):
         T, E = logits.shape
         dev = logits.device
         nws = _lib.lib().moe_balance_workspace_bytes(T, E)
-        _need(nws > 0, "invalid balance loss arguments")
-        ws = torch.empty(nws, dtype=torch.uint8, device=dev)
+        if nws == 0:
+            raise ValueError("invalid balance loss arguments")
+        # d_e for the backward pass lies behind the workspace, whose size is a multiple of 256
+        buf = torch.empty(nws + 4 * E, dtype=torch.uint8, device=dev)
         loss = torch.empty((), dtype=torch.float32, device=dev)
-        coef = torch.empty(E, dtype=torch.float32, device=dev)
         counts = torch.empty(E, dtype=torch.int32, device=dev)
-        _call(dev, "moe_balance_forward", _ptr(logits), T, E, _row_step(logits), _ptr(topk_ids), topk_ids.shape[1],
-              _ptr(mask), _ptr(loss), _ptr(counts), _ptr(coef), _ptr(ws), nws)
-        ctx.save_for_backward(logits, coef, mask)
+        ws = buf.data_ptr()
+        step = _row_step(logits)
+        _call(dev, "moe_balance_forward", logits.data_ptr(), T, E, step, topk_ids.data_ptr(), topk_ids.shape[1], _ptr(mask),
+              loss.data_ptr(), counts.data_ptr(), ws + nws, ws, nws)
+        ctx.save_for_backward(logits, buf, mask)
+        ctx.coef, ctx.step = nws, step
         ctx.mark_non_differentiable(counts)
         ctx.set_materialize_grads(False)
         return loss, counts
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, g, _):
+        if torch.is_grad_enabled():
+            raise RuntimeError("balance_loss has no second derivative (create_graph)")
         if g is None:
             return None, None, None
-        logits, coef, mask = ctx.saved_tensors
+        logits, buf, mask = ctx.saved_tensors
         T, E = logits.shape
         grad = torch.empty((T, E), dtype=torch.float32, device=logits.device)
-        _call(logits.device, "moe_balance_backward", _ptr(logits), T, E, _row_step(logits), _ptr(mask), _ptr(coef),
-              _ptr(g), _ptr(grad))
+        _call(logits.device, "moe_balance_backward", logits.data_ptr(), T, E, ctx.step, _ptr(mask),
+              buf.data_ptr() + ctx.coef, g.data_ptr(), grad.data_ptr())
         return grad, None, None
 
 
@@ -106,30 +122,42 @@ def balance_loss(logits, topk_ids, token_mask=None):
 
 
 def _check_weights(w_q, w_s, fmt, dims):
-    _need(fmt in (FMT_MXFP4, FMT_NVFP4), "fmt must be FMT_MXFP4 or FMT_NVFP4")
-    for n, t in (("w_q", w_q), ("w_s", w_s)):
-        _need(t.dtype == torch.uint8 and t.is_contiguous() and t.dim() == dims, f"{n} must be contiguous uint8 {dims}-D")
-    K = 2 * w_q.shape[-1]
-    _need(K % _GROUP[fmt] == 0 and w_s.shape == (*w_q.shape[:-1], K // _GROUP[fmt]), "w_s shape")
-    return K
+    """The shape of the codes, with K in place of K/2."""
+    _need(fmt == FMT_MXFP4 or fmt == FMT_NVFP4, "fmt must be FMT_MXFP4 or FMT_NVFP4")
+    for t in (w_q, w_s):
+        if t.dtype != torch.uint8 or t.dim() != dims or not t.is_contiguous():
+            raise ValueError(f"w_q and w_s must be contiguous uint8 {dims}-D")
+    *rows, half = w_q.shape
+    group = _GROUP[fmt] // 2
+    _need(half % group == 0 and list(w_s.shape) == [*rows, half // group], "w_s shape")
+    return *rows, 2 * half
 
 
 def _check_bias(bias, shape):
-    if bias is not None:
-        _need(bias.dtype in (torch.float32, torch.bfloat16) and bias.shape == shape and bias.is_contiguous(),
-              f"bias: contiguous fp32 or bf16 {list(shape)}")
-    return 1 if bias is not None and bias.dtype == torch.float32 else 0
+    """Whether the bias is fp32."""
+    if bias is None:
+        return 0
+    _need((bias.dtype == torch.float32 or bias.dtype == torch.bfloat16) and bias.shape == shape and bias.is_contiguous(),
+          "bias: contiguous fp32 or bf16, one value for each row of the weights")
+    return 1 if bias.dtype == torch.float32 else 0
 
 
 def _check_out(out_dtype):
-    _need(out_dtype in (torch.bfloat16, torch.float32), "out_dtype must be bfloat16 or float32")
-    return 1 if out_dtype == torch.float32 else 0
+    if out_dtype == torch.bfloat16:
+        return 0
+    _need(out_dtype == torch.float32, "out_dtype must be bfloat16 or float32")
+    return 1
 
 
-def _row_stride(x, K):
-    _need(x.dtype == torch.bfloat16 and x.dim() == 2 and x.shape[1] == K and (x.stride(1) == 1 or K == 1), "x: bf16 rows [*, K]")
-    _need(x.shape[0] <= 1 or x.stride(0) >= K, "x's rows must not overlap")
-    return x.stride(0) if x.shape[0] > 1 else K + -K % 8
+def _check_rows(x, K):
+    """(rows, elements from row to row; the stride of a single row says nothing)."""
+    _need(x.dtype == torch.bfloat16 and x.dim() == 2 and x.shape[1] == K and x.stride(1) == 1, "x: bf16 rows [*, K]")
+    M = x.shape[0]
+    if M <= 1:
+        return M, K + -K % 8
+    ldx = x.stride(0)
+    _need(ldx >= K, "x's rows must not overlap")
+    return M, ldx
 
 
 def fp4_matvec(x, w_q, w_s, bias=None, *, fmt=FMT_MXFP4, global_scale=None, out_dtype=torch.bfloat16):
@@ -138,16 +166,15 @@ def fp4_matvec(x, w_q, w_s, bias=None, *, fmt=FMT_MXFP4, global_scale=None, out_
 
     x bf16 [M, K] (rows may be strided), w_q uint8 [N, K/2], w_s uint8 flat scales [N, K/32] or [N, K/16], bias fp32
     or bf16 [N] or None.  Returns y [M, N] in out_dtype (bfloat16 or float32)."""
-    _same_device(x, "x", w_q=w_q, w_s=w_s, bias=bias)
-    K = _check_weights(w_q, w_s, fmt, 2)
-    N, M = w_q.shape[0], x.shape[0]
-    ldx = _row_stride(x, K)
+    device = _same_device(x, "x", w_q=w_q, w_s=w_s, bias=bias)
+    N, K = _check_weights(w_q, w_s, fmt, 2)
+    M, ldx = _check_rows(x, K)
     _need((global_scale is not None) == (fmt == FMT_NVFP4), "global_scale goes with FMT_NVFP4, and only with it")
     is_fp32 = _check_bias(bias, (N,))
     out_fp32 = _check_out(out_dtype)
-    y = torch.empty((M, N), dtype=out_dtype, device=x.device)
-    _call(x.device, "fp4_matvec", fmt, _ptr(w_q), _ptr(w_s), 1.0 if global_scale is None else float(global_scale), N, K,
-          _ptr(bias), is_fp32, _ptr(x), M, ldx, _ptr(y), N, out_fp32)
+    y = torch.empty((M, N), dtype=out_dtype, device=device)
+    _call(device, "fp4_matvec", fmt, w_q.data_ptr(), w_s.data_ptr(), 1.0 if global_scale is None else global_scale, N, K,
+          _ptr(bias), is_fp32, x.data_ptr(), M, ldx, y.data_ptr(), N, out_fp32)
     return y
 
 
@@ -160,16 +187,16 @@ def fp4_expert_matvec(x, w_q, w_s, expert_offsets, sorted_pairs, bias=None, *, f
     or None, global_scales fp32 [E] (NVFP4).  expert_offsets int32 [E + 1] and sorted_pairs int32 [P] as `route`
     returns them.  Returns y [P, N], or [P, N/2] = silu(gate rows) * up rows with swiglu (rows [w1; w3]).  A pair
     that sorted_pairs does not list keeps what its row of `y` held."""
-    _same_device(x, "x", w_q=w_q, w_s=w_s, bias=bias, expert_offsets=expert_offsets, sorted_pairs=sorted_pairs,
-                 global_scales=global_scales, y=y)
-    K = _check_weights(w_q, w_s, fmt, 3)
-    E, N = w_q.shape[:2]
-    ldx = _row_stride(x, K)
-    for n, t in (("expert_offsets", expert_offsets), ("sorted_pairs", sorted_pairs)):
-        _need(t.dtype == torch.int32 and t.dim() == 1 and t.is_contiguous(), f"{n}: contiguous int32 1-D")
+    device = _same_device(x, "x", w_q=w_q, w_s=w_s, bias=bias, expert_offsets=expert_offsets, sorted_pairs=sorted_pairs,
+                          global_scales=global_scales, y=y)
+    E, N, K = _check_weights(w_q, w_s, fmt, 3)
+    M, ldx = _check_rows(x, K)
+    for t in (expert_offsets, sorted_pairs):
+        _need(t.dtype == torch.int32 and t.dim() == 1 and t.is_contiguous(),
+              "expert_offsets and sorted_pairs: contiguous int32 1-D")
     _need(expert_offsets.shape[0] == E + 1, "expert_offsets: E + 1 entries")
     P = sorted_pairs.shape[0]
-    _need(top_k >= 1 and x.shape[0] * top_k == P, "x must have one row for every top_k pairs")
+    _need(top_k >= 1 and M * top_k == P, "x must have one row for every top_k pairs")
     _need((global_scales is not None) == (fmt == FMT_NVFP4), "global_scales goes with FMT_NVFP4, and only with it")
     if global_scales is not None:
         _need(global_scales.dtype == torch.float32 and global_scales.shape == (E,) and global_scales.is_contiguous(),
@@ -179,12 +206,13 @@ def fp4_expert_matvec(x, w_q, w_s, expert_offsets, sorted_pairs, bias=None, *, f
     width = N // 2 if swiglu else N
     if y is None:
         out_fp32 = _check_out(out_dtype)
-        y = torch.empty((P, width), dtype=out_dtype, device=x.device)
+        y = torch.empty((P, width), dtype=out_dtype, device=device)
     else:
         out_fp32 = _check_out(y.dtype)
         _need(y.shape == (P, width) and y.is_contiguous(), "y: contiguous [P, N] (swiglu: [P, N/2])")
-    _call(x.device, "fp4_expert_matvec", fmt, _ptr(w_q), _ptr(w_s), _ptr(global_scales), E, N, K, _ptr(bias), is_fp32,
-          _ptr(x), ldx, top_k, _ptr(expert_offsets), _ptr(sorted_pairs), P, 1 if swiglu else 0, _ptr(y), out_fp32)
+    _call(device, "fp4_expert_matvec", fmt, w_q.data_ptr(), w_s.data_ptr(), _ptr(global_scales), E, N, K, _ptr(bias),
+          is_fp32, x.data_ptr(), ldx, top_k, expert_offsets.data_ptr(), sorted_pairs.data_ptr(), P, 1 if swiglu else 0,
+          y.data_ptr(), out_fp32)
     return y
 
 
@@ -220,6 +248,8 @@ class PagedCache:
         self.k_q, self.k_s, self.v_q, self.v_s = storage
         _same_device(self.k_q, "k_q", k_s=self.k_s, v_q=self.v_q, v_s=self.v_s)
         self._dref = ctypes.byref(self.dims)
+        self._memory = tuple(_ptr(t) for t in storage)
+        self._device = self.k_q.device
 
     def _index(self, page_table, cu_rows, start):
         _same_device(self.k_q, "the cache", page_table=page_table, cu_rows=cu_rows, start=start)
@@ -231,21 +261,24 @@ class PagedCache:
         if start is not None:
             _need(start.dtype == torch.int32 and start.shape == (B,) and start.is_contiguous(), "start: contiguous int32 [B]")
         _need(B <= 1 or page_table.stride(0) >= P, "page_table's rows must not overlap")
-        return _ptr(cu_rows), _ptr(start), _ptr(page_table), page_table.stride(0) if B > 1 else P, B, P
+        return cu_rows.data_ptr(), _ptr(start), page_table.data_ptr(), page_table.stride(0) if B > 1 else P, B, P
 
     def _rows(self, t, name, dim):
-        _need(t.dtype == torch.bfloat16 and t.dim() == 3 and t.shape[1:] == (self.dims.heads, dim) and t.stride(2) == 1,
-              f"{name}: bf16 [rows, {self.dims.heads}, {dim}], last dimension contiguous")
+        heads = self.dims.heads
+        if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.stride(2) != 1:
+            raise ValueError(f"{name}: bf16 [rows, {heads}, {dim}], last dimension contiguous")
         # the stride of a dimension of one entry says nothing
-        return (_ptr(t), t.stride(0) if t.shape[0] > 1 else self.dims.heads * dim + -self.dims.heads * dim % 8,
-                t.stride(1) if self.dims.heads > 1 else dim + -dim % 8)
+        return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * dim, t.stride(1) if heads > 1 else dim
 
     def _planes(self, k, v):
         d = self.dims
         _need((v is None) == (d.v_dim == 0), "v goes with v_dim > 0, and only with it")
         _same_device(self.k_q, "the cache", k=k, v=v)
-        _need(v is None or v.shape[0] == k.shape[0], "k and v must have the same number of rows")
-        return (*self._rows(k, "k", d.k_dim), *((None, 0, 0) if v is None else self._rows(v, "v", d.v_dim)))
+        k_args = self._rows(k, "k", d.k_dim)
+        if v is None:
+            return *k_args, None, 0, 0
+        _need(v.shape[0] == k.shape[0], "k and v must have the same number of rows")
+        return *k_args, *self._rows(v, "v", d.v_dim)
 
     def write(self, k, v, page_table, cu_rows, start=None):
         """Quantizes the rows of k [rows, heads, k_dim] and v (None with v_dim=0) into the cache.  Rows
@@ -255,8 +288,7 @@ class PagedCache:
         share a slot."""
         index = self._index(page_table, cu_rows, start)
         planes = self._planes(k, v)
-        _call(self.k_q.device, "mxfp4_cache_write", self._dref, *planes, k.shape[0], *index, _ptr(self.k_q),
-              _ptr(self.k_s), _ptr(self.v_q), _ptr(self.v_s))
+        _call(self._device, "mxfp4_cache_write", self._dref, *planes, k.shape[0], *index, *self._memory)
 
     def read(self, page_table, cu_rows, start=None, rows=None, k_out=None, v_out=None):
         """Reads rows back as bf16: (k [rows, heads, k_dim], v or None), rows and positions as in `write`.  Give
@@ -266,11 +298,10 @@ class PagedCache:
         d = self.dims
         if k_out is None:
             _need(rows is not None and rows >= 0 and v_out is None, "give rows, or the outputs")
-            k_out = torch.empty((rows, d.heads, d.k_dim), dtype=torch.bfloat16, device=self.k_q.device)
+            k_out = torch.empty((rows, d.heads, d.k_dim), dtype=torch.bfloat16, device=self._device)
             if d.v_dim:
-                v_out = torch.empty((rows, d.heads, d.v_dim), dtype=torch.bfloat16, device=self.k_q.device)
+                v_out = torch.empty((rows, d.heads, d.v_dim), dtype=torch.bfloat16, device=self._device)
         planes = self._planes(k_out, v_out)
         _need(rows is None or rows == k_out.shape[0], "rows must be the outputs' rows")
-        _call(self.k_q.device, "mxfp4_cache_read", self._dref, _ptr(self.k_q), _ptr(self.k_s), _ptr(self.v_q),
-              _ptr(self.v_s), k_out.shape[0], *index, *planes)
+        _call(self._device, "mxfp4_cache_read", self._dref, *self._memory, k_out.shape[0], *index, *planes)
         return k_out, v_out

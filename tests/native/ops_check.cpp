@@ -104,6 +104,7 @@ static void test_matvec() {
   CHECK(mv(7, p, p, 1, 16, 64, p, 1, 64, p, 16) == MXFP4_ERR_LAYOUT);
   CHECK(mv(0, p, p, 1, 16, 48, p, 1, 64, p, 16) == MXFP4_ERR_SHAPE);  // K % 32
   CHECK(mv(1, p, p, 1, 16, 40, p, 1, 64, p, 16) == MXFP4_ERR_SHAPE);  // K % 16
+  CHECK(mv(1, p, p, 1, 16, 16, p, 1, 64, p, 16) == MXFP4_ERR_SHAPE);  // K < 32
   CHECK(mv(0, p, p, 1, 0, 64, p, 1, 64, p, 16) == MXFP4_ERR_SHAPE);
   CHECK(mv(0, p, p, 1, 16, 0, p, 1, 64, p, 16) == MXFP4_ERR_SHAPE);
   CHECK(mv(0, p, p, 1, (1 << 20) + 1, 64, p, 1, 64, p, 1 << 21) == MXFP4_ERR_SHAPE);
