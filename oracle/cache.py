@@ -35,13 +35,16 @@ def encode_ref(x_bits, fmt, gs):
 
 
 def decode_ref(q, s, fmt, gs):
-    """The cached values as binary32 numbers, one rounding from bf16: the MX formats' are exact, NVFP4's are a
-    binary32 quotient."""
+    """The cached values as binary32 numbers, one rounding from bf16: the MX formats' are exact, NVFP4's are the
+    binary32 quotient scale / global scale times the code, rounded to binary32 again."""
     if fmt == "mxfp4":
         return Q.dequant_ref(q, s).astype(np.float32)
     if fmt == "mxfp8":
         return Q.mxfp8_dequant_ref(q, s).astype(np.float32)
-    return (Q.nvfp4_dequant_ref(q, s, 1.0).astype(np.float32) / np.float32(gs)).astype(np.float32)
+    f = (Q.E4M3_MAGNITUDES[s].astype(np.float32) / np.float32(gs)).astype(np.float32)
+    codes = Q.unpack_codes(q)
+    v = np.where(codes & 8, -1.0, 1.0) * Q.E2M1_MAGNITUDES[codes & 7]
+    return (v.astype(np.float32) * np.repeat(f, Q.NV_BLOCK, axis=-1)).astype(np.float32)
 
 
 def bf16_bits(v):

@@ -1,5 +1,5 @@
 """GPU parity of the block-quantized paged cache with the oracle: codes and scale bytes bit for bit, values read
-back bit for bit (the MX formats' values are exact in bf16; NVFP4's is a binary32 quotient, rounded once more)."""
+back bit for bit (the MX formats' values are exact in bf16; NVFP4's are binary32 numbers, rounded once more)."""
 
 import numpy as np
 import pytest
