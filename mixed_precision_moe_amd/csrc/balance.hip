@@ -17,13 +17,14 @@
 
 namespace {
 
-constexpr int kThreads = 256;  // of the first launch and the backward pass
+constexpr int kThreads = 1024;  // of the first launch and the backward pass
 constexpr int kWaves = kThreads / 64;
-constexpr int kJoin = 1024;  // threads of the second launch
-constexpr int kJoinCols = 32;
+constexpr int kJoin = 256;  // threads of the second launch
+constexpr int kJoinCols = 8;
 // The largest T * E that one workgroup takes by itself.
 constexpr int64_t kSingle = 8192;
-constexpr int kMaxBlocks = 512;
+constexpr int kMaxBlocks = 256;    // workgroups of the first launch
+constexpr int kMaxBackward = 512;  // and of the backward pass
 
 typedef float f4_t __attribute__((ext_vector_type(4)));
 
@@ -98,6 +99,26 @@ MX_DEV void load_row(const float* __restrict__ l, int E, int lr, float* v) {
   }
 }
 
+// Sums of a and b over the workgroup, to every thread; red: 2 * 16 values.
+MX_DEV void block_sums(double& a, double& b, double* red) {
+#pragma unroll
+  for (int h = 1; h < 64; h <<= 1) {
+    a += __shfl_xor(a, h);
+    b += __shfl_xor(b, h);
+  }
+  const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  if ((threadIdx.x & 63) == 0) {
+    red[wave] = a;
+    red[16 + wave] = b;
+  }
+  __syncthreads();
+  a = b = 0.0;
+  for (int w = 0; w < waves; w++) {
+    a += red[w];
+    b += red[16 + w];
+  }
+}
+
 // loss and coef from the joined sums; one workgroup, all threads.  n and S may be global or LDS.
 MX_DEV void finish(int E, int k, const int32_t* n, const double* S, int64_t V, float* loss, float* coef, double* red) {
   const int t = threadIdx.x, nt = blockDim.x;
@@ -106,32 +127,28 @@ MX_DEV void finish(int E, int k, const int32_t* n, const double* S, int64_t V, f
     dot += (double)n[e] * S[e];
     pairs += (double)n[e];
   }
-  red[t] = dot;
-  red[nt + t] = pairs;
-  __syncthreads();
-  for (int h = nt / 2; h > 0; h >>= 1) {
-    if (t < h) {
-      red[t] += red[t + h];
-      red[nt + t] += red[nt + t + h];
-    }
-    __syncthreads();
-  }
+  block_sums(dot, pairs, red);
   const double each = V > 0 ? (double)E / ((double)k * (double)V * (double)V) : 0.0;
-  const double mean = red[nt] / (double)E;
-  if (t == 0) *loss = (float)(each * red[0]);
+  const double mean = pairs / (double)E;
+  if (t == 0) *loss = (float)(each * dot);
   for (int e = t; e < E; e += nt) coef[e] = (float)(each * ((double)n[e] - mean));
 }
 
+// What a workgroup found about a column: the sum of its probabilities, its pairs.
+struct Part {
+  float p;
+  int32_t n;
+};
+
 template <int LPR, int VPL, int VEC>
-__global__ __launch_bounds__(kThreads) void balance_forward_kernel(BalanceArgs a, float* __restrict__ part_p,
-                                                                   int32_t* __restrict__ part_n,
+__global__ __launch_bounds__(kThreads) void balance_forward_kernel(BalanceArgs a, Part* __restrict__ parts,
                                                                    int32_t* __restrict__ part_v, uint32_t* ticket) {
   constexpr int RPW = 64 / LPR;
   constexpr int GROUPS = kWaves * RPW;  // rows in flight in the workgroup
   constexpr int COLS = LPR * VPL;
-  __shared__ float cols[GROUPS * COLS];  // 16 bytes * kThreads * VPL / 4: 16 KB at VPL = 16
+  __shared__ float cols[kWaves * COLS];
   __shared__ int32_t hist[COLS];
-  __shared__ int32_t live_in[GROUPS];
+  __shared__ int32_t live_in[kWaves];
   const int t = threadIdx.x, E = a.E;
   const int lr = t & (LPR - 1), group = t / LPR;
   for (int e = t; e < E; e += kThreads) hist[e] = 0;
@@ -150,97 +167,129 @@ __global__ __launch_bounds__(kThreads) void balance_forward_kernel(BalanceArgs a
 #pragma unroll
   for (int i = 0; i < VPL; i++) acc[i] = 0.0f;
   int32_t live = 0;
-  for (int64_t r = (int64_t)blockIdx.x * GROUPS + group; r < a.T; r += (int64_t)gridDim.x * GROUPS) {
-    if (a.mask && !a.mask[r]) continue;  // uniform over the row's lanes, which exchange among themselves alone
-    float v[VPL];
-    load_row<LPR, VPL, VEC>(a.logits + r * a.ldl, E, lr, v);
-    softmax_row<LPR, VPL>(v);
+  // two rows at a time: the loads of both are on their way before either is worked on
+  const int64_t stride = (int64_t)gridDim.x * GROUPS;
+  for (int64_t r = (int64_t)blockIdx.x * GROUPS + group; r < a.T; r += 2 * stride) {
+    // uniform over a row's lanes, which exchange among themselves alone
+    const bool second = r + stride < a.T;
+    const bool live0 = !a.mask || a.mask[r], live1 = second && (!a.mask || a.mask[r + stride]);
+    float v[2][VPL];
+    if (live0) load_row<LPR, VPL, VEC>(a.logits + r * a.ldl, E, lr, v[0]);
+    if (live1) load_row<LPR, VPL, VEC>(a.logits + (r + stride) * a.ldl, E, lr, v[1]);
+    if (live0) {
+      softmax_row<LPR, VPL>(v[0]);
 #pragma unroll
-    for (int i = 0; i < VPL; i++) acc[i] += v[i];
-    live++;
+      for (int i = 0; i < VPL; i++) acc[i] += v[0][i];
+      live++;
+    }
+    if (live1) {
+      softmax_row<LPR, VPL>(v[1]);
+#pragma unroll
+      for (int i = 0; i < VPL; i++) acc[i] += v[1][i];
+      live++;
+    }
   }
+  // the wave's rows first, by their lanes, then the waves in LDS
+  const int wave = t >> 6;
 #pragma unroll
-  for (int i = 0; i < VPL; i++) cols[group * COLS + column<LPR, VPL, VEC>(lr, i)] = acc[i];
-  if (lr == 0) live_in[group] = live;
+  for (int h = LPR; h < 64; h <<= 1) {
+#pragma unroll
+    for (int i = 0; i < VPL; i++) acc[i] += __shfl_xor(acc[i], h);
+    live += __shfl_xor(live, h);
+  }
+  if ((t & 63) < LPR) {
+#pragma unroll
+    for (int i = 0; i < VPL; i++) cols[wave * COLS + column<LPR, VPL, VEC>(lr, i)] = acc[i];
+  }
+  if ((t & 63) == 0) live_in[wave] = live;
   __syncthreads();
 
   if (gridDim.x > 1) {
     for (int e = t; e < E; e += kThreads) {
       float s = 0.0f;
-      for (int g = 0; g < GROUPS; g++) s += cols[g * COLS + e];
-      part_p[(int64_t)blockIdx.x * E + e] = s;
-      part_n[(int64_t)blockIdx.x * E + e] = hist[e];
+      for (int w = 0; w < kWaves; w++) s += cols[w * COLS + e];
+      parts[(int64_t)blockIdx.x * E + e] = Part{s, hist[e]};
     }
     if (t == 0) {
       int32_t v = 0;
-      for (int g = 0; g < GROUPS; g++) v += live_in[g];
+      for (int w = 0; w < kWaves; w++) v += live_in[w];
       part_v[blockIdx.x] = v;
       if (blockIdx.x == 0) *ticket = 0;  // for the second launch
     }
     return;
   }
   __shared__ double sums[COLS];
-  __shared__ double red[2 * kThreads];
+  __shared__ double red[32];
   for (int e = t; e < E; e += kThreads) {
     double s = 0.0;
-    for (int g = 0; g < GROUPS; g++) s += (double)cols[g * COLS + e];
+    for (int w = 0; w < kWaves; w++) s += (double)cols[w * COLS + e];
     sums[e] = s;
     a.counts[e] = hist[e];
   }
   int64_t V = 0;
-  for (int g = 0; g < GROUPS; g++) V += live_in[g];
+  for (int w = 0; w < kWaves; w++) V += live_in[w];
   __syncthreads();
   finish(E, a.k, hist, sums, V, a.loss, a.coef, red);
 }
 
-// Joins the partial sums of `blocks` workgroups: kJoinCols columns a workgroup, 32 threads a column.
+// Joins the partial sums of `blocks` <= kMaxBlocks workgroups: kJoinCols columns a workgroup, the blocks spread over
+// its waves' halves.  The last workgroup to finish has the loss.
 __global__ __launch_bounds__(kJoin) void balance_join_kernel(BalanceArgs a, int32_t blocks,
-                                                             const float* __restrict__ part_p,
-                                                             const int32_t* __restrict__ part_n,
+                                                             const Part* __restrict__ parts,
                                                              const int32_t* __restrict__ part_v, double* sums,
                                                              uint32_t* ticket) {
-  constexpr int SPLIT = kJoin / kJoinCols;
-  __shared__ double red[2 * kJoin];
-  __shared__ int32_t redn[kJoin];
+  constexpr int SPLIT = kJoin / kJoinCols, LOADS = kMaxBlocks / SPLIT;
+  __shared__ double reds[kJoin / 64][kJoinCols];
+  __shared__ int32_t redn[kJoin / 64][kJoinCols];
+  __shared__ double red[32];
   __shared__ bool last;
   const int t = threadIdx.x, E = a.E;
   const int c = t % kJoinCols, part = t / kJoinCols, e = blockIdx.x * kJoinCols + c;
+  Part p[LOADS];
+#pragma unroll
+  for (int i = 0; i < LOADS; i++) {
+    const int b = part + i * SPLIT;
+    p[i] = Part{0.0f, 0};
+    if (b < blocks && e < E) p[i] = parts[(int64_t)b * E + e];
+  }
   double s = 0.0;
   int32_t n = 0;
-  if (e < E) {
-#pragma unroll 4
-    for (int b = part; b < blocks; b += SPLIT) {
-      s += (double)part_p[(int64_t)b * E + e];
-      n += part_n[(int64_t)b * E + e];
-    }
+#pragma unroll
+  for (int i = 0; i < LOADS; i++) {
+    s += (double)p[i].p;
+    n += p[i].n;
   }
-  red[t] = s;
-  redn[t] = n;
-  __syncthreads();
-  if (t < kJoinCols && e < E) {
-    for (int q = 1; q < SPLIT; q++) {
-      s += red[q * kJoinCols + c];
-      n += redn[q * kJoinCols + c];
-    }
-    sums[e] = s;
-    a.counts[e] = n;
+#pragma unroll
+  for (int h = kJoinCols; h < 64; h <<= 1) {
+    s += __shfl_xor(s, h);
+    n += __shfl_xor(n, h);
   }
-  __threadfence();
+  if ((t & 63) < kJoinCols) {
+    reds[t >> 6][c] = s;
+    redn[t >> 6][c] = n;
+  }
   __syncthreads();
-  if (t == 0) last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+  if (t < 64) {  // the first wave: it publishes the columns and takes a number
+    if (t < kJoinCols && e < E) {
+      for (int w = 1; w < kJoin / 64; w++) {
+        s += reds[w][c];
+        n += redn[w][c];
+      }
+      sums[e] = s;
+      a.counts[e] = n;
+    }
+    __threadfence();
+    if (t == 0)
+      last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+  }
   __syncthreads();
   if (!last) return;
   __threadfence();
-  // the tokens that count: every thread a few workgroups' numbers, then a tree
-  int32_t v = 0;
-  for (int b = t; b < blocks; b += kJoin) v += part_v[b];
-  redn[t] = v;
+  double v = 0.0, none = 0.0;  // the tokens that count
+  for (int b = t; b < blocks; b += kJoin) v += (double)part_v[b];
+  block_sums(v, none, red);
   __syncthreads();
-  for (int h = kJoin / 2; h > 0; h >>= 1) {
-    if (t < h) redn[t] += redn[t + h];
-    __syncthreads();
-  }
-  finish(E, a.k, a.counts, sums, redn[0], a.loss, a.coef, red);
+  finish(E, a.k, a.counts, sums, (int64_t)v, a.loss, a.coef, red);
 }
 
 template <int LPR, int VPL, int VEC>
@@ -329,22 +378,22 @@ int32_t balance_blocks(int64_t T, int32_t E) {
 }
 
 int launch_balance_forward(const BalanceArgs& a, const BalanceWs& w, uint8_t* ws, hipStream_t stream) {
-  float* pp = (float*)(ws + w.part_p);
-  int32_t *pn = (int32_t*)(ws + w.part_n), *pv = (int32_t*)(ws + w.part_v);
+  Part* parts = (Part*)(ws + w.parts);
+  int32_t* pv = (int32_t*)(ws + w.part_v);
   uint32_t* ticket = (uint32_t*)(ws + w.ticket);
   const int st = with_shape(a.E, [&](auto r) {
     using R = decltype(r);
     if (vec4(a.logits, a.ldl, a.E))
-      hipLaunchKernelGGL((balance_forward_kernel<R::LPR, R::VPL, 4>), dim3(w.blocks), dim3(kThreads), 0, stream, a, pp,
-                         pn, pv, ticket);
+      hipLaunchKernelGGL((balance_forward_kernel<R::LPR, R::VPL, 4>), dim3(w.blocks), dim3(kThreads), 0, stream, a, parts,
+                         pv, ticket);
     else
-      hipLaunchKernelGGL((balance_forward_kernel<R::LPR, R::VPL, 1>), dim3(w.blocks), dim3(kThreads), 0, stream, a, pp,
-                         pn, pv, ticket);
+      hipLaunchKernelGGL((balance_forward_kernel<R::LPR, R::VPL, 1>), dim3(w.blocks), dim3(kThreads), 0, stream, a, parts,
+                         pv, ticket);
     return status();
   });
   if (st || w.blocks == 1) return st;
   hipLaunchKernelGGL(balance_join_kernel, dim3((a.E + kJoinCols - 1) / kJoinCols), dim3(kJoin), 0, stream, a, w.blocks,
-                     pp, pn, pv, (double*)(ws + w.sums), ticket);
+                     parts, pv, (double*)(ws + w.sums), ticket);
   return status();
 }
 
@@ -353,7 +402,7 @@ int launch_balance_backward(const float* logits, int64_t T, int32_t E, int64_t l
   return with_shape(E, [&](auto r) {
     using R = decltype(r);
     const int64_t n = (T + rows_in_flight<R>() - 1) / rows_in_flight<R>();
-    const dim3 grid((unsigned)(n < 2048 ? n : 2048));
+    const dim3 grid((unsigned)(n < kMaxBackward ? n : kMaxBackward));
     if (vec4(logits, ldl, E) && vec4(grad, E, E))
       hipLaunchKernelGGL((balance_backward_kernel<R::LPR, R::VPL, 4>), grid, dim3(kThreads), 0, stream, logits, T, E,
                          ldl, mask, coef, grad_loss, grad);

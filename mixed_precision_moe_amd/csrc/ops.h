@@ -12,7 +12,7 @@
 // Balance loss (balance.hip).  Workspace: per-workgroup partial column sums and counts, the joined
 // column sums and a ticket.
 struct BalanceWs {
-  uint64_t part_p, part_n, part_v, sums, ticket, total;
+  uint64_t parts, part_v, sums, ticket, total;
   int32_t blocks;  // workgroups of the first launch
 };
 // Workgroups of the forward pass over T tokens and E experts; 1: it finishes by itself.

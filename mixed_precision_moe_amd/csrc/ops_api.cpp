@@ -34,8 +34,7 @@ BalanceWs balance_ws(int64_t T, int32_t E) {
   uint64_t p = 0;
   auto take = [&](uint64_t bytes) { uint64_t o = p; p = up256(p + bytes); return o; };
   const uint64_t cells = (uint64_t)w.blocks * (uint64_t)E;
-  w.part_p = take(4 * cells);
-  w.part_n = take(4 * cells);
+  w.parts = take(8 * cells);
   w.part_v = take(4 * (uint64_t)w.blocks);
   w.sums = take(8 * (uint64_t)E);
   w.ticket = take(4);

@@ -77,8 +77,7 @@ static void test_balance() {
   CHECK(g_launches == 0);
   CHECK(fw(f, 100, 64, 70, i, 2, f, fake(), n) == MXFP4_OK && g_launches == 1);
   // the workspace's parts follow each other inside it
-  CHECK(g_bws.part_p + 4 * (uint64_t)g_bws.blocks * 64 <= g_bws.part_n);
-  CHECK(g_bws.part_n + 4 * (uint64_t)g_bws.blocks * 64 <= g_bws.part_v);
+  CHECK(g_bws.parts + 8 * (uint64_t)g_bws.blocks * 64 <= g_bws.part_v);
   CHECK(g_bws.part_v + 4 * (uint64_t)g_bws.blocks <= g_bws.sums && g_bws.sums + 8 * 64 <= g_bws.ticket);
   CHECK(g_bws.ticket + 4 <= g_bws.total && g_bws.total == n && g_bws.sums % 8 == 0);
   // no tokens: loss and counts are still written
