@@ -29,24 +29,26 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _same_device(first, name, **others):
-    """Every tensor on the GPU that holds `first`."""
-    if not first.is_cuda:
+def _gpu_of(name, first, *others):
+    """The number of the GPU that holds `first` (called `name`) and every other tensor."""
+    index = first.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be a GPU tensor")
-    device = first.device
-    for n, t in others.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{n} must be on {name}'s device")
-    return device
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"every tensor must be on {name}'s device")
+    return index
 
 
-def _call(device, fn, *args):
-    """fn(*args, stream) on the current stream of `device`, which need not be the current device."""
-    index = device.index
-    if index == torch.cuda.current_device():
+_current_gpu = torch.cuda.current_device
+
+
+def _call(index, fn, *args):
+    """fn(*args, stream) on the current stream of GPU `index`, which need not be the current device."""
+    if index == _current_gpu():
         status = getattr(_lib.lib(), fn)(*args, _stream_of(index))
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             status = getattr(_lib.lib(), fn)(*args, _stream_of(index))
     if status:
         check(fn, status)
@@ -65,7 +67,7 @@ class _BalanceLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, topk_ids, mask):
         T, E = logits.shape
-        dev = logits.device
+        dev, index = logits.device, logits.get_device()
         nws = _lib.lib().moe_balance_workspace_bytes(T, E)
         if nws == 0:
             raise ValueError("invalid balance loss arguments")
@@ -75,7 +77,7 @@ class _BalanceLoss(torch.autograd.Function):
         counts = torch.empty(E, dtype=torch.int32, device=dev)
         ws = buf.data_ptr()
         step = _row_step(logits)
-        _call(dev, "moe_balance_forward", logits.data_ptr(), T, E, step, topk_ids.data_ptr(), topk_ids.shape[1], _ptr(mask),
+        _call(index, "moe_balance_forward", logits.data_ptr(), T, E, step, topk_ids.data_ptr(), topk_ids.shape[1], _ptr(mask),
               loss.data_ptr(), counts.data_ptr(), ws + nws, ws, nws)
         ctx.save_for_backward(logits, buf, mask)
         ctx.coef, ctx.step = nws, step
@@ -92,7 +94,7 @@ class _BalanceLoss(torch.autograd.Function):
         logits, buf, mask = ctx.saved_tensors
         T, E = logits.shape
         grad = torch.empty((T, E), dtype=torch.float32, device=logits.device)
-        _call(logits.device, "moe_balance_backward", logits.data_ptr(), T, E, ctx.step, _ptr(mask),
+        _call(logits.get_device(), "moe_balance_backward", logits.data_ptr(), T, E, ctx.step, _ptr(mask),
               buf.data_ptr() + ctx.coef, g.data_ptr(), grad.data_ptr())
         return grad, None, None
 
@@ -104,7 +106,7 @@ def balance_loss(logits, topk_ids, token_mask=None):
     [0, E) is a dropped pair), token_mask bool or uint8 [T] or None: tokens that count.  Returns (loss, counts):
     loss fp32, 0-dim, differentiable in the logits: E / (k V^2) * sum_e counts_e * sum_t softmax(logits_t)_e
     over the V tokens that count (0 without any); counts int32 [E], constants of the gradient."""
-    _same_device(logits, "logits", topk_ids=topk_ids, token_mask=token_mask)
+    _gpu_of("logits", logits, topk_ids, token_mask)
     _need(logits.dtype == torch.float32 and logits.dim() == 2, "logits: fp32 [T, E]")
     _need(logits.stride(1) == 1 or logits.shape[1] == 1, "logits' last dimension must be contiguous")
     T, E = logits.shape
@@ -166,14 +168,14 @@ def fp4_matvec(x, w_q, w_s, bias=None, *, fmt=FMT_MXFP4, global_scale=None, out_
 
     x bf16 [M, K] (rows may be strided), w_q uint8 [N, K/2], w_s uint8 flat scales [N, K/32] or [N, K/16], bias fp32
     or bf16 [N] or None.  Returns y [M, N] in out_dtype (bfloat16 or float32)."""
-    device = _same_device(x, "x", w_q=w_q, w_s=w_s, bias=bias)
+    gpu = _gpu_of("x", x, w_q, w_s, bias)
     N, K = _check_weights(w_q, w_s, fmt, 2)
     M, ldx = _check_rows(x, K)
     _need((global_scale is not None) == (fmt == FMT_NVFP4), "global_scale goes with FMT_NVFP4, and only with it")
     is_fp32 = _check_bias(bias, (N,))
     out_fp32 = _check_out(out_dtype)
-    y = torch.empty((M, N), dtype=out_dtype, device=device)
-    _call(device, "fp4_matvec", fmt, w_q.data_ptr(), w_s.data_ptr(), 1.0 if global_scale is None else global_scale, N, K,
+    y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+    _call(gpu, "fp4_matvec", fmt, w_q.data_ptr(), w_s.data_ptr(), 1.0 if global_scale is None else global_scale, N, K,
           _ptr(bias), is_fp32, x.data_ptr(), M, ldx, y.data_ptr(), N, out_fp32)
     return y
 
@@ -187,8 +189,7 @@ def fp4_expert_matvec(x, w_q, w_s, expert_offsets, sorted_pairs, bias=None, *, f
     or None, global_scales fp32 [E] (NVFP4).  expert_offsets int32 [E + 1] and sorted_pairs int32 [P] as `route`
     returns them.  Returns y [P, N], or [P, N/2] = silu(gate rows) * up rows with swiglu (rows [w1; w3]).  A pair
     that sorted_pairs does not list keeps what its row of `y` held."""
-    device = _same_device(x, "x", w_q=w_q, w_s=w_s, bias=bias, expert_offsets=expert_offsets, sorted_pairs=sorted_pairs,
-                          global_scales=global_scales, y=y)
+    gpu = _gpu_of("x", x, w_q, w_s, bias, expert_offsets, sorted_pairs, global_scales, y)
     E, N, K = _check_weights(w_q, w_s, fmt, 3)
     M, ldx = _check_rows(x, K)
     for t in (expert_offsets, sorted_pairs):
@@ -206,11 +207,11 @@ def fp4_expert_matvec(x, w_q, w_s, expert_offsets, sorted_pairs, bias=None, *, f
     width = N // 2 if swiglu else N
     if y is None:
         out_fp32 = _check_out(out_dtype)
-        y = torch.empty((P, width), dtype=out_dtype, device=device)
+        y = torch.empty((P, width), dtype=out_dtype, device=x.device)
     else:
         out_fp32 = _check_out(y.dtype)
         _need(y.shape == (P, width) and y.is_contiguous(), "y: contiguous [P, N] (swiglu: [P, N/2])")
-    _call(device, "fp4_expert_matvec", fmt, w_q.data_ptr(), w_s.data_ptr(), _ptr(global_scales), E, N, K, _ptr(bias),
+    _call(gpu, "fp4_expert_matvec", fmt, w_q.data_ptr(), w_s.data_ptr(), _ptr(global_scales), E, N, K, _ptr(bias),
           is_fp32, x.data_ptr(), ldx, top_k, expert_offsets.data_ptr(), sorted_pairs.data_ptr(), P, 1 if swiglu else 0,
           y.data_ptr(), out_fp32)
     return y
@@ -246,39 +247,39 @@ class PagedCache:
             _need(t is not None and t.dtype == torch.uint8 and t.shape == s and t.is_contiguous(),
                   f"{n}: contiguous uint8 {list(s)}")
         self.k_q, self.k_s, self.v_q, self.v_s = storage
-        _same_device(self.k_q, "k_q", k_s=self.k_s, v_q=self.v_q, v_s=self.v_s)
+        self._gpu = _gpu_of("k_q", *storage)
+        self._device = self.k_q.device
+        self._heads, self._k_dim, self._v_dim = heads, k_dim, v_dim
         self._dref = ctypes.byref(self.dims)
         self._memory = tuple(_ptr(t) for t in storage)
-        self._device = self.k_q.device
 
     def _index(self, page_table, cu_rows, start):
-        _same_device(self.k_q, "the cache", page_table=page_table, cu_rows=cu_rows, start=start)
-        _need(page_table.dtype == torch.int32 and page_table.dim() == 2 and
-              (page_table.stride(1) == 1 or page_table.shape[1] <= 1), "page_table: int32 [B, pages]")
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 or cu_rows.dtype != torch.int32:
+            raise ValueError("page_table: int32 [B, pages], cu_rows: int32 [B + 1]")
         B, P = page_table.shape
-        _need(cu_rows.dtype == torch.int32 and cu_rows.shape == (B + 1,) and cu_rows.is_contiguous(),
-              "cu_rows: contiguous int32 [B + 1]")
-        if start is not None:
-            _need(start.dtype == torch.int32 and start.shape == (B,) and start.is_contiguous(), "start: contiguous int32 [B]")
-        _need(B <= 1 or page_table.stride(0) >= P, "page_table's rows must not overlap")
+        if P > 1 and page_table.stride(1) != 1 or B > 1 and page_table.stride(0) < P:
+            raise ValueError("page_table's last dimension must be contiguous, its rows must not overlap")
+        if cu_rows.shape != (B + 1,) or not cu_rows.is_contiguous():
+            raise ValueError("cu_rows: contiguous int32 [B + 1]")
+        if start is not None and (start.dtype != torch.int32 or start.shape != (B,) or not start.is_contiguous()):
+            raise ValueError("start: contiguous int32 [B]")
         return cu_rows.data_ptr(), _ptr(start), page_table.data_ptr(), page_table.stride(0) if B > 1 else P, B, P
 
     def _rows(self, t, name, dim):
-        heads = self.dims.heads
+        heads = self._heads
         if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.stride(2) != 1:
             raise ValueError(f"{name}: bf16 [rows, {heads}, {dim}], last dimension contiguous")
         # the stride of a dimension of one entry says nothing
         return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * dim, t.stride(1) if heads > 1 else dim
 
     def _planes(self, k, v):
-        d = self.dims
-        _need((v is None) == (d.v_dim == 0), "v goes with v_dim > 0, and only with it")
-        _same_device(self.k_q, "the cache", k=k, v=v)
-        k_args = self._rows(k, "k", d.k_dim)
+        if (v is None) != (self._v_dim == 0):
+            raise ValueError("v goes with v_dim > 0, and only with it")
+        k_args = self._rows(k, "k", self._k_dim)
         if v is None:
             return *k_args, None, 0, 0
         _need(v.shape[0] == k.shape[0], "k and v must have the same number of rows")
-        return *k_args, *self._rows(v, "v", d.v_dim)
+        return *k_args, *self._rows(v, "v", self._v_dim)
 
     def write(self, k, v, page_table, cu_rows, start=None):
         """Quantizes the rows of k [rows, heads, k_dim] and v (None with v_dim=0) into the cache.  Rows
@@ -286,22 +287,23 @@ class PagedCache:
         position i lives in page page_table[b, i // page_size].  Rows outside every sequence, and positions without
         a page (past the table, or a page number outside the cache), are passed over.  Two rows of one call must not
         share a slot."""
+        _gpu_of("the cache", self.k_q, k, v, page_table, cu_rows, start)
         index = self._index(page_table, cu_rows, start)
         planes = self._planes(k, v)
-        _call(self._device, "mxfp4_cache_write", self._dref, *planes, k.shape[0], *index, *self._memory)
+        _call(self._gpu, "mxfp4_cache_write", self._dref, *planes, k.shape[0], *index, *self._memory)
 
     def read(self, page_table, cu_rows, start=None, rows=None, k_out=None, v_out=None):
         """Reads rows back as bf16: (k [rows, heads, k_dim], v or None), rows and positions as in `write`.  Give
         `rows` (the outputs are allocated; rows outside every sequence are then undefined) or the outputs, whose
         rows outside every sequence are left as they were.  Positions without a page read as zeros."""
         index = self._index(page_table, cu_rows, start)
-        d = self.dims
         if k_out is None:
             _need(rows is not None and rows >= 0 and v_out is None, "give rows, or the outputs")
-            k_out = torch.empty((rows, d.heads, d.k_dim), dtype=torch.bfloat16, device=self._device)
-            if d.v_dim:
-                v_out = torch.empty((rows, d.heads, d.v_dim), dtype=torch.bfloat16, device=self._device)
+            k_out = torch.empty((rows, self._heads, self._k_dim), dtype=torch.bfloat16, device=self._device)
+            if self._v_dim:
+                v_out = torch.empty((rows, self._heads, self._v_dim), dtype=torch.bfloat16, device=self._device)
+        _gpu_of("the cache", self.k_q, k_out, v_out, page_table, cu_rows, start)
         planes = self._planes(k_out, v_out)
         _need(rows is None or rows == k_out.shape[0], "rows must be the outputs' rows")
-        _call(self._device, "mxfp4_cache_read", self._dref, *self._memory, k_out.shape[0], *index, *planes)
+        _call(self._gpu, "mxfp4_cache_read", self._dref, *self._memory, k_out.shape[0], *index, *planes)
         return k_out, v_out

@@ -211,6 +211,42 @@ def test_in_a_training_step():
     assert counts.sum().item() == 180
 
 
+def test_very_many_tokens():
+    l, ids, mask = case(300007, 8, 2, 15, True)
+    assert_close(*run(l, ids, mask), l, ids, mask, 0.01)
+
+
+def test_second_derivatives_and_changed_logits_are_refused():
+    l, ids, _ = case(20, 6, 2, 16)
+    ld, idd, _ = device_inputs(l, ids, None)
+    loss, _ = mx.balance_loss(ld, idd)
+    with pytest.raises(RuntimeError, match="second derivative"):
+        torch.autograd.grad(loss, ld, create_graph=True)
+    x = ld * 1.0
+    loss, _ = mx.balance_loss(x, idd)
+    x.add_(1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+def test_calls_on_two_streams_at_once_and_from_another_device(monkeypatch):
+    l, ids, mask = case(5000, 96, 4, 17, True)
+    ld, idd, md = device_inputs(l, ids, mask)
+    want = [t.detach().clone() for t in run(l, ids, mask, 0.5)]
+    w = torch.tensor(0.5, device="cuda")
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(6):
+        with torch.cuda.stream(streams[i % 2]):
+            loss, counts = mx.balance_loss(ld, idd, md)
+            got.append((loss, counts, torch.autograd.grad(loss, ld, w)[0]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
+    monkeypatch.setattr(mx.ops, "_current_gpu", lambda: -1)  # as if another device were the current one
+    assert all(torch.equal(a, b) for a, b in zip(run(l, ids, mask, 0.5), want))
+
+
 def test_on_another_stream_and_in_a_graph():
     l, ids, mask = case(2000, 128, 8, 12, True)
     ld, idd, md = device_inputs(l, ids, mask)

@@ -146,6 +146,22 @@ def test_many_sequences():
     cycle("mxfp8", 16, 1, 64, 32, have, new)
 
 
+@pytest.mark.parametrize("fmt", list(FMTS))
+def test_many_rows(fmt):
+    """Waves that take several rows: narrow ones, and more rows than waves are wanted, with sequences, gaps and missing
+    pages inside a wave's rows."""
+    g = np.random.default_rng(3)
+    have, new = list(g.integers(0, 9, 900)), list(g.integers(0, 25, 900))
+    cycle(fmt, 8, 1, 32, 32, have, new, lead=5, tail=9, holes=True)
+    have, new = list(g.integers(0, 3, 41)), list(g.integers(1500, 2100, 41))
+    cycle(fmt, 64, 1, 64, 32, have, new, holes=True, seed=1)
+
+
+def test_the_widest_row():
+    cycle("mxfp8", 2, 512, 2048, 0, [1], [2])
+    cycle("nvfp4", 1, 1, 1 << 20, 16, [0], [2])
+
+
 def test_codes_are_the_quantizers():
     """A cached row holds what quantize / nvfp4_quantize give for it."""
     g = synth.rng(321)
@@ -255,6 +271,17 @@ def test_another_stream_and_a_graph():
         np.testing.assert_array_equal(bf16_host_bits(out[0]), host.read(0, slots, 0))
         eager = c.read(table, cu_all, rows=18)
         assert torch.equal(eager[0], out[0]) and torch.equal(eager[1], out[1])
+
+
+def test_calls_from_another_device(monkeypatch):
+    c, host, g = make("mxfp4", 3, 4, 2, 32, 32)
+    kb, vb = rows_of(g, 5, 2, 32), rows_of(g, 5, 2, 32)
+    monkeypatch.setattr(mx.ops, "_current_gpu", lambda: -1)  # as if another device were the current one
+    c.write(bf16_dev(kb), bf16_dev(vb), i32([[2, 1]]), i32([0, 5]))
+    slots = C.slots_ref(5, [0, 5], None, [[2, 1]], 4, 3)
+    host.write((kb, vb), slots)
+    host.check(c)
+    np.testing.assert_array_equal(bf16_host_bits(c.read(i32([[2, 1]]), i32([0, 5]), rows=5)[1]), host.read(1, slots, 0))
 
 
 def test_refusals():

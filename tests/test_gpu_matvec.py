@@ -220,6 +220,57 @@ def test_bad_offsets_and_pairs_stay_inside():
     assert bool((mx.fp4_expert_matvec(*args[:3], none, sp, **kw, y=torch.full_like(y, 7.0)) == 7.0).all())
 
 
+def test_long_rows_and_many_rows():
+    """K past the blocks that one round of waves takes; more rows of x than a grid has places for."""
+    dense(2, 3, 1 << 18, "mxfp4", None, torch.float32, seed=6)
+    dense(6, 5, (1 << 17) + 16, "nvfp4", "fp32", seed=6)
+    g = synth.rng(314)
+    M = (1 << 20) - 7
+    q, s, _ = weights(g, (20, 32), "mxfp4")
+    x = synth.to_bf16_bits(g.standard_normal((1000, 32), dtype=np.float32))
+    xd = bf16_dev(x).repeat(M // 1000 + 1, 1)[:M]
+    qd, sd = torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda()
+    y = mx.fp4_matvec(xd, qd, sd)
+    first = mx.fp4_matvec(xd[:1000], qd, sd)
+    assert_dense(first, x, q, s, None, None, torch.bfloat16)
+    ref, mag = V.matvec_ref(x, q, s)
+    at = np.arange(M - 3000, M) % 1000
+    err = np.abs(host(y[M - 3000:]) - ref[at])
+    assert np.all(err <= linear_bound(ref[at], mag[at], 32) + 2.0 ** -8 * np.abs(ref[at]) + 2.0 ** -133)
+
+
+def test_expert_weights_past_4_gib():
+    """The last of 1024 experts' codes lie past 2^32 bytes, its scales past 2^28; two tokens choose it and the first."""
+    E, N, K = 1024, 2056, 4096
+    g = synth.rng(315)
+    q0, s0, _ = weights(g, (2, N, K), "mxfp4")
+    q = torch.zeros(E, N, K // 2, dtype=torch.uint8, device="cuda")
+    s = torch.zeros(E, N, K // 32, dtype=torch.uint8, device="cuda")
+    assert q.numel() > 1 << 32
+    for i, e in enumerate((0, E - 1)):
+        q[e], s[e] = torch.from_numpy(q0[i]).cuda(), torch.from_numpy(s0[i]).cuda()
+    x = synth.to_bf16_bits(g.standard_normal((2, K), dtype=np.float32))
+    ids = np.array([[E - 1, 0], [0, E - 1]])
+    offs, sp = pairs_of(ids, E)
+    y = mx.fp4_expert_matvec(bf16_dev(x), q, s, offs, sp, top_k=2, out_dtype=torch.float32)
+    ref, mag = V.expert_matvec_ref(x, q0, s0, np.where(ids == 0, 0, 1), True)
+    assert np.all(np.abs(host(y) - ref) <= linear_bound(ref, mag, K) + U * np.abs(ref))
+
+
+def test_calls_on_two_streams_at_once_and_from_another_device(monkeypatch):
+    xd, qd, sd, gs, y = dense(5, 300, 2048, "mxfp4", None, seed=7)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(8):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append(mx.fp4_matvec(xd, qd, sd))
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, y) for t in got)
+    monkeypatch.setattr(mx.ops, "_current_gpu", lambda: -1)  # as if another device were the current one
+    assert torch.equal(mx.fp4_matvec(xd, qd, sd), y)
+
+
 def test_no_rows():
     q, s = torch.zeros(16, 32, dtype=torch.uint8, device="cuda"), torch.zeros(16, 2, dtype=torch.uint8, device="cuda")
     assert mx.fp4_matvec(torch.zeros(0, 64, dtype=torch.bfloat16, device="cuda"), q, s).shape == (0, 16)
