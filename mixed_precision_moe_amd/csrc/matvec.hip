@@ -18,7 +18,9 @@ typedef unsigned u32x2_t __attribute__((ext_vector_type(2)));
 typedef u32x4_t u32x4_a8 __attribute__((aligned(8)));
 
 constexpr int kStep = 128;     // K elements of one step: 32 for each quarter of the wave
-constexpr int64_t kFull = 2048;  // waves that fill the chip
+constexpr int64_t kFull = 2048;      // waves that fill the chip
+constexpr int64_t kFullWide = 6144;  // waves of four tiles that keep it evenly loaded
+constexpr int64_t kWide = 4096;      // tiles from which a wave takes four of them
 template <int CTRL>
 MX_DEV float dpp(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
@@ -46,16 +48,15 @@ MX_DEV bf16x8_t dequant8(uint32_t codes, float scale) {
   return __builtin_bit_cast(bf16x8_t, out);
 }
 
-// The codes of the 32 elements from k on of a row of K elements.  Past the row's end it loads the row's last 32 again
-// (no branch, nothing out of bounds): x is zero there.  NVFP4 rows may end inside the 32 (K % 32 == 16): then
-// what is loaded starts 16 elements early, and settle() moves it.
+// The codes of 32 elements, from byte `at` of a row on.  NVFP4 rows start on 8-byte boundaries.
 template <int FMT>
-MX_DEV u32x4_t load_codes(const uint8_t* q, int k, int K) {
-  const int at = min(k, K - 32);
-  if (FMT == MXFP4_FMT_MXFP4) return *reinterpret_cast<const u32x4_t*>(q + at / 2);
-  return *reinterpret_cast<const u32x4_a8*>(q + at / 2);
+MX_DEV u32x4_t load_codes(const uint8_t* q, uint32_t at) {
+  if (FMT == MXFP4_FMT_MXFP4) return *reinterpret_cast<const u32x4_t*>(q + at);
+  return *reinterpret_cast<const u32x4_a8*>(q + at);
 }
 
+// Past a row's end its last 32 elements are loaded again (nothing out of bounds: x is zero there).  NVFP4 rows may end
+// inside the 32 (K % 32 == 16): then what was loaded starts 16 elements early, and moves here.
 template <int FMT>
 MX_DEV void settle(u32x4_t& q, int k, int K) {
   if (FMT == MXFP4_FMT_MXFP4 || K % 32 == 0) return;
@@ -77,37 +78,38 @@ MX_DEV uint16_t to_bf16(float f) {  // round to nearest even; infinities pass, N
 template <int FMT>
 constexpr int kBlock = FMT == MXFP4_FMT_NVFP4 ? 16 : 32;
 
-// The weights of 16 rows (the lane's is row rc): codes and scales, and where the scale tensor ends.
-struct Rows {
-  const uint8_t* q;        // codes of the lane's row of the first tile
-  const uint8_t* s0;       // scales: the tensor
-  int64_t s_at, s_bytes;   // the lane's row of the first tile in it; its length
-  int64_t q_tile, s_tile;  // bytes from tile to tile
+// The weights of R tiles of 16 rows: where each tile's codes and scales start (the same for all lanes), how many bytes
+// of scales the tensor has from there on, and the lane's row of the tile (rows past the last repeat it).
+template <int R>
+struct Tiles {
+  const uint8_t *q[R], *s[R];
+  int32_t s_left[R];
+  uint32_t row[R];
 };
 
-// DW dwords from byte `at` on of a tensor of `bytes` bytes (at < bytes); bytes past its end read as zeros.  near_end:
-// they may reach past it (the same for the whole wave).
+// DW dwords from byte `at` on of `left` bytes (at < left); bytes past them read as zeros.  near_end: they may reach past
+// (the same for the whole wave).
 template <int DW>
-MX_DEV void load_bytes(const uint8_t* t, int64_t at, int64_t bytes, bool near_end, uint32_t* v) {
+MX_DEV void load_bytes(const uint8_t* t, uint32_t at, int left, bool near_end, uint32_t* v) {
   typedef unsigned vec_t __attribute__((ext_vector_type(DW)));
   typedef vec_t vec_a1 __attribute__((aligned(1)));
-  if (near_end && bytes < 4 * DW) {  // the whole tensor is shorter than a load
+  if (near_end && left < 4 * DW) {  // less than a load altogether
 #pragma unroll 1
     for (int i = 0; i < DW; i++) {
       uint32_t d = 0;
 #pragma unroll 1
-      for (int b = 0; b < 4; b++) d |= at + 4 * i + b < bytes ? (uint32_t)t[at + 4 * i + b] << (8 * b) : 0;
+      for (int b = 0; b < 4; b++) d |= (int)at + 4 * i + b < left ? (uint32_t)t[at + 4 * i + b] << (8 * b) : 0;
 #pragma unroll
       for (int j = 0; j < DW; j++) v[j] = i == j ? d : v[j];
     }
     return;
   }
-  const int64_t from = near_end ? min(at, bytes - 4 * DW) : at;
+  const uint32_t from = near_end ? min(at, (uint32_t)(left - 4 * DW)) : at;
   const vec_t w = *reinterpret_cast<const vec_a1*>(t + from);
 #pragma unroll
   for (int i = 0; i < DW; i++) v[i] = w[i];
   if (near_end) {
-    const int d = (int)(at - from);  // the bytes from d < 4 DW on move to the front
+    const uint32_t d = at - from;  // the bytes from d < 4 DW on move to the front
 #pragma unroll
     for (int h = DW / 2; h > 0; h >>= 1)
 #pragma unroll
@@ -124,13 +126,12 @@ MX_DEV void load_bytes(const uint8_t* t, int64_t at, int64_t bytes, bool near_en
 // scales and one or a few loads of x serve (a byte of scales at a time beside the codes took a third of the
 // kernel's time); the next block's loads are on their way while a block is worked on.  x goes through a piece of LDS
 // of the wave's own (xs), which turns whole rows as they are loaded into the instruction's other operand.
-// That operand has 16 columns.  For XR <= 4 four columns belong to a row of x and hold different eighths of the
+// That operand has 16 columns.  FEW (XR <= 4): four columns belong to a row of x and hold different eighths of the
 // quarter's 32 elements, so that one 16-byte read serves all four operands of W.  Operand j's product is wanted in
 // the columns that hold the eighth j alone: each j has sums of its own, and a row's four columns are added up at
 // the end.  What the other columns sum up is dropped, also where it is not finite.
-template <int FMT, int R, int XR, int SB, typename RowX>
-MX_DEV void tile_sums(const Rows& w, int K, int wave, int waves, RowX row_of, uint16_t* xs, float* part) {
-  constexpr bool FEW = XR <= 4;
+template <int FMT, int R, int XR, int SB, bool FEW, typename RowX>
+MX_DEV void tile_sums(const Tiles<R>& w, int K, int wave, int waves, RowX row_of, uint16_t* xs, float* part) {
   constexpr int kB = SB * kStep, DW = SB * (FMT == MXFP4_FMT_NVFP4 ? 2 : 1);
   constexpr int PR = kB / 8, RPL = 64 / PR;              // 16-byte pieces of a row's block; rows of one load
   constexpr int XL = XR > RPL ? XR / RPL : 1;            // loads of x
@@ -141,29 +142,48 @@ MX_DEV void tile_sums(const Rows& w, int K, int wave, int waves, RowX row_of, ui
 #pragma unroll
   for (int l = 0; l < XL; l++) x[l] = row_of(l * RPL + lane / PR);
   uint16_t* xput = xs + lane / PR * kPitch + k_x;
-  const uint16_t* xget = xs + (FEW ? (rc >> 2) % XR * kPitch + (rc & 3) * 8 : rc * kPitch) + k_lane;
+  const uint16_t* xget = xs + (FEW ? (rc >> 2) % XR * kPitch + (rc & 3) * 8 : rc % XR * kPitch) + k_lane;
   struct Block {
     u32x4_t q[R][SB], x[XL];
     uint32_t s[R][DW];
   };
-  auto load = [&](Block& b, int k0) {
+  uint32_t q_at[R], s_at[R];
 #pragma unroll
-    for (int l = 0; l < XL; l++) b.x[l] = *reinterpret_cast<const u32x4_t*>(x[l] + min(k0 + k_x, K - 8));
+  for (int r = 0; r < R; r++) {
+    q_at[r] = w.row[r] * (uint32_t)(K / 2);
+    s_at[r] = w.row[r] * (uint32_t)(K / kBlock<FMT>);
+  }
+  auto load = [&](Block& b, int k0) {
+    const bool near_end = k0 + kB > K;
+    if (!near_end) {
+#pragma unroll
+      for (int l = 0; l < XL; l++) b.x[l] = *reinterpret_cast<const u32x4_t*>(x[l] + k0 + k_x);
+    } else {
+#pragma unroll
+      for (int l = 0; l < XL; l++) b.x[l] = *reinterpret_cast<const u32x4_t*>(x[l] + min(k0 + k_x, K - 8));
+    }
 #pragma unroll
     for (int r = 0; r < R; r++) {
-      const int64_t at = w.s_at + r * w.s_tile + k0 / kBlock<FMT>;
-      load_bytes<DW>(w.s0, at, w.s_bytes, k0 + kB > K, b.s[r]);
+      load_bytes<DW>(w.s[r], s_at[r] + k0 / kBlock<FMT>, w.s_left[r], near_end, b.s[r]);
+      if (!near_end) {
 #pragma unroll
-      for (int i = 0; i < SB; i++) b.q[r][i] = load_codes<FMT>(w.q + r * w.q_tile, k0 + i * kStep + k_lane, K);
+        for (int i = 0; i < SB; i++) b.q[r][i] = load_codes<FMT>(w.q[r], q_at[r] + (k0 + k_lane) / 2 + i * (kStep / 2));
+      } else {
+#pragma unroll
+        for (int i = 0; i < SB; i++)
+          b.q[r][i] = load_codes<FMT>(w.q[r], q_at[r] + min(k0 + i * kStep + k_lane, K - 32) / 2);
+      }
     }
-    __builtin_amdgcn_sched_barrier(0);  // the loads go out before the other block is worked on
+    __builtin_amdgcn_sched_barrier(0);  // the loads go out before anything waits for one
   };
   f32x4_t acc[R][FEW ? 4 : 1] = {};
   auto work = [&](Block& b, int k0) {
 #pragma unroll
-    for (int l = 0; l < XL; l++) {  // past K: zeros
+    for (int l = 0; l < XL; l++) {
+      if (k0 + kB > K) {  // past K: zeros
 #pragma unroll
-      for (int i = 0; i < 4; i++) b.x[l][i] = k0 + k_x < K ? b.x[l][i] : 0;
+        for (int i = 0; i < 4; i++) b.x[l][i] = k0 + k_x < K ? b.x[l][i] : 0;
+      }
       if (XR >= RPL || lane / PR < XR) *reinterpret_cast<u32x4_t*>(xput + l * RPL * kPitch) = b.x[l];
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -230,18 +250,22 @@ constexpr int wave_bytes(int R, int xr, int few_steps) {
   return x > sums ? x : sums;
 }
 
+// Waves per SIMD that the registers are made to fit: four tiles need more of them than four waves leave.
+constexpr int waves_a_simd(int R) { return R == 4 ? 3 : 4; }
+
 // One workgroup: a tile of 16 outputs (SWIGLU: 16 gate rows and the 16 up rows), its waves sharing the blocks of K,
 // against up to 16 rows of x at a time.  XR: the most rows there are (1, 4 or 16); SB: steps of a block for up to four.
 // R: tiles of 16 rows of W (SWIGLU: the gate's and the up projection's).
 template <int FMT, bool EXPERT, bool SWIGLU, int XR, int R, int SB>
-__global__ __launch_bounds__(1024, 4) void matvec_kernel(MatvecArgs a) {
+__global__ __launch_bounds__(XR > kFew ? 512 : 1024, waves_a_simd(R)) void matvec_kernel(MatvecArgs a) {
+  constexpr int OT = SWIGLU ? R / 2 : R;  // tiles of outputs
   constexpr int kWave = wave_bytes(R, XR, SB);
   extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
   const int K = (int)a.K;
   const int64_t n_out = SWIGLU ? a.N / 2 : a.N;
-  const int64_t n0 = (int64_t)blockIdx.x * (SWIGLU ? 16 : 16 * R);
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * OT);
   int64_t e = 0, first = 0, count = a.M;
   if (EXPERT) {
     e = blockIdx.y;
@@ -266,11 +290,18 @@ __global__ __launch_bounds__(1024, 4) void matvec_kernel(MatvecArgs a) {
     count = (hi > a.M ? a.M : hi) - first;
     if (count <= 0) return;
   }
-  const float gs = EXPERT && FMT == MXFP4_FMT_NVFP4 ? a.gscales[e] : a.gscale;
+  const float rgs = FMT == MXFP4_FMT_NVFP4 ? 1.0f / (EXPERT ? a.gscales[e] : a.gscale) : 1.0f;
   const int KQ = K / 2, KS = K / kBlock<FMT>;
-  const int64_t row = e * a.N + min(n0 + (lane & 15), n_out - 1);  // past the last row: repeats it, not stored
-  const int64_t apart = SWIGLU ? n_out : R > 1 ? e * a.N + min(n0 + 16 + (lane & 15), n_out - 1) - row : 0;
-  const Rows w = {a.wq + row * KQ, a.ws, row * KS, (int64_t)a.E * a.N * KS, apart * KQ, apart * KS};
+  Tiles<R> w;
+#pragma unroll
+  for (int r = 0; r < R; r++) {
+    const int64_t first_row = min(n0 + 16 * (r % OT), n_out - 1);
+    const int64_t row = e * a.N + first_row + r / OT * n_out;
+    w.q[r] = a.wq + row * KQ;
+    w.s[r] = a.ws + row * KS;
+    w.s_left[r] = (int32_t)min(((int64_t)a.E * a.N - row) * KS, (int64_t)1 << 30);
+    w.row[r] = (uint32_t)min((int64_t)(lane & 15), n_out - 1 - first_row);
+  }
   uint8_t* mine = smem + wave * kWave;
   const int64_t m_step = EXPERT ? 16 : (int64_t)gridDim.y * 16;
   for (int64_t m0 = EXPERT ? 0 : (int64_t)blockIdx.y * 16; m0 < count; m0 += m_step) {
@@ -284,28 +315,33 @@ __global__ __launch_bounds__(1024, 4) void matvec_kernel(MatvecArgs a) {
       const int64_t p = pair_of(min(c, cols - 1));
       return a.x + (p < 0 ? 0 : EXPERT ? (int64_t)((uint32_t)p / (uint32_t)a.top_k) : p) * a.ldx;
     };
-    if (XR == 1 || (EXPERT && cols == 1))
-      tile_sums<FMT, R, 1, SB>(w, K, wave, waves, row_of, (uint16_t*)mine, (float*)mine);
-    else if (XR == 4 || cols <= kFew)
-      tile_sums<FMT, R, 4, SB>(w, K, wave, waves, row_of, (uint16_t*)mine, (float*)mine);
+    uint16_t* xs = (uint16_t*)mine;
+    float* part = (float*)mine;
+    if (R < 4 && (XR == 1 || (EXPERT && cols == 1)))
+      tile_sums<FMT, R, 1, SB, true>(w, K, wave, waves, row_of, xs, part);
+    else if (R < 4 && (XR == 4 || cols <= kFew))
+      tile_sums<FMT, R, 4, SB, true>(w, K, wave, waves, row_of, xs, part);
+    else if (R == 4 && cols <= 4)
+      tile_sums<FMT, R, 4, kManySteps, false>(w, K, wave, waves, row_of, xs, part);
+    else if (cols <= 8)
+      tile_sums<FMT, R, 8, kManySteps, false>(w, K, wave, waves, row_of, xs, part);
     else
-      tile_sums<FMT, R, 16, kManySteps>(w, K, wave, waves, row_of, (uint16_t*)mine, (float*)mine);
+      tile_sums<FMT, R, 16, kManySteps, false>(w, K, wave, waves, row_of, xs, part);
     __syncthreads();
-    constexpr int kOuts = SWIGLU ? 1 : R;  // tiles of outputs
-    for (int o = tid; o < cols * 16 * kOuts; o += blockDim.x) {
-      const int at = o & 15, tile = (o >> 4) % kOuts, col = (o >> 4) / kOuts;
+    for (int o = tid; o < cols * 16 * OT; o += blockDim.x) {
+      const int at = o % (16 * OT), col = o / (16 * OT), tile = at / 16;
       float v[SWIGLU ? 2 : 1];
 #pragma unroll
       for (int r = 0; r < (SWIGLU ? 2 : 1); r++) {
         v[r] = 0.0f;
         for (int g = 0; g < waves; g++)
-          v[r] += reinterpret_cast<const float*>(smem + g * kWave)[(tile + r) * 256 + col * 16 + at];
+          v[r] += reinterpret_cast<const float*>(smem + g * kWave)[(tile + r * OT) * 256 + col * 16 + at % 16];
       }
-      const int64_t n = n0 + tile * 16 + at, out_row = pair_of(col);
+      const int64_t n = n0 + at, out_row = pair_of(col);
       if (n < n_out && out_row >= 0) {
 #pragma unroll
         for (int r = 0; r < (SWIGLU ? 2 : 1); r++) {
-          if (FMT == MXFP4_FMT_NVFP4) v[r] /= gs;
+          if (FMT == MXFP4_FMT_NVFP4) v[r] *= rgs;
           if (a.bias) v[r] += bias_at(a.bias, a.bias_fp32, e * a.N + n + r * n_out);
         }
         const float y = SWIGLU ? v[0] / (1.0f + __expf(-v[0])) * v[SWIGLU ? 1 : 0] : v[0];
@@ -319,20 +355,22 @@ __global__ __launch_bounds__(1024, 4) void matvec_kernel(MatvecArgs a) {
   }
 }
 
-template <int FMT, bool EXPERT, bool SWIGLU, int XR, int SB>
+template <int FMT, bool EXPERT, bool SWIGLU, int XR, int R, int SB>
 int launch_rows(const MatvecArgs& a, hipStream_t stream) {
-  constexpr int R = SWIGLU || XR > kFew ? 2 : 1, kRows = SWIGLU ? 16 : 16 * R;
+  constexpr int kRows = 16 * (SWIGLU ? R / 2 : R);
   const int64_t n_out = SWIGLU ? a.N / 2 : a.N;
   const int64_t groups = EXPERT ? (a.M < a.E ? a.M : a.E) : (a.M + 15) / 16;
   const int64_t tiles = (n_out + kRows - 1) / kRows;
   const int kB = (XR > kFew ? kManySteps : SB) * kStep;
   const int64_t blocks = (a.K + kB - 1) / kB;
-  // blocks of K a wave works through: as few as leave waves to fill the chip, and 16 waves a workgroup
-  int64_t each = tiles * groups * blocks / kFull;
+  // blocks of K a wave works through: as few as leave waves to fill the chip, and 16 waves a workgroup (8 for many rows
+  // of x, whose LDS they share); a wave less where the last round would be less than half full
+  int64_t each = tiles * groups * blocks / (R == 4 ? kFullWide : kFull);
   each = each < 1 ? 1 : each;
   const int64_t most = XR > kFew ? 8 : 16;
   if ((blocks + each - 1) / each > most) each = (blocks + most - 1) / most;
-  const int waves = (int)((blocks + each - 1) / each);
+  int waves = (int)((blocks + each - 1) / each);
+  if (waves > 1 && (waves - blocks % waves) % waves * 2 >= waves) waves--;
   const dim3 grid((unsigned)tiles, (unsigned)(groups < 65535 ? groups : 65535));
   const int lds = waves * wave_bytes(R, XR, SB);
   hipLaunchKernelGGL((matvec_kernel<FMT, EXPERT, SWIGLU, XR, R, SB>), grid, dim3(64 * waves), lds, stream, a);
@@ -341,13 +379,17 @@ int launch_rows(const MatvecArgs& a, hipStream_t stream) {
 
 template <int FMT, bool EXPERT, bool SWIGLU, int SB>
 int launch_steps(const MatvecArgs& a, hipStream_t stream) {
-  if (a.M == 1) return launch_rows<FMT, EXPERT, SWIGLU, 1, SB>(a, stream);
-  return a.M <= kFew ? launch_rows<FMT, EXPERT, SWIGLU, 4, SB>(a, stream)
-                     : launch_rows<FMT, EXPERT, SWIGLU, 16, SB>(a, stream);
+  constexpr int kOne = SWIGLU ? 2 : 1;
+  if (a.M == 1) return launch_rows<FMT, EXPERT, SWIGLU, 1, kOne, SB>(a, stream);
+  return a.M <= kFew ? launch_rows<FMT, EXPERT, SWIGLU, 4, kOne, SB>(a, stream)
+                     : launch_rows<FMT, EXPERT, SWIGLU, 16, 2, SB>(a, stream);
 }
 
 template <int FMT, bool EXPERT, bool SWIGLU>
 int launch_waves(const MatvecArgs& a, hipStream_t stream) {
+  const int64_t n_out = SWIGLU ? a.N / 2 : a.N;
+  if (EXPERT && a.M >= 3 * (int64_t)a.E && a.K >= 6 * kManySteps * kStep && (n_out + 15) / 16 * a.E >= kWide)
+    return launch_rows<FMT, EXPERT, SWIGLU, 16, EXPERT ? 4 : 2, kManySteps>(a, stream);
   // blocks of four steps, or of two where those would be more than a fifth padding
   const int64_t padded = (a.K + 4 * kStep - 1) / (4 * kStep) * (4 * kStep);
   return padded * 4 > a.K * 5 ? launch_steps<FMT, EXPERT, SWIGLU, 2>(a, stream)
