@@ -1,5 +1,18 @@
 // Matrix-vector products with 4-bit weights in the standard layout: y = x W^T (/ global scale) + b for a few
 // rows of x, and the same product of every routed pair with its expert's matrix (with SwiGLU on request).
+//
+// What bounds them is the weights' way from memory (0.53 or 0.56 bytes each, read once per 16 rows of x), and for small
+// matrices the chain of a launch, one load, one join.  So the weights are dequantized to bf16 in registers (exact: two
+// significant bits times a power of two, or times four bits) and multiplied on the matrix cores whatever the number of
+// rows, the waves of a workgroup share K and meet once, and nothing is set up or waited for before the first load of
+// weights but, in the expert form, the expert's number.  Measured (one pass, kernel alone):
+//   1 x 7168 x 7168           MXFP4  7.5 us (3.7 TB/s), NVFP4 10.2 us (2.8 TB/s: four instead of one instruction a pair)
+//   1 x 28672 x 7168          MXFP4 24 us (4.5 TB/s), NVFP4 25 us; loads of the same pieces alone 17.5 us
+//   16 x 7168 x 2048          MXFP4  5.6 us; 16 x 7168 x 7168 10.5 us
+//   64 tokens, top-8 of 128   2048 x 768: MXFP4 29 us, NVFP4 33 us; 1536 x 2048 with SwiGLU 46 and 56 us (4.5, 3.9 TB/s)
+// Tried and slower: scales a byte at a time beside the codes (a third of the time); x 16 bytes a row from memory (half of
+// the time at 16 rows); scales and x of the whole workgroup in LDS behind a barrier (7168 x 7168: 11 to 14 us); a ring or a
+// second set of registers for the next block (spills, or fewer waves: 12 to 18 us).
 #include <hip/hip_runtime.h>
 
 #include "ops.h"
@@ -18,9 +31,9 @@ typedef unsigned u32x2_t __attribute__((ext_vector_type(2)));
 typedef u32x4_t u32x4_a8 __attribute__((aligned(8)));
 
 constexpr int kStep = 128;     // K elements of one step: 32 for each quarter of the wave
-constexpr int64_t kFull = 2048;      // waves that fill the chip
-constexpr int64_t kFullWide = 6144;  // waves of four tiles that keep it evenly loaded
-constexpr int64_t kWide = 4096;      // tiles from which a wave takes four of them
+constexpr int64_t kFull = 2048;      // waves that fill the chip (1 x 7168 x 7168 NVFP4: 10.2 us, with 6144 11.9 us)
+constexpr int64_t kFullWide = 6144;  // waves of four tiles (1536 x 2048 with SwiGLU, NVFP4: 56 us, with 2048 60 us)
+constexpr int64_t kWide = 4096;      // tiles that are enough for a wave to take four of them
 template <int CTRL>
 MX_DEV float dpp(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
@@ -123,9 +136,9 @@ MX_DEV void load_bytes(const uint8_t* t, uint32_t at, int left, bool near_end, u
 //
 // A step is 128 elements of K: each quarter of the wave holds 32 of them, 16 bytes of codes a lane (a 64-byte piece of
 // 16 rows), which make four operands of the matrix instruction.  A block is SB steps that one load each of a row's
-// scales and one or a few loads of x serve (a byte of scales at a time beside the codes took a third of the
-// kernel's time); the next block's loads are on their way while a block is worked on.  x goes through a piece of LDS
-// of the wave's own (xs), which turns whole rows as they are loaded into the instruction's other operand.
+// scales and one or a few loads of x serve; all loads of a block go out together, and the other waves of the SIMD work
+// meanwhile.  x goes through a piece of LDS of the wave's own (xs), which turns whole rows as they are loaded into the
+// instruction's other operand.
 // That operand has 16 columns.  FEW (XR <= 4): four columns belong to a row of x and hold different eighths of the
 // quarter's 32 elements, so that one 16-byte read serves all four operands of W.  Operand j's product is wanted in
 // the columns that hold the eighth j alone: each j has sums of its own, and a row's four columns are added up at
@@ -290,7 +303,7 @@ __global__ __launch_bounds__(XR > kFew ? 512 : 1024, waves_a_simd(R)) void matve
     count = (hi > a.M ? a.M : hi) - first;
     if (count <= 0) return;
   }
-  const float rgs = FMT == MXFP4_FMT_NVFP4 ? 1.0f / (EXPERT ? a.gscales[e] : a.gscale) : 1.0f;
+  const float gs = EXPERT && FMT == MXFP4_FMT_NVFP4 ? a.gscales[e] : a.gscale;
   const int KQ = K / 2, KS = K / kBlock<FMT>;
   Tiles<R> w;
 #pragma unroll
@@ -341,7 +354,7 @@ __global__ __launch_bounds__(XR > kFew ? 512 : 1024, waves_a_simd(R)) void matve
       if (n < n_out && out_row >= 0) {
 #pragma unroll
         for (int r = 0; r < (SWIGLU ? 2 : 1); r++) {
-          if (FMT == MXFP4_FMT_NVFP4) v[r] *= rgs;
+          if (FMT == MXFP4_FMT_NVFP4) v[r] /= gs;  // (its reciprocal may overflow)
           if (a.bias) v[r] += bias_at(a.bias, a.bias_fp32, e * a.N + n + r * n_out);
         }
         const float y = SWIGLU ? v[0] / (1.0f + __expf(-v[0])) * v[SWIGLU ? 1 : 0] : v[0];
@@ -388,9 +401,12 @@ int launch_steps(const MatvecArgs& a, hipStream_t stream) {
 template <int FMT, bool EXPERT, bool SWIGLU>
 int launch_waves(const MatvecArgs& a, hipStream_t stream) {
   const int64_t n_out = SWIGLU ? a.N / 2 : a.N;
+  // Four tiles a wave, which share its rows of x, where experts have three pairs on average and K is long: 1536 x 2048 with
+  // SwiGLU, four pairs an expert, NVFP4 64 -> 56 us.  With two pairs (4000 x 1600) two tiles take 59 us, four 71 us.
   if (EXPERT && a.M >= 3 * (int64_t)a.E && a.K >= 6 * kManySteps * kStep && (n_out + 15) / 16 * a.E >= kWide)
     return launch_rows<FMT, EXPERT, SWIGLU, 16, EXPERT ? 4 : 2, kManySteps>(a, stream);
-  // blocks of four steps, or of two where those would be more than a fifth padding
+  // Blocks of four steps, or of two where those would be more than a fifth padding (K = 768: 38 -> 35 us; K = 7168: 10.4
+  // and 10.7 us).
   const int64_t padded = (a.K + 4 * kStep - 1) / (4 * kStep) * (4 * kStep);
   return padded * 4 > a.K * 5 ? launch_steps<FMT, EXPERT, SWIGLU, 2>(a, stream)
                               : launch_steps<FMT, EXPERT, SWIGLU, 4>(a, stream);

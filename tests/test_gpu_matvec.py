@@ -121,6 +121,24 @@ def test_every_code_and_scale():
     np.testing.assert_array_equal(host(y), V.matvec_ref(x, q, s, None, 1.0)[0])
 
 
+@pytest.mark.parametrize("k", [-140, -120, 100, 127])
+def test_extreme_global_scales(k):
+    """A power of two as global scale moves the exponent and nothing else: also one whose reciprocal overflows, or has
+    no full precision."""
+    g = synth.rng(316)
+    q = g.integers(0, 256, (40, 48), dtype=np.uint8)
+    s = g.integers(1, 127, (40, 6), dtype=np.uint8)
+    e = 40 if k > 0 else -60  # keeps the quotients in range
+    x = synth.to_bf16_bits(g.standard_normal((2, 96)) * 2.0 ** e)
+    args = (bf16_dev(x), torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda())
+    one = host(mx.fp4_matvec(*args, fmt=mx.FMT_NVFP4, global_scale=1.0, out_dtype=torch.float32))
+    y = host(mx.fp4_matvec(*args, fmt=mx.FMT_NVFP4, global_scale=2.0 ** k, out_dtype=torch.float32))
+    want = np.ldexp(one, -k)
+    keep = np.abs(want) >= 2.0 ** -126
+    assert keep.any()
+    np.testing.assert_array_equal(y[keep], want[keep])
+
+
 def test_equals_the_linear_layer():
     """Against mx.Linear on the same weights, within both layers' tolerances."""
     g = synth.rng(312)
