@@ -100,18 +100,20 @@ struct Tiles {
   uint32_t row[R];
 };
 
-// DW dwords from byte `at` on of `left` bytes (at < left); bytes past them read as zeros.  near_end: they may reach past
-// (the same for the whole wave).
+// DW dwords from byte `at` on of `left` bytes (at < left), of which the first `n` are the row's own (n the same for the
+// whole wave); what lies past either reads as zeros: another row's scale may be one whose product with a code and a
+// zero is NaN.
 template <int DW>
-MX_DEV void load_bytes(const uint8_t* t, uint32_t at, int left, bool near_end, uint32_t* v) {
+MX_DEV void load_bytes(const uint8_t* t, uint32_t at, int left, int n, uint32_t* v) {
   typedef unsigned vec_t __attribute__((ext_vector_type(DW)));
   typedef vec_t vec_a1 __attribute__((aligned(1)));
+  const bool near_end = n < 4 * DW;
   if (near_end && left < 4 * DW) {  // less than a load altogether
 #pragma unroll 1
     for (int i = 0; i < DW; i++) {
       uint32_t d = 0;
 #pragma unroll 1
-      for (int b = 0; b < 4; b++) d |= (int)at + 4 * i + b < left ? (uint32_t)t[at + 4 * i + b] << (8 * b) : 0;
+      for (int b = 0; b < 4; b++) d |= 4 * i + b < n && (int)at + 4 * i + b < left ? (uint32_t)t[at + 4 * i + b] << (8 * b) : 0;
 #pragma unroll
       for (int j = 0; j < DW; j++) v[j] = i == j ? d : v[j];
     }
@@ -128,7 +130,11 @@ MX_DEV void load_bytes(const uint8_t* t, uint32_t at, int left, bool near_end, u
 #pragma unroll
       for (int i = 0; i < DW; i++) v[i] = d / (4 * h) % 2 ? (i + h < DW ? v[i + h] : 0) : v[i];
 #pragma unroll
-    for (int i = 0; i < DW; i++) v[i] = __builtin_amdgcn_alignbyte(i + 1 < DW ? v[i + 1] : 0, v[i], d & 3);
+    for (int i = 0; i < DW; i++) {
+      const int own = n - 4 * i;
+      v[i] = __builtin_amdgcn_alignbyte(i + 1 < DW ? v[i + 1] : 0, v[i], d & 3);
+      v[i] &= own >= 4 ? ~0u : own <= 0 ? 0u : (1u << (8 * own)) - 1;
+    }
   }
 }
 
@@ -177,7 +183,7 @@ MX_DEV void tile_sums(const Tiles<R>& w, int K, int wave, int waves, RowX row_of
     }
 #pragma unroll
     for (int r = 0; r < R; r++) {
-      load_bytes<DW>(w.s[r], s_at[r] + k0 / kBlock<FMT>, w.s_left[r], near_end, b.s[r]);
+      load_bytes<DW>(w.s[r], s_at[r] + k0 / kBlock<FMT>, w.s_left[r], (K - k0) / kBlock<FMT>, b.s[r]);
       if (!near_end) {
 #pragma unroll
         for (int i = 0; i < SB; i++) b.q[r][i] = load_codes<FMT>(w.q[r], q_at[r] + (k0 + k_lane) / 2 + i * (kStep / 2));

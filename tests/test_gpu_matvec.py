@@ -104,6 +104,51 @@ def test_rows_that_are_not_finite_stay_among_themselves(fmt, M):
     assert torch.equal(z[keep], y[keep]) and not torch.isfinite(z[1]).any() and not torch.isfinite(z[M - 1]).any()
 
 
+def loud_neighbours(shape, fmt):
+    """Weights whose odd rows are the largest the contract allows (MXFP4: 2^127) or NaN (NVFP4), and the same with odd
+    rows of zeros.  K ends inside a step, so a row's last step lies beside the next row's scales."""
+    g = synth.rng(316, *shape)
+    *rows, K = shape
+    q = g.integers(0, 256, (*rows, K // 2), dtype=np.uint8)
+    q[..., ::2, -8:] = 0x7F  # 6 and -6 where a scale that is not the row's own would overflow them
+    if fmt == "mxfp4":
+        s = np.full((*rows, K // 32), 120, np.uint8)
+        s[..., 1::2, :] = 254
+        q[..., 1::2, :] = 0x22  # ones
+    else:
+        s = np.full((*rows, K // 16), 0x38, np.uint8)
+        s[..., 1::2, :] = 0x7F
+    quiet_q, quiet_s = q.copy(), s.copy()
+    quiet_q[..., 1::2, :] = 0
+    quiet_s[..., 1::2, :] = 0
+    return [torch.from_numpy(t).cuda() for t in (q, s, quiet_q, quiet_s)]
+
+
+@pytest.mark.parametrize("fmt,K", [("mxfp4", 32), ("mxfp4", 96), ("mxfp4", 1056), ("nvfp4", 32), ("nvfp4", 48), ("nvfp4", 112),
+                                   ("nvfp4", 1040)])
+@pytest.mark.parametrize("M", [1, 3, 8, 16])
+def test_a_rows_scales_touch_no_other_row(fmt, K, M):
+    q, s, quiet_q, quiet_s = loud_neighbours((39, K), fmt)
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(K)).bfloat16().cuda()
+    gs = {"fmt": FMTS[fmt], "global_scale": 1.0 if fmt == "nvfp4" else None, "out_dtype": torch.float32}
+    y, z = mx.fp4_matvec(x, q, s, **gs), mx.fp4_matvec(x, quiet_q, quiet_s, **gs)
+    assert torch.isfinite(z).all() and torch.equal(y[:, ::2], z[:, ::2])
+
+
+# the second shape has four tiles a wave
+@pytest.mark.parametrize("fmt", list(FMTS))
+@pytest.mark.parametrize("E,N,K,pairs", [(6, 39, 1056, 3), (6, 39, 1056, 9), (64, 1024, 1568, 4), (64, 1024, 1568, 11)])
+def test_an_experts_scales_touch_no_other_row(fmt, E, N, K, pairs):
+    q, s, quiet_q, quiet_s = loud_neighbours((E, N, K), fmt)
+    P = pairs * E
+    x = torch.randn(P, K, generator=torch.Generator().manual_seed(K)).bfloat16().cuda()
+    offs = torch.arange(0, P + 1, pairs, dtype=torch.int32, device="cuda")
+    listed = torch.arange(P, dtype=torch.int32, device="cuda")
+    kw = {"fmt": FMTS[fmt], "global_scales": torch.ones(E, device="cuda") if fmt == "nvfp4" else None, "out_dtype": torch.float32}
+    y, z = mx.fp4_expert_matvec(x, q, s, offs, listed, **kw), mx.fp4_expert_matvec(x, quiet_q, quiet_s, offs, listed, **kw)
+    assert torch.isfinite(z).all() and torch.equal(y[:, ::2], z[:, ::2])
+
+
 def test_every_code_and_scale():
     """Each E2M1 code under scales over the formats' normal ranges, one at a time against a unit vector: exact."""
     K, N = 64, 120
