@@ -367,8 +367,8 @@ int fp4_expert_matvec(int32_t fmt, const void* w_q, const void* w_s, const float
  * slot: what such a slot then holds is not specified.  The read returns code * scale, rounded once to bf16
  * (NVFP4: the scale divided by the plane's global scale and multiplied by the code in binary32, then rounded).
  * k / v device bf16, element (row, head, i) at row * ldt + head * ldh + i; ldt, ldh multiples of 8, ldh >= dim,
- * ldt >= dim.  heads * dim <= 2^20.  Neither call uses a workspace.  The cache's pointers may be NULL when
- * num_pages is 0, the table when max_pages is 0. */
+ * ldt >= dim; the vectors that the read writes must not overlap.  heads * dim <= 2^20.  Neither call uses a
+ * workspace.  The cache's pointers may be NULL when num_pages is 0, the table when max_pages is 0. */
 typedef struct {
   int32_t fmt, heads, k_dim, v_dim, page_size;
   int64_t num_pages;

@@ -105,7 +105,8 @@ def balance_loss(logits, topk_ids, token_mask=None):
     logits fp32 [T, E] (rows may be strided), topk_ids int32 [T, k] as `route` returns them (an id outside
     [0, E) is a dropped pair), token_mask bool or uint8 [T] or None: tokens that count.  Returns (loss, counts):
     loss fp32, 0-dim, differentiable in the logits: E / (k V^2) * sum_e counts_e * sum_t softmax(logits_t)_e
-    over the V tokens that count (0 without any); counts int32 [E], constants of the gradient."""
+    over the V tokens that count (0 without any); counts int32 [E], constants of the gradient.  To capture its backward
+    pass into a graph, drop every eager autograd graph of the same leaves first, as torch asks for any backward pass."""
     _gpu_of("logits", logits, topk_ids, token_mask)
     _need(logits.dtype == torch.float32 and logits.dim() == 2, "logits: fp32 [T, E]")
     _need(logits.stride(1) == 1 or logits.shape[1] == 1, "logits' last dimension must be contiguous")
@@ -295,7 +296,8 @@ class PagedCache:
     def read(self, page_table, cu_rows, start=None, rows=None, k_out=None, v_out=None):
         """Reads rows back as bf16: (k [rows, heads, k_dim], v or None), rows and positions as in `write`.  Give
         `rows` (the outputs are allocated; rows outside every sequence are then undefined) or the outputs, whose
-        rows outside every sequence are left as they were.  Positions without a page read as zeros."""
+        rows outside every sequence are left as they were and whose vectors must not overlap.
+        Positions without a page read as zeros."""
         index = self._index(page_table, cu_rows, start)
         if k_out is None:
             _need(rows is not None and rows >= 0 and v_out is None, "give rows, or the outputs")
