@@ -323,8 +323,10 @@ enum {
  * (32 or 16), 32 <= K <= 2^20, 1 <= N <= 2^20.  global_scale host, positive and finite (NVFP4; MXFP4 ignores it).
  * bias [N] fp32 or bf16 or NULL.  x_bf16 device bf16 [M, ldx], ldx >= K, ldx % 8 == 0, 0 <= M <= 2^20.
  * y device [M, ldy], ldy >= N, bf16 or fp32 (out_is_fp32).
- * Arithmetic: a weight times its scale is exact in bf16 (at most six significant bits), the products
- * accumulate in fp32, the global scale divides and the bias is added in fp32, one rounding to bf16.
+ * Arithmetic: a weight times its scale is exact in bf16 (at most six significant bits) and the products
+ * accumulate in fp32, or (NVFP4, up to four rows) x times the codes of a block of 16 accumulates in fp32 and
+ * then takes the scale in fp32; the global scale divides and the bias is added in fp32, one rounding to bf16.
+ * Products of x and an NVFP4 code below 2^-117 may be lost.
  * Weights of 2^128 and more, or of less than 2^-126, are outside the contract.
  * Deterministic: repeated calls give the same bits (other numbers of rows may sum in another order).  The weights
  * are read once per 16 rows of x: for many rows mxfp4_linear_forward is the faster layer. */

@@ -5,11 +5,14 @@
 // matrices the chain of a launch, one load, one join.  So the weights are dequantized to bf16 in registers (exact: two
 // significant bits times a power of two, or times four bits) and multiplied on the matrix cores whatever the number of
 // rows, the waves of a workgroup share K and meet once, and nothing is set up or waited for before the first load of
-// weights but, in the expert form, the expert's number.  Measured (one pass, kernel alone):
-//   1 x 7168 x 7168           MXFP4  7.5 us (3.7 TB/s), NVFP4 10.2 us (2.8 TB/s: four instead of one instruction a pair)
-//   1 x 28672 x 7168          MXFP4 24 us (4.5 TB/s), NVFP4 25 us; loads of the same pieces alone 17.5 us
+// weights but, in the expert form, the expert's number.  NVFP4's dequantization takes four instructions a pair of weights
+// (MXFP4: one) and then bounds small numbers of rows: there the scale goes behind the matrix instruction (tile_sums_nv).
+// Measured (one pass, kernel alone):
+//   1 x 7168 x 7168           MXFP4  7.8 us (3.5 TB/s), NVFP4 9.6 us (3.0 TB/s)
+//   1 x 28672 x 7168          MXFP4 24 us (4.5 TB/s), NVFP4 25 us (4.6 TB/s); loads of the same pieces alone 17.5 us
 //   16 x 7168 x 2048          MXFP4  5.6 us; 16 x 7168 x 7168 10.5 us
-//   64 tokens, top-8 of 128   2048 x 768: MXFP4 29 us, NVFP4 33 us; 1536 x 2048 with SwiGLU 46 and 56 us (4.5, 3.9 TB/s)
+//   64 tokens, top-8 of 128   2048 x 768: MXFP4 29 us, NVFP4 33 us; 1536 x 2048 with SwiGLU 46 and 57 us (4.5, 3.9 TB/s)
+//   16 tokens, the latter     MXFP4 30 us, NVFP4 38 us
 // Tried and slower: scales a byte at a time beside the codes (a third of the time); x 16 bytes a row from memory (half of
 // the time at 16 rows); scales and x of the whole workgroup in LDS behind a barrier (7168 x 7168: 11 to 14 us); a ring or a
 // second set of registers for the next block (spills, or fewer waves: 12 to 18 us).
@@ -31,7 +34,7 @@ typedef unsigned u32x2_t __attribute__((ext_vector_type(2)));
 typedef u32x4_t u32x4_a8 __attribute__((aligned(8)));
 
 constexpr int kStep = 128;     // K elements of one step: 32 for each quarter of the wave
-constexpr int64_t kFull = 2048;      // waves that fill the chip (1 x 7168 x 7168 NVFP4: 10.2 us, with 6144 11.9 us)
+constexpr int64_t kFull = 2048;      // waves that fill the chip (1 x 7168 x 7168 NVFP4: 9.5 us, with 1024 and 4096 11.0, 11.4)
 constexpr int64_t kFullWide = 6144;  // waves of four tiles (1536 x 2048 with SwiGLU, NVFP4: 56 us, with 2048 60 us)
 constexpr int64_t kWide = 4096;      // tiles that are enough for a wave to take four of them
 template <int CTRL>
@@ -100,14 +103,13 @@ struct Tiles {
   uint32_t row[R];
 };
 
-// DW dwords from byte `at` on of `left` bytes (at < left), of which the first `n` are the row's own (n the same for the
-// whole wave); what lies past either reads as zeros: another row's scale may be one whose product with a code and a
-// zero is NaN.
+// DW dwords from byte `at` on of `left` bytes, of which the first `n` are the row's own (at < left where n > 0); what
+// lies past either reads as zeros: another row's scale may be one whose product with a code and a zero is NaN.
+// near_end: some lane has n < 4 DW.
 template <int DW>
-MX_DEV void load_bytes(const uint8_t* t, uint32_t at, int left, int n, uint32_t* v) {
+MX_DEV void load_bytes(const uint8_t* t, uint32_t at, int left, bool near_end, int n, uint32_t* v) {
   typedef unsigned vec_t __attribute__((ext_vector_type(DW)));
   typedef vec_t vec_a1 __attribute__((aligned(1)));
-  const bool near_end = n < 4 * DW;
   if (near_end && left < 4 * DW) {  // less than a load altogether
 #pragma unroll 1
     for (int i = 0; i < DW; i++) {
@@ -183,7 +185,7 @@ MX_DEV void tile_sums(const Tiles<R>& w, int K, int wave, int waves, RowX row_of
     }
 #pragma unroll
     for (int r = 0; r < R; r++) {
-      load_bytes<DW>(w.s[r], s_at[r] + k0 / kBlock<FMT>, w.s_left[r], (K - k0) / kBlock<FMT>, b.s[r]);
+      load_bytes<DW>(w.s[r], s_at[r] + k0 / kBlock<FMT>, w.s_left[r], near_end, (K - k0) / kBlock<FMT>, b.s[r]);
       if (!near_end) {
 #pragma unroll
         for (int i = 0; i < SB; i++) b.q[r][i] = load_codes<FMT>(w.q[r], q_at[r] + (k0 + k_lane) / 2 + i * (kStep / 2));
@@ -259,11 +261,140 @@ MX_DEV void tile_sums(const Tiles<R>& w, int K, int wave, int waves, RowX row_of
   }
 }
 
+// The same for NVFP4 weights and up to four rows of x, with the scales behind the matrix instruction: of a product's 16
+// columns, four belong to a row of x and hold one quarter of the wave's elements each (zeros for the others), so what
+// comes out of two instructions is a sum over the 16 elements of one block at a time, which takes its scale in binary32.
+// A lane then has 16 conversions, 8 multiply-adds and 8 scales (4 instructions) for its 32 elements of a step, where scaled
+// weights take 64 instructions.  1 x 7168 x 7168: 10.5 -> 9.6 us, 1 x 28672 x 7168: 28.6 -> 25 us; 1536 x 2048 with SwiGLU,
+// 16 tokens, top-8 of 128: 44 -> 38 us.  The same for 5 to 8 rows (two sets of columns) spilled: 2048 x 768, 64 tokens, 33 -> 40 us.
+// kDown on the codes keeps the sums below the scaled ones' (2^-9 is E4M3's least scale); the result takes it back.
+// LDS of the wave: rows of x, a row of zeros, the scales turned into the columns' layout.
+constexpr float kDown = 0x1p-9f;
+constexpr int nv_x_bytes(int xr, int sb) { return (xr + 1) * (sb * kStep + 8) * 2; }
+constexpr int nv_bytes(int R, int xr, int sb) { return nv_x_bytes(xr, sb) + R * sb * 128; }
+
+template <int R, int XR, int SB, typename RowX>
+MX_DEV void tile_sums_nv(const Tiles<R>& w, int K, int wave, int waves, RowX row_of, uint16_t* xs, float* part) {
+  constexpr int kB = SB * kStep, DW = SB / 2;
+  constexpr int PR = kB / 8, RPL = 64 / PR;
+  constexpr int XL = XR > RPL ? XR / RPL : 1;
+  constexpr int kPitch = kB + 8;
+  const int lane = threadIdx.x & 63, rc = lane & 15, quarter = lane >> 4, f = rc & 3;
+  const int k_lane = quarter * 32, k_x = lane % PR * 8;
+  const uint16_t* x[XL];
+#pragma unroll
+  for (int l = 0; l < XL; l++) x[l] = row_of(l * RPL + lane / PR);
+  uint16_t* xput = xs + lane / PR * kPitch + k_x;
+  uint16_t* zeros = xs + XR * kPitch;
+  if (lane * 8 < kB) *reinterpret_cast<u32x4_t*>(zeros + lane * 8) = u32x4_t{0, 0, 0, 0};
+  const uint16_t* xget = (quarter == f ? xs + (rc >> 2) % XR * kPitch : zeros) + k_lane;
+  // scales: [quarter of the elements][row][step], two bytes each
+  uint8_t* scales = (uint8_t*)xs + nv_x_bytes(XR, SB);
+  uint8_t* sput = scales + (SB == 4 ? rc * 8 + quarter * 2 : (quarter & 1) * 128 + rc * 4 + (quarter >> 1) * 2);
+  const uint8_t* sget = scales + f * (SB * 32) + quarter * (SB * 8);
+  uint32_t q_at[R], s_at[R];
+#pragma unroll
+  for (int r = 0; r < R; r++) {
+    q_at[r] = w.row[r] * (uint32_t)(K / 2);
+    s_at[r] = w.row[r] * (uint32_t)(K / 16) + quarter * (2 * SB);
+  }
+  f32x4_t acc[R] = {};
+  for (int k0 = wave * kB; k0 < K; k0 += waves * kB) {
+    const bool near_end = k0 + kB > K;
+    u32x4_t q[R][SB], xl[XL];
+    uint32_t s[R][DW];
+#pragma unroll
+    for (int l = 0; l < XL; l++) xl[l] = *reinterpret_cast<const u32x4_t*>(x[l] + (near_end ? min(k0 + k_x, K - 8) : k0 + k_x));
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+      load_bytes<DW>(w.s[r], s_at[r] + k0 / 16, w.s_left[r], near_end, (K - k0) / 16 - quarter * (2 * SB), s[r]);
+      if (!near_end) {
+#pragma unroll
+        for (int i = 0; i < SB; i++) q[r][i] = load_codes<MXFP4_FMT_NVFP4>(w.q[r], q_at[r] + (k0 + k_lane) / 2 + i * (kStep / 2));
+      } else {
+#pragma unroll
+        for (int i = 0; i < SB; i++)
+          q[r][i] = load_codes<MXFP4_FMT_NVFP4>(w.q[r], q_at[r] + min(k0 + i * kStep + k_lane, K - 32) / 2);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);  // the loads go out before anything waits for one
+#pragma unroll
+    for (int l = 0; l < XL; l++) {
+      if (near_end) {  // past K: zeros
+#pragma unroll
+        for (int i = 0; i < 4; i++) xl[l][i] = k0 + k_x < K ? xl[l][i] : 0;
+      }
+      if (XR >= RPL || lane / PR < XR) *reinterpret_cast<u32x4_t*>(xput + l * RPL * kPitch) = xl[l];
+    }
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+      // SB == 4: the lane has a step's four pairs of scales; SB == 2: half of a step's
+#pragma unroll
+      for (int h = 0; h < SB; h++)
+        *reinterpret_cast<uint16_t*>(sput + r * (SB * 128) + h * (SB == 4 ? 128 : 64)) = (uint16_t)(s[r][h / 2] >> (16 * (h & 1)));
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    uint32_t sc[R][4][DW];  // rows 4 * quarter + i: two bytes a step
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+#pragma unroll
+      for (int h = 0; h < DW; h++) {
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(sget + r * (SB * 128) + h * 16);
+#pragma unroll
+        for (int i = 0; i < 4; i++) sc[r][(h * 4 + i) / DW][(h * 4 + i) % DW] = v[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < SB; i++) {
+      bf16x8_t xv[4];
+#pragma unroll
+      for (int j = 0; j < 4; j++) xv[j] = *reinterpret_cast<const bf16x8_t*>(xget + i * kStep + j * 8);
+#pragma unroll
+      for (int r = 0; r < R; r++) {
+        settle<MXFP4_FMT_NVFP4>(q[r][i], k0 + i * kStep + k_lane, K);
+#pragma unroll
+        for (int h = 0; h < 2; h++) {  // the two blocks of the lane's 32 elements
+          f32x4_t t = {0, 0, 0, 0};
+#pragma unroll
+          for (int j = 2 * h; j < 2 * h + 2; j++)
+            t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dequant8<MXFP4_FMT_MXFP4>(q[r][i][j], kDown), xv[j], t, 0, 0, 0);
+#pragma unroll
+          for (int o = 0; o < 4; o++) {
+            const f32x2_t two = i % 2 ? __builtin_amdgcn_cvt_pk_f32_fp8((int)sc[r][o][i / 2], true)
+                                      : __builtin_amdgcn_cvt_pk_f32_fp8((int)sc[r][o][i / 2], false);
+            acc[r][o] = fmaf(t[o], two[h], acc[r][o]);
+          }
+        }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+#pragma unroll
+  for (int r = 0; r < R; r++) {
+    f32x4_t v = acc[r];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      v[i] += dpp<0xB1>(v[i]);  // lane ^ 1
+      v[i] += dpp<0x4E>(v[i]);  // lane ^ 2
+      v[i] *= 1.0f / kDown;
+    }
+    if (f == 0) *reinterpret_cast<f32x4_t*>(part + r * 256 + (rc >> 2) * 16 + quarter * 4) = v;
+  }
+}
+
 constexpr int kFew = 4;
 constexpr int kManySteps = 2;  // steps of a block for more rows: their x takes registers and LDS
-// LDS of a wave: its piece of x, then its sums.
-constexpr int wave_bytes(int R, int xr, int few_steps) {
-  const int few = (xr < kFew ? xr : kFew) * (few_steps * kStep + 8) * 2;
+// Where tile_sums_nv takes up to four rows.  Not beside the body for 16 rows with short blocks (64 tokens, top-8 of 128,
+// 2048 x 768: 33 us, with it 35 us), nor with four tiles (no faster).
+constexpr bool scales_behind(int fmt, int R, int xr, int sb) {
+  return fmt == MXFP4_FMT_NVFP4 && R < 4 && (xr <= kFew || sb == 4);
+}
+// LDS of a wave: its piece of x (and what tile_sums_nv adds), then its sums.
+constexpr int wave_bytes(int fmt, int R, int xr, int few_steps) {
+  const int f = xr < kFew ? xr : kFew;
+  const int few = scales_behind(fmt, R, xr, few_steps) ? nv_bytes(R, f, few_steps) : f * (few_steps * kStep + 8) * 2;
   const int many = xr > kFew ? xr * (kManySteps * kStep + 8) * 2 : 0;
   const int x = few > many ? few : many, sums = R * 1024;
   return x > sums ? x : sums;
@@ -278,7 +409,7 @@ constexpr int waves_a_simd(int R) { return R == 4 ? 3 : 4; }
 template <int FMT, bool EXPERT, bool SWIGLU, int XR, int R, int SB>
 __global__ __launch_bounds__(XR > kFew ? 512 : 1024, waves_a_simd(R)) void matvec_kernel(MatvecArgs a) {
   constexpr int OT = SWIGLU ? R / 2 : R;  // tiles of outputs
-  constexpr int kWave = wave_bytes(R, XR, SB);
+  constexpr int kWave = wave_bytes(FMT, R, XR, SB);
   extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
@@ -336,7 +467,11 @@ __global__ __launch_bounds__(XR > kFew ? 512 : 1024, waves_a_simd(R)) void matve
     };
     uint16_t* xs = (uint16_t*)mine;
     float* part = (float*)mine;
-    if (R < 4 && (XR == 1 || (EXPERT && cols == 1)))
+    if (scales_behind(FMT, R, XR, SB) && (XR == 1 || (EXPERT && cols == 1)))
+      tile_sums_nv<R, 1, SB>(w, K, wave, waves, row_of, xs, part);
+    else if (scales_behind(FMT, R, XR, SB) && (XR == 4 || cols <= kFew))
+      tile_sums_nv<R, 4, SB>(w, K, wave, waves, row_of, xs, part);
+    else if (R < 4 && (XR == 1 || (EXPERT && cols == 1)))
       tile_sums<FMT, R, 1, SB, true>(w, K, wave, waves, row_of, xs, part);
     else if (R < 4 && (XR == 4 || cols <= kFew))
       tile_sums<FMT, R, 4, SB, true>(w, K, wave, waves, row_of, xs, part);
@@ -391,7 +526,7 @@ int launch_rows(const MatvecArgs& a, hipStream_t stream) {
   int waves = (int)((blocks + each - 1) / each);
   if (waves > 1 && (waves - blocks % waves) % waves * 2 >= waves) waves--;
   const dim3 grid((unsigned)tiles, (unsigned)(groups < 65535 ? groups : 65535));
-  const int lds = waves * wave_bytes(R, XR, SB);
+  const int lds = waves * wave_bytes(FMT, R, XR, SB);
   hipLaunchKernelGGL((matvec_kernel<FMT, EXPERT, SWIGLU, XR, R, SB>), grid, dim3(64 * waves), lds, stream, a);
   return hipGetLastError() == hipSuccess ? MXFP4_OK : MXFP4_ERR_DEVICE;
 }

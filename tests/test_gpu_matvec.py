@@ -3,7 +3,8 @@
 Tolerance, from the arithmetic (u = 2^-24).  Weights times their scales are exact in bf16 and so are the products
 in binary32; an output is a sum of K products, of which at most 32 inside one matrix instruction, then K / 128
 accumulations in sequence and 16 partial sums add a rounding each (counted twice, whichever way the matrix unit
-rounds): 2 (K / 128 + 48) u of sum |x W|.  The global scale's division and the bias add 2 u each of what they give, and
+rounds): 2 (K / 128 + 48) u of sum |x W|.  (Few rows of x with NVFP4 weights: two matrix instructions sum a block of 16, and
+2 K / 128 multiply-adds with its scale follow, one rounding each: the same bound.)  The global scale's division and the bias add 2 u each of what they give, and
 the result is rounded once: 2^-9 of itself to bf16 and half an ulp (2^-8 bounds it at every place of a binade) or u.
 SwiGLU: silu has a slope of at most 1.1, its own evaluation errs by (|g| + 8) u.
 """
@@ -72,6 +73,16 @@ def dense(M, N, K, fmt, bias, out=torch.bfloat16, pad=0, seed=0):
     assert_dense(y, x, q, s, gs, b, out)
     assert torch.equal(y, mx.fp4_matvec(xd, qd, sd, bt, fmt=FMTS[fmt], global_scale=gs, out_dtype=out))
     return xd, qd, sd, gs, y
+
+
+@pytest.mark.parametrize("fmt", list(FMTS))
+@pytest.mark.parametrize("M", [1, 4, 8, 16])
+def test_large_and_small_rows_scale_exactly(fmt, M):
+    """A power of two on x is one on y: nothing on the way overflows or goes below binary32's normal range."""
+    xd, qd, sd, gs, y = dense(M, 37, 1040 if fmt == "nvfp4" else 1056, fmt, None, torch.float32, seed=5)
+    for e in (100, -90):
+        z = mx.fp4_matvec((xd.float() * 2.0 ** e).bfloat16(), qd, sd, fmt=FMTS[fmt], global_scale=gs, out_dtype=torch.float32)
+        assert torch.equal(z.double(), y.double() * 2.0 ** e)
 
 
 # rows below, at and past a tile of 16; outputs that fill no tile; K of one block, below a step, ragged, long
