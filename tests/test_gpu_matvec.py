@@ -253,6 +253,15 @@ def test_experts(fmt, T, E, k, N, K, swiglu, shared, bias):
     expert(T, E, k, N, K, fmt, swiglu, shared, bias)
 
 
+# blocks of four steps, with one to four rows an expert, more than a tile, and sixteen waves
+@pytest.mark.parametrize("fmt", list(FMTS))
+@pytest.mark.parametrize("T,E,k,N,K,swiglu,shared,bias", [
+    (1, 6, 1, 34, 512, True, True, True), (1, 6, 2, 34, 8224, True, True, False), (2, 5, 2, 20, 8224, False, False, True),
+    (7, 6, 3, 40, 2048, True, True, True), (9, 20, 4, 33, 1056, False, True, True), (45, 5, 2, 38, 1024, True, False, True)])
+def test_experts_with_long_rows(fmt, T, E, k, N, K, swiglu, shared, bias):
+    expert(T, E, k, N, K, fmt, swiglu, shared, bias, torch.float32 if T == 1 else torch.bfloat16)
+
+
 @pytest.mark.parametrize("fmt", list(FMTS))
 def test_more_pairs_than_a_tile_on_one_expert(fmt):
     expert(37, 9, 2, 40, 128, fmt, True, True, True, torch.float32, 1, crowd=True)
