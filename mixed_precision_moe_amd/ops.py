@@ -63,6 +63,18 @@ def _row_step(t):
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
+def _check_logits(logits):
+    _need(logits.dtype == torch.float32 and logits.dim() == 2, "logits: fp32 [T, E]")
+    T, E = logits.shape
+    _need(logits.stride(1) == 1 or E == 1, "logits' last dimension must be contiguous")
+    _need(T <= 1 or logits.stride(0) >= E, "logits' rows must not overlap")
+
+
+def _check_mask(mask, T):
+    _need(mask.dtype in (torch.bool, torch.uint8) and mask.shape == (T,) and mask.is_contiguous(),
+          "token_mask: contiguous bool or uint8 [T]")
+
+
 class _BalanceLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, topk_ids, mask):
@@ -76,11 +88,10 @@ class _BalanceLoss(torch.autograd.Function):
         loss = torch.empty((), dtype=torch.float32, device=dev)
         counts = torch.empty(E, dtype=torch.int32, device=dev)
         ws = buf.data_ptr()
-        step = _row_step(logits)
-        _call(index, "moe_balance_forward", logits.data_ptr(), T, E, step, topk_ids.data_ptr(), topk_ids.shape[1], _ptr(mask),
-              loss.data_ptr(), counts.data_ptr(), ws + nws, ws, nws)
+        _call(index, "moe_balance_forward", logits.data_ptr(), T, E, _row_step(logits), topk_ids.data_ptr(),
+              topk_ids.shape[1], _ptr(mask), loss.data_ptr(), counts.data_ptr(), ws + nws, ws, nws)
         ctx.save_for_backward(logits, buf, mask)
-        ctx.coef, ctx.step = nws, step
+        ctx.coef, ctx.shape = nws, (T, E)
         ctx.mark_non_differentiable(counts)
         ctx.set_materialize_grads(False)
         return loss, counts
@@ -91,10 +102,17 @@ class _BalanceLoss(torch.autograd.Function):
             raise RuntimeError("balance_loss has no second derivative (create_graph)")
         if g is None:
             return None, None, None
+        # saved-tensor hooks may return others than were saved: with other strides, which the kernel can take, or unfit
         logits, buf, mask = ctx.saved_tensors
-        T, E = logits.shape
+        T, E = ctx.shape
+        index = _gpu_of("logits", logits, buf, mask, g)
+        _check_logits(logits)
+        _need(logits.shape == ctx.shape and buf.dtype == torch.uint8 and buf.shape == (ctx.coef + 4 * E,) and
+              buf.is_contiguous(), "the tensors saved for the backward pass have changed")
+        if mask is not None:
+            _check_mask(mask, T)
         grad = torch.empty((T, E), dtype=torch.float32, device=logits.device)
-        _call(logits.get_device(), "moe_balance_backward", logits.data_ptr(), T, E, ctx.step, _ptr(mask),
+        _call(index, "moe_balance_backward", logits.data_ptr(), T, E, _row_step(logits), _ptr(mask),
               buf.data_ptr() + ctx.coef, g.data_ptr(), grad.data_ptr())
         return grad, None, None
 
@@ -108,15 +126,12 @@ def balance_loss(logits, topk_ids, token_mask=None):
     over the V tokens that count (0 without any); counts int32 [E], constants of the gradient.  To capture its backward
     pass into a graph, drop every eager autograd graph of the same leaves first, as torch asks for any backward pass."""
     _gpu_of("logits", logits, topk_ids, token_mask)
-    _need(logits.dtype == torch.float32 and logits.dim() == 2, "logits: fp32 [T, E]")
-    _need(logits.stride(1) == 1 or logits.shape[1] == 1, "logits' last dimension must be contiguous")
-    T, E = logits.shape
-    _need(T <= 1 or logits.stride(0) >= E, "logits' rows must not overlap")
+    _check_logits(logits)
+    T = logits.shape[0]
     _need(topk_ids.dtype == torch.int32 and topk_ids.dim() == 2 and topk_ids.shape[0] == T and topk_ids.is_contiguous(),
           "topk_ids: contiguous int32 [T, k]")
     if token_mask is not None:
-        _need(token_mask.dtype in (torch.bool, torch.uint8) and token_mask.shape == (T,) and token_mask.is_contiguous(),
-              "token_mask: contiguous bool or uint8 [T]")
+        _check_mask(token_mask, T)
     return _BalanceLoss.apply(logits, topk_ids, token_mask)
 
 

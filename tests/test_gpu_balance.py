@@ -167,6 +167,19 @@ def test_strided_and_misaligned_rows(T, E, off, pad):
     assert_close(loss, counts, grad, l, ids, mask, 0.01)
 
 
+@pytest.mark.parametrize("T,E,off,pad", [(8, 4, 0, 12), (70, 32, 1, 8), (600, 64, 0, 64)])
+def test_strided_rows_under_saved_tensor_hooks(T, E, off, pad):
+    """The rows come back from the host without the space between them."""
+    l, ids, mask = case(T, E, 3, 9, True)
+    buf = torch.full((T, off + E + pad), float("nan"), device="cuda")
+    buf[:, off:off + E] = torch.from_numpy(l).cuda()
+    view = buf[:, off:off + E].detach().requires_grad_()
+    with torch.autograd.graph.save_on_cpu():
+        loss, counts = mx.balance_loss(view, torch.from_numpy(ids).cuda(), torch.from_numpy(mask).cuda())
+    grad, = torch.autograd.grad(loss, view, torch.tensor(0.01, device="cuda"))
+    assert_close(loss, counts, grad, l, ids, mask, 0.01)
+
+
 def test_gradient_against_differences():
     """Central differences of the device's own loss, h = 2^-5: the curvature term h^2/6 |f'''| is below 2^-10 of the
     bound p D on the gradient, the loss's rounding 2^-24 f / h is the other allowance."""
