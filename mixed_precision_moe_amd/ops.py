@@ -3,6 +3,7 @@ their C entry points.  Like the rest of the binding it checks dtypes, shapes and
 outputs and passes raw pointers; the work runs on the current stream of the tensors' device."""
 
 import ctypes
+import functools
 
 import torch
 
@@ -58,16 +59,19 @@ def _call(index, fn, *args):
 # Balance loss.
 
 
-def _row_step(t):
-    """Elements from row to row; the stride of a single row says nothing."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
 def _check_logits(logits):
-    _need(logits.dtype == torch.float32 and logits.dim() == 2, "logits: fp32 [T, E]")
+    """(tokens, experts, elements from row to row; the stride of a single row says nothing)."""
+    if logits.dtype != torch.float32 or logits.dim() != 2:
+        raise ValueError("logits: fp32 [T, E]")
     T, E = logits.shape
-    _need(logits.stride(1) == 1 or E == 1, "logits' last dimension must be contiguous")
-    _need(T <= 1 or logits.stride(0) >= E, "logits' rows must not overlap")
+    step, unit = logits.stride()
+    if unit != 1 and E > 1:
+        raise ValueError("logits' last dimension must be contiguous")
+    if T <= 1:
+        return T, E, E
+    if step < E:
+        raise ValueError("logits' rows must not overlap")
+    return T, E, step
 
 
 def _check_mask(mask, T):
@@ -75,23 +79,27 @@ def _check_mask(mask, T):
           "token_mask: contiguous bool or uint8 [T]")
 
 
+@functools.lru_cache(maxsize=256)
+def _balance_workspace(T, E):
+    return _lib.lib().moe_balance_workspace_bytes(T, E)
+
+
 class _BalanceLoss(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, topk_ids, mask):
-        T, E = logits.shape
+    def forward(ctx, logits, topk_ids, mask, T, E, step):
         dev, index = logits.device, logits.get_device()
-        nws = _lib.lib().moe_balance_workspace_bytes(T, E)
+        nws = _balance_workspace(T, E)
         if nws == 0:
             raise ValueError("invalid balance loss arguments")
-        # d_e for the backward pass lies behind the workspace, whose size is a multiple of 256
-        buf = torch.empty(nws + 4 * E, dtype=torch.uint8, device=dev)
+        ws = torch.empty(nws, dtype=torch.uint8, device=dev)
+        coef = torch.empty(E, dtype=torch.float32, device=dev)
         loss = torch.empty((), dtype=torch.float32, device=dev)
         counts = torch.empty(E, dtype=torch.int32, device=dev)
-        ws = buf.data_ptr()
-        _call(index, "moe_balance_forward", logits.data_ptr(), T, E, _row_step(logits), topk_ids.data_ptr(),
-              topk_ids.shape[1], _ptr(mask), loss.data_ptr(), counts.data_ptr(), ws + nws, ws, nws)
-        ctx.save_for_backward(logits, buf, mask)
-        ctx.coef, ctx.shape = nws, (T, E)
+        _call(index, "moe_balance_forward", logits.data_ptr(), T, E, step, topk_ids.data_ptr(), topk_ids.shape[1],
+              _ptr(mask), loss.data_ptr(), counts.data_ptr(), coef.data_ptr(), ws.data_ptr(), nws)
+        ctx.save_for_backward(logits, mask)
+        # d_e, which is neither an input nor an output and which saved-tensor hooks therefore need not see
+        ctx.coef, ctx.sizes, ctx.index = coef, (T, E), index
         ctx.mark_non_differentiable(counts)
         ctx.set_materialize_grads(False)
         return loss, counts
@@ -101,20 +109,19 @@ class _BalanceLoss(torch.autograd.Function):
         if torch.is_grad_enabled():
             raise RuntimeError("balance_loss has no second derivative (create_graph)")
         if g is None:
-            return None, None, None
+            return None, None, None, None, None, None
         # saved-tensor hooks may return others than were saved: with other strides, which the kernel can take, or unfit
-        logits, buf, mask = ctx.saved_tensors
-        T, E = ctx.shape
-        index = _gpu_of("logits", logits, buf, mask, g)
-        _check_logits(logits)
-        _need(logits.shape == ctx.shape and buf.dtype == torch.uint8 and buf.shape == (ctx.coef + 4 * E,) and
-              buf.is_contiguous(), "the tensors saved for the backward pass have changed")
+        logits, mask = ctx.saved_tensors
+        T, E, step = _check_logits(logits)
+        index = ctx.index
+        if (T, E) != ctx.sizes or logits.get_device() != index or mask is not None and mask.get_device() != index:
+            raise ValueError("the tensors saved for the backward pass have changed")
         if mask is not None:
             _check_mask(mask, T)
         grad = torch.empty((T, E), dtype=torch.float32, device=logits.device)
-        _call(index, "moe_balance_backward", logits.data_ptr(), T, E, _row_step(logits), _ptr(mask),
-              buf.data_ptr() + ctx.coef, g.data_ptr(), grad.data_ptr())
-        return grad, None, None
+        _call(index, "moe_balance_backward", logits.data_ptr(), T, E, step, _ptr(mask), ctx.coef.data_ptr(), g.data_ptr(),
+              grad.data_ptr())
+        return grad, None, None, None, None, None
 
 
 def balance_loss(logits, topk_ids, token_mask=None):
@@ -126,13 +133,12 @@ def balance_loss(logits, topk_ids, token_mask=None):
     over the V tokens that count (0 without any); counts int32 [E], constants of the gradient.  To capture its backward
     pass into a graph, drop every eager autograd graph of the same leaves first, as torch asks for any backward pass."""
     _gpu_of("logits", logits, topk_ids, token_mask)
-    _check_logits(logits)
-    T = logits.shape[0]
+    T, E, step = _check_logits(logits)
     _need(topk_ids.dtype == torch.int32 and topk_ids.dim() == 2 and topk_ids.shape[0] == T and topk_ids.is_contiguous(),
           "topk_ids: contiguous int32 [T, k]")
     if token_mask is not None:
         _check_mask(token_mask, T)
-    return _BalanceLoss.apply(logits, topk_ids, token_mask)
+    return _BalanceLoss.apply(logits, topk_ids, token_mask, T, E, step)
 
 
 # ------------------------------------------------------------------------------------------------

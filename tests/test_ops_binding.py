@@ -61,3 +61,17 @@ def test_backward_refuses_other_tensors_than_were_saved(calls, change):
     with pytest.raises((ValueError, RuntimeError)):
         torch.autograd.grad(loss, logits)
     assert not calls
+
+
+@pytest.mark.parametrize("T,E", [(8, 4), (5000, 96), (3000, 1024)])
+def test_only_the_rows_the_mask_and_d_live_until_the_backward_pass(calls, T, E):
+    kept = []
+
+    def pack(t):
+        kept.append(t)
+        return t
+
+    with saved(pack, lambda t: t):
+        _, loss = balance(T, E, mask=True)
+    kept += [t for t in vars(loss.grad_fn).values() if torch.is_tensor(t)]
+    assert {t.untyped_storage().nbytes() for t in kept} <= {4 * T * (E + 12), T, 4 * E}
