@@ -419,12 +419,13 @@ __global__ __launch_bounds__(XR > kFew ? 512 : 1024, waves_a_simd(R)) void matve
   int64_t e = 0, first = 0, count = a.M;
   if (EXPERT) {
     e = blockIdx.y;
-    if (gridDim.y < (unsigned)a.E) {  // fewer pairs than experts: the blockIdx.y-th expert that has any
+    if (gridDim.y < (unsigned)a.E) {  // fewer pairs than experts: the blockIdx.y-th expert that has any, once clamped
+      const int pairs = (int)a.M;  // < E
       int seen = 0;
       e = -1;
       for (int base = 0; base < a.E && e < 0; base += 64) {
         const int i = base + lane;
-        const bool has = i < a.E && a.offsets[i + 1] > a.offsets[i];
+        const bool has = i < a.E && min(a.offsets[i + 1], pairs) > max(a.offsets[i], 0);
         uint64_t m = __ballot(has);
         const int n = __popcll(m);
         if (seen + n > (int)blockIdx.y) {

@@ -303,6 +303,23 @@ def test_bad_offsets_and_pairs_stay_inside():
     assert bool((mx.fp4_expert_matvec(*args[:3], none, sp, **kw, y=torch.full_like(y, 7.0)) == 7.0).all())
 
 
+@pytest.mark.parametrize("fmt", list(FMTS))
+def test_offsets_outside_the_pairs_with_fewer_pairs_than_experts(fmt):
+    """An expert is one of those that have pairs by its clamped offsets, not by the offsets as given."""
+    E, N, K, P = 70, 24, 64, 3
+    g = synth.rng(317)
+    q, s, _ = weights(g, (E, N, K), fmt)
+    x = synth.to_bf16_bits(g.standard_normal((P, K), dtype=np.float32))
+    args = bf16_dev(x), torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda()
+    kw = {"fmt": FMTS[fmt], "global_scales": torch.ones(E, device="cuda") if fmt == "nvfp4" else None}
+    sp = torch.tensor([1, 2, 0], dtype=torch.int32, device="cuda")
+    for good, bad in (([0] * 60 + [1] + [3] * 10, list(range(-60, 0)) + [1] + [3] * 10),
+                      ([0] * 4 + [2, 3] + [3] * 65, [-9, -7, -7, 0, 2] + list(range(50, 116)))):
+        y, z = (mx.fp4_expert_matvec(*args, torch.tensor(o, dtype=torch.int32, device="cuda"), sp, **kw,
+                                     y=torch.full((P, N), 7.0, device="cuda")) for o in (good, bad))
+        assert not (y == 7.0).all(1).any() and torch.equal(y, z)
+
+
 def test_long_rows_and_many_rows():
     """K past the blocks that one round of waves takes; more rows of x than a grid has places for."""
     dense(2, 3, 1 << 18, "mxfp4", None, torch.float32, seed=6)
