@@ -248,14 +248,15 @@ class PagedCache:
 
     A token has `heads` vectors of k_dim (and v_dim; None: k_dim) elements; page_size tokens make a page.
     The memory is four uint8 tensors k_q, k_s, v_q, v_s (codes [num_pages, page_size, heads, dim/2], MXFP8: dim;
-    scales [num_pages, page_size, heads, dim/32], NVFP4: dim/16), allocated as zeros or given as `storage`."""
+    scales [num_pages, page_size, heads, dim/32], NVFP4: dim/16), allocated as zeros or given as `storage`.  They and
+    `dims` (a copy of the sizes) cannot be rebound; another memory is another PagedCache."""
 
     def __init__(self, num_pages, page_size, heads, k_dim, v_dim=None, fmt=FMT_MXFP8, k_global_scale=1.0,
                  v_global_scale=1.0, storage=None, device=None):
         v_dim = k_dim if v_dim is None else v_dim
-        self.dims = CacheDims(fmt, heads, k_dim, v_dim, page_size, num_pages, k_global_scale, v_global_scale)
+        self._dims = CacheDims(fmt, heads, k_dim, v_dim, page_size, num_pages, k_global_scale, v_global_scale)
         sizes = (ctypes.c_size_t * 4)()
-        check("mxfp4_cache_bytes", _lib.lib().mxfp4_cache_bytes(ctypes.byref(self.dims), sizes))
+        check("mxfp4_cache_bytes", _lib.lib().mxfp4_cache_bytes(ctypes.byref(self._dims), sizes))
         per = 1 if fmt == FMT_MXFP8 else 2
         shapes = [(num_pages, page_size, heads, d // by) for d in (k_dim, v_dim) for by in (per, _GROUP[fmt])]
         if storage is None:
@@ -268,12 +269,25 @@ class PagedCache:
                 continue
             _need(t is not None and t.dtype == torch.uint8 and t.shape == s and t.is_contiguous(),
                   f"{n}: contiguous uint8 {list(s)}")
-        self.k_q, self.k_s, self.v_q, self.v_s = storage
+        self._storage = k_q, *_ = tuple(storage)
         self._gpu = _gpu_of("k_q", *storage)
-        self._device = self.k_q.device
+        self._device = k_q.device
         self._heads, self._k_dim, self._v_dim = heads, k_dim, v_dim
-        self._dref = ctypes.byref(self.dims)
-        self._memory = tuple(_ptr(t) for t in storage)
+        self._dref = ctypes.byref(self._dims)
+
+    # what the kernels' bounds were checked against: read only
+    dims = property(lambda self: CacheDims.from_buffer_copy(self._dims))
+    k_q = property(lambda self: self._storage[0])
+    k_s = property(lambda self: self._storage[1])
+    v_q = property(lambda self: self._storage[2])
+    v_s = property(lambda self: self._storage[3])
+
+    def _memory(self):
+        """The tensors' addresses now: their memory may have moved since the last call."""
+        k_q, k_s, v_q, v_s = self._storage
+        if v_q is None:
+            return k_q.data_ptr(), k_s.data_ptr(), None, None
+        return k_q.data_ptr(), k_s.data_ptr(), v_q.data_ptr(), v_s.data_ptr()
 
     def _index(self, page_table, cu_rows, start):
         if page_table.dtype != torch.int32 or page_table.dim() != 2 or cu_rows.dtype != torch.int32:
@@ -309,10 +323,10 @@ class PagedCache:
         position i lives in page page_table[b, i // page_size].  Rows outside every sequence, and positions without
         a page (past the table, or a page number outside the cache), are passed over.  Two rows of one call must not
         share a slot."""
-        _gpu_of("the cache", self.k_q, k, v, page_table, cu_rows, start)
+        _gpu_of("the cache", self._storage[0], k, v, page_table, cu_rows, start)
         index = self._index(page_table, cu_rows, start)
         planes = self._planes(k, v)
-        _call(self._gpu, "mxfp4_cache_write", self._dref, *planes, k.shape[0], *index, *self._memory)
+        _call(self._gpu, "mxfp4_cache_write", self._dref, *planes, k.shape[0], *index, *self._memory())
 
     def read(self, page_table, cu_rows, start=None, rows=None, k_out=None, v_out=None):
         """Reads rows back as bf16: (k [rows, heads, k_dim], v or None), rows and positions as in `write`.  Give
@@ -325,8 +339,8 @@ class PagedCache:
             k_out = torch.empty((rows, self._heads, self._k_dim), dtype=torch.bfloat16, device=self._device)
             if self._v_dim:
                 v_out = torch.empty((rows, self._heads, self._v_dim), dtype=torch.bfloat16, device=self._device)
-        _gpu_of("the cache", self.k_q, k_out, v_out, page_table, cu_rows, start)
+        _gpu_of("the cache", self._storage[0], k_out, v_out, page_table, cu_rows, start)
         planes = self._planes(k_out, v_out)
         _need(rows is None or rows == k_out.shape[0], "rows must be the outputs' rows")
-        _call(self._gpu, "mxfp4_cache_read", self._dref, *self._memory, k_out.shape[0], *index, *planes)
+        _call(self._gpu, "mxfp4_cache_read", self._dref, *self._memory(), k_out.shape[0], *index, *planes)
         return k_out, v_out

@@ -75,3 +75,51 @@ def test_only_the_rows_the_mask_and_d_live_until_the_backward_pass(calls, T, E):
         _, loss = balance(T, E, mask=True)
     kept += [t for t in vars(loss.grad_fn).values() if torch.is_tensor(t)]
     assert {t.untyped_storage().nbytes() for t in kept} <= {4 * T * (E + 12), T, 4 * E}
+
+
+def cache(v_dim=32):
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+    store = [u8(4, 8, 2, 32), u8(4, 8, 2, 2), u8(4, 8, 2, 16), u8(4, 8, 2, 1)]
+    return mx.PagedCache(4, 8, 2, 64, v_dim, mx.FMT_MXFP4, storage=store if v_dim else store[:2] + [None, None])
+
+
+def write_and_read(c, calls):
+    """The cache's four addresses as the write and the read got them."""
+    k, v = torch.zeros(3, 2, 64, dtype=torch.bfloat16), torch.zeros(3, 2, 32, dtype=torch.bfloat16)
+    v = v if c.v_q is not None else None
+    table, cu = torch.zeros(1, 1, dtype=torch.int32), torch.tensor([0, 3], dtype=torch.int32)
+    c.write(k, v, table, cu)
+    c.read(table, cu, k_out=k, v_out=v)
+    (fw, w), (fr, r) = calls[-2:]
+    assert (fw, fr) == ("mxfp4_cache_write", "mxfp4_cache_read") and w[0]._obj.num_pages == r[0]._obj.num_pages == 4
+    assert w[-4:] == r[1:5]
+    return w[-4:]
+
+
+@pytest.mark.parametrize("v_dim", [32, 0])
+def test_the_caches_memory_and_sizes_are_not_replaced(calls, v_dim):
+    c = cache(v_dim)
+    names = ("k_q", "k_s", "v_q", "v_s")
+    for name in names:
+        with pytest.raises(AttributeError):
+            setattr(c, name, torch.zeros(1, 8, 2, 32, dtype=torch.uint8))
+    with pytest.raises(AttributeError):
+        c.dims = None
+    c.dims.num_pages = 1 << 20  # of a copy
+    c.dims.page_size = 1 << 10
+    assert (c.dims.num_pages, c.dims.page_size) == (4, 8)
+    assert write_and_read(c, calls) == tuple(t if t is None else t.data_ptr() for t in (getattr(c, n) for n in names))
+
+
+def test_the_caches_addresses_are_those_at_the_call(calls):
+    """Memory that moves under its tensors: given back and taken again, as an offloaded cache's is."""
+    c = cache()
+    old = write_and_read(c, calls)
+    c.k_q.untyped_storage().resize_(0)
+    assert write_and_read(c, calls)[0] == 0
+    held = torch.empty(c.k_q.numel(), dtype=torch.uint8)  # what was free is likely to be here
+    c.k_q.untyped_storage().resize_(c.k_q.numel())
+    c.v_s.set_(torch.ones_like(c.v_s))
+    new = write_and_read(c, calls)
+    assert new == tuple(t.data_ptr() for t in (c.k_q, c.k_s, c.v_q, c.v_s)) and new[0] != held.data_ptr()
+    assert new[1:3] == old[1:3]
