@@ -92,8 +92,7 @@ class _BalanceLoss(torch.autograd.Function):
         if nws == 0:
             raise ValueError("invalid balance loss arguments")
         ws = torch.empty(nws, dtype=torch.uint8, device=dev)
-        coef = torch.empty(E, dtype=torch.float32, device=dev)
-        loss = torch.empty((), dtype=torch.float32, device=dev)
+        coef, loss = logits.new_empty(E), logits.new_empty(())
         counts = torch.empty(E, dtype=torch.int32, device=dev)
         _call(index, "moe_balance_forward", logits.data_ptr(), T, E, step, topk_ids.data_ptr(), topk_ids.shape[1],
               _ptr(mask), loss.data_ptr(), counts.data_ptr(), coef.data_ptr(), ws.data_ptr(), nws)
@@ -118,7 +117,7 @@ class _BalanceLoss(torch.autograd.Function):
             raise ValueError("the tensors saved for the backward pass have changed")
         if mask is not None:
             _check_mask(mask, T)
-        grad = torch.empty((T, E), dtype=torch.float32, device=logits.device)
+        grad = logits.new_empty((T, E))
         _call(index, "moe_balance_backward", logits.data_ptr(), T, E, step, _ptr(mask), ctx.coef.data_ptr(), g.data_ptr(),
               grad.data_ptr())
         return grad, None, None, None, None, None
