@@ -367,7 +367,8 @@ int fp4_expert_matvec(int32_t fmt, const void* w_q, const void* w_s, const float
  * The write quantizes each block of each row: MXFP4 and NVFP4 bit for bit as mxfp4_quantize and
  * nvfp4_quantize, MXFP8 as MXFP4_ACT_MXFP8 quantizes activations.  Two rows of one call must not share a
  * slot: what such a slot then holds is not specified.  The read returns code * scale, rounded once to bf16
- * (NVFP4: the scale divided by the plane's global scale and multiplied by the code in binary32, then rounded).
+ * (NVFP4: the scale divided by the plane's global scale and multiplied by the code in binary32, then rounded; where
+ * the quotient alone would overflow, codes whose value does not still have it).
  * k / v device bf16, element (row, head, i) at row * ldt + head * ldh + i; ldt, ldh multiples of 8, ldh >= dim,
  * ldt >= dim; the vectors that the read writes must not overlap.  heads * dim <= 2^20.  Neither call uses a
  * workspace.  The cache's pointers may be NULL when num_pages is 0, the table when max_pages is 0. */

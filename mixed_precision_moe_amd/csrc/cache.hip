@@ -108,13 +108,17 @@ MX_DEV u32x4_t decode(const uint32_t* q, uint32_t s, float gs) {
     o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[1], sc, false));
     o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[1], sc, true));
   } else {
-    // one division a block: scale / global scale, rounded to binary32, times the code
-    const float f = __builtin_amdgcn_cvt_f32_fp8((int)s, 0) / gs;
+    // one division a block: scale / global scale, rounded to binary32, times the code.  Under a small global scale the
+    // quotient may be past binary32's range where its product with a code of 0 or 1/2 is not: 2^-30 keeps it inside
+    // (448 * 2^-30 over the smallest number is below 2^128), and the code takes it back.
+    const bool small = gs < 1.0f;
+    const float up = small ? 0x1p30f : 1.0f;
+    const float f = __builtin_amdgcn_cvt_f32_fp8((int)s, 0) * (small ? 0x1p-30f : 1.0f) / gs;
     auto two = [&](auto v) { return bf16_pair(f32x2_t{v[0] * f, v[1] * f}); };
-    o[0] = two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[0], 1.0f, 0));
-    o[1] = two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[0], 1.0f, 1));
-    o[2] = two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[0], 1.0f, 2));
-    o[3] = two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[0], 1.0f, 3));
+    o[0] = two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[0], up, 0));
+    o[1] = two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[0], up, 1));
+    o[2] = two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[0], up, 2));
+    o[3] = two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[0], up, 3));
   }
   return o;
 }

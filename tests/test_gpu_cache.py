@@ -210,6 +210,45 @@ def test_windows_and_wide_tables():
     np.testing.assert_array_equal(got, host.read(0, C.slots_ref(5, [0, 3, 5], [-2, 4 * table.shape[1] - 1], table, 4, c.dims.num_pages), 0))
 
 
+def all_nvfp4_values(gs):
+    """A one-plane NVFP4 cache of every code under every finite scale, and its values in float64."""
+    s = np.arange(254, dtype=np.uint8)
+    s[127:] += 1  # 0x7F and 0xFF are NaN
+    q = np.tile(np.arange(16, dtype=np.uint8).reshape(8, 2) @ np.array([1, 16], np.uint8), (254, 1))
+    store = [torch.from_numpy(t.reshape(2, 127, 1, -1)).cuda() for t in (q, s)]
+    c = mx.PagedCache(2, 127, 1, 16, 0, mx.FMT_NVFP4, gs, storage=(*store, None, None))
+    code = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6, -0.0, -0.5, -1, -1.5, -2, -3, -4, -6])
+    m, e = np.minimum(s & 127, 126), (s & 127) >> 3
+    scale = np.where(e > 0, np.ldexp(8.0 + m % 8, e.astype(int) - 10), np.ldexp(m % 8.0, -9)) * np.where(s & 128, -1, 1)
+    with np.errstate(over="ignore"):
+        v = code[None, :] * scale[:, None] / float(np.float32(gs))
+    k, _ = c.read(i32([[0, 1]]), i32([0, 254]), rows=254)
+    return k.view(254, 16).double().cpu().numpy(), v
+
+
+@pytest.mark.parametrize("k", [-149, -140, -126, -120, -1, 0, 60, 100, 118, 120, 127])
+def test_nvfp4_values_under_a_power_of_two(k):
+    """A power of two as global scale moves the exponent and nothing else (values have six bits), also one under which a
+    scale alone would overflow; past bf16's range there are infinities, below it the steps of 2^-133."""
+    got, v = all_nvfp4_values(2.0 ** k)
+    with np.errstate(over="ignore"):
+        want = np.where(np.abs(v) >= 2.0 ** 128, np.copysign(np.inf, v), np.where(np.abs(v) < 2.0 ** -126, np.rint(v * 2.0 ** 133) * 2.0 ** -133, v))
+    np.testing.assert_array_equal(got, want)
+    assert k in (-149, -140) or np.isfinite(got).any() and got.any()
+
+
+@pytest.mark.parametrize("gs", [1.4e-45, 3e-39, 1.1e-36, 2.3e-36, 0.0137, 0.99999994, 1.0000001, 77.123, 448.0 / 0.02, 2.9e30, 3.4e38])
+def test_nvfp4_values_under_any_global_scale(gs):
+    """The quotient and its product with the code are rounded to binary32 (2^-24 each; below its normal range 2^-150 and six
+    times that), then once to bf16: 2^-8 of the value bounds half a step, 2^-134 it below the normal range."""
+    got, v = all_nvfp4_values(gs)
+    top = (2 - 2.0 ** -7) * 2.0 ** 127
+    with np.errstate(invalid="ignore"):
+        near = np.abs(got - v) <= (2.0 ** -8 + 2.0 ** -22) * np.abs(v) + 2.0 ** -134 + 2.0 ** -147
+    assert np.all(np.where(np.abs(v) > top, np.abs(got) >= top, near))
+    assert not got[np.isnan(got)].size and np.all(np.signbit(got) == np.signbit(v))
+
+
 def test_offsets_past_32_bits():
     """Slots whose bytes lie past 4 GiB of a plane, and a slot number times its elements past 2^32."""
     pages, page, heads, dim = 18000, 64, 32, 128  # 4.7e9 elements, 2.4e9 bytes of codes; MXFP8: 4.7e9 bytes
