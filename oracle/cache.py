@@ -35,19 +35,22 @@ def encode_ref(x_bits, fmt, gs):
 
 
 def decode_ref(q, s, fmt, gs):
-    """The cached values as binary32 numbers, one rounding from bf16: the MX formats' are exact, NVFP4's are the
-    binary32 quotient scale / global scale times the code, rounded to binary32 again."""
+    """The cached values in float64: code * scale (NVFP4: / global scale, a binary32 number; the quotient's rounding to
+    float64 is the only one).  A value that is read back is one of these, rounded to bf16."""
     if fmt == "mxfp4":
-        return Q.dequant_ref(q, s).astype(np.float32)
+        return Q.dequant_ref(q, s)
     if fmt == "mxfp8":
-        return Q.mxfp8_dequant_ref(q, s).astype(np.float32)
-    f = (Q.E4M3_MAGNITUDES[s].astype(np.float32) / np.float32(gs)).astype(np.float32)
+        return Q.mxfp8_dequant_ref(q, s)
     codes = Q.unpack_codes(q)
     v = np.where(codes & 8, -1.0, 1.0) * Q.E2M1_MAGNITUDES[codes & 7]
-    return (v.astype(np.float32) * np.repeat(f, Q.NV_BLOCK, axis=-1)).astype(np.float32)
+    return v * np.repeat(Q.E4M3_MAGNITUDES[s].astype(np.float64), Q.NV_BLOCK, axis=-1) / float(np.float32(gs))
 
 
 def bf16_bits(v):
-    """binary32 -> bf16 bits, nearest even; infinities stay."""
-    u = np.asarray(v, dtype=np.float32).view(np.uint32).astype(np.uint64)
-    return ((u + 0x7FFF + ((u >> np.uint64(16)) & np.uint64(1))) >> np.uint64(16)).astype(np.uint16)
+    """Numbers (not NaN) -> bf16 bits in one rounding, nearest even; infinities stay."""
+    v = np.asarray(v, dtype=np.float64)
+    a = np.abs(v)
+    step = np.ldexp(1.0, np.maximum(np.frexp(np.where(np.isfinite(a), a, 0.0))[1] - 1, -126) - 7)
+    r = np.where(np.isfinite(a), np.rint(a / step) * step, a)
+    r = np.copysign(np.where(r >= 2.0 ** 128, np.inf, r), v).astype(np.float32)  # exact: eight bits
+    return (r.view(np.uint32) >> np.uint32(16)).astype(np.uint16)

@@ -237,7 +237,7 @@ def test_nvfp4_values_under_a_power_of_two(k):
     assert k in (-149, -140) or np.isfinite(got).any() and got.any()
 
 
-@pytest.mark.parametrize("gs", [1.4e-45, 3e-39, 1.1e-36, 2.3e-36, 0.0137, 0.99999994, 1.0000001, 77.123, 448.0 / 0.02, 2.9e30, 3.4e38])
+@pytest.mark.parametrize("gs", [1.4e-45, 3e-39, 1.1e-36, 2.3e-36, 0.0137, 512 / 257, 512 / 285, 0.99999994, 1.0000001, 77.123, 448.0 / 0.02, 2.9e30, 3.4e38])
 def test_nvfp4_values_under_any_global_scale(gs):
     """The quotient and its product with the code are rounded to binary32 (2^-24 each; below its normal range 2^-150 and six
     times that), then once to bf16: 2^-8 of the value bounds half a step, 2^-134 it below the normal range."""

@@ -2,6 +2,7 @@
 difference quotients."""
 
 import math
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -114,6 +115,33 @@ def test_cache_values_are_near_what_was_written(fmt, gs):
     # half the widest step: a sixth of the block's maximum in E2M1 (saturation and the scale's own rounding add
     # an eighth and 2^-4), 2^-4 of the value in E4M3
     assert np.all(np.abs(got - v) <= (2.0 ** -4 * np.abs(v) + 2.0 ** -10 * top if fmt == "mxfp8" else top * (1 / 6 + 1 / 8 + 2.0 ** -4)))
+
+
+def nearest_bf16(v):
+    """The bf16 number nearest to the fraction v >= 0 in bf16's normal range, the even one of two."""
+    e = 0
+    while v >= Fraction(2) ** (e + 1):
+        e += 1
+    while v < Fraction(2) ** e:
+        e -= 1
+    return round(v / Fraction(2) ** (e - 7)) * Fraction(2) ** (e - 7)
+
+
+# scale / global scale a hair off a midpoint of bf16: binary32 on the way rounds it onto the midpoint, or past it
+@pytest.mark.parametrize("gs", [8 * 64 / 257, 8 * 64 / 261, 8 * 64 / 285, 27 * 64 / 509, 45 * 64 / 371, 300.0, 0.3, 1e-30, 1e30])
+def test_cache_values_are_the_definition_rounded_once(gs):
+    gs = float(np.float32(gs))
+    q = np.tile(np.arange(16, dtype=np.uint8).reshape(8, 2) @ np.array([1, 16], np.uint8), (127, 1))
+    got = C.bf16_bits(C.decode_ref(q, np.arange(127, dtype=np.uint8)[:, None], "nvfp4", gs))
+    mags = [Fraction(0), Fraction(1, 2), Fraction(1), Fraction(3, 2), Fraction(2), Fraction(3), Fraction(4), Fraction(6)]
+    for s in range(127):
+        m, e = s % 8, s // 8
+        scale = Fraction(8 + m if e else m, 8) * Fraction(2) ** (max(e, 1) - 7)
+        for code in range(16):
+            v = mags[code % 8] * scale / Fraction(gs)
+            want = float(nearest_bf16(v)) if v else 0.0
+            bits = int(np.float32(want).view(np.uint32)) >> 16 | (0x8000 if code >= 8 else 0)
+            assert got[s, code] == bits, (s, code)
 
 
 def test_bf16_rounding_is_to_nearest_even():
