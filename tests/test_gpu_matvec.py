@@ -262,6 +262,100 @@ def test_experts_with_long_rows(fmt, T, E, k, N, K, swiglu, shared, bias):
     expert(T, E, k, N, K, fmt, swiglu, shared, bias, torch.float32 if T == 1 else torch.bfloat16)
 
 
+# pairs of the experts in turn: mostly up to 4, mostly 5 to 8, up to more than two tiles of x; none among them
+PAIRS = {4: (4, 1, 3, 4, 0, 2, 4, 5, 4, 3), 8: (5, 8, 0, 6, 1, 7, 4), 16: (9, 16, 3, 12, 17, 0, 8, 33, 5)}
+
+
+# Four tiles of 16 rows a wave: experts with three pairs on average or more, K of 1536 or more and 4096 tiles in all.
+# Outputs end in the first, second and third of a workgroup's tiles, inside a tile and at its end; K ends inside a step.
+@pytest.mark.parametrize("fmt", list(FMTS))
+@pytest.mark.parametrize("E,n_out,K,most,swiglu,bias,out", [
+    (1024, 65, 1568, 4, False, None, torch.float32), (1024, 65, 1536, 4, True, "fp32", torch.bfloat16),
+    (820, 80, 1808, 8, False, "bf16", torch.bfloat16), (600, 100, 1584, 8, True, None, torch.float32),
+    (512, 128, 2048, 16, False, "fp32", torch.float32), (300, 219, 1552, 16, True, "bf16", torch.bfloat16)])
+def test_four_tiles_a_wave(fmt, E, n_out, K, most, swiglu, bias, out):
+    if fmt == "mxfp4":
+        K = -(-K // 32) * 32
+    print(f"four tiles {fmt} E={E} n_out={n_out} K={K} most={most} swiglu={swiglu} bias={bias}", flush=True)
+    counts = np.resize(PAIRS[most], E)
+    P, N, D = int(counts.sum()), n_out * (2 if swiglu else 1), 13
+    assert P >= 3 * E and (n_out + 15) // 16 * E >= 4096 and K >= 1536
+    g = synth.rng(318, E, n_out, K)
+    q, s, gs = weights(g, (D, N, K), fmt)  # expert e has matrix e % D
+    of = torch.arange(E, device="cuda") % D
+    gsv = None if gs is None else (gs * (0.5 + np.arange(E) / E)).astype(np.float32)
+    b = g.normal(0, 0.1, (E, N)).astype(np.float32) if bias else None
+    bt = None if b is None else torch.from_numpy(b).cuda()
+    if bias == "bf16":
+        bt = bt.bfloat16()
+        b = host(bt)
+    x = synth.to_bf16_bits(g.standard_normal((P, K), dtype=np.float32))
+    offs = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    sp = g.permutation(P).astype(np.int32)
+    args = (bf16_dev(x), torch.from_numpy(q).cuda()[of], torch.from_numpy(s).cuda()[of], torch.from_numpy(offs).cuda(),
+            torch.from_numpy(sp).cuda(), bt)
+    kw = dict(fmt=FMTS[fmt], global_scales=None if gsv is None else torch.from_numpy(gsv).cuda(), swiglu=swiglu, out_dtype=out)
+    y = mx.fp4_expert_matvec(*args, **kw)
+    h, mag = np.empty((P, N)), np.empty((P, N))
+    for d in range(D):
+        w = V.weights_ref(q[d], s[d], None if gs is None else 1.0)
+        for e in range(d, E, D):
+            p = sp[offs[e]:offs[e + 1]]
+            xe, c = V.bf16_to_f64(x[p]), 1.0 if gsv is None else float(gsv[e])
+            h[p], mag[p] = xe @ w.T / c, np.abs(xe) @ np.abs(w).T / c
+            if b is not None:
+                h[p] += b[e]
+    expert_of = np.empty(P, int)
+    expert_of[sp] = np.repeat(np.arange(E), counts)
+    ref, tol = with_swiglu(h, linear_bound(h, mag, K, None if b is None else b[expert_of]), swiglu)
+    tol = tol + (2.0 ** -8 if out == torch.bfloat16 else U) * np.abs(ref) + 2.0 ** -133
+    err = np.abs(host(y) - ref)
+    assert y.shape == ref.shape and np.all(err <= tol), float((err / tol).max())
+    assert torch.equal(y, mx.fp4_expert_matvec(*args, **kw))
+
+
+def with_swiglu(h, tol, swiglu):
+    """(reference, bound) behind the product's: silu has a slope of at most 1.1, its own evaluation errs by (|g| + 8) u."""
+    if not swiglu:
+        return h, tol
+    ref = V.swiglu_ref(h)
+    gate, up = np.split(h, 2, 1)
+    tg, tu = np.split(tol, 2, 1)
+    silu = gate / (1 + np.exp(-gate))
+    return ref, 1.1 * tg * (np.abs(up) + tu) + np.abs(silu) * tu + (np.abs(gate) + 8) * U * np.abs(ref)
+
+
+@pytest.mark.parametrize("fmt", list(FMTS))
+def test_the_decode_layers_products(fmt):
+    """Both products of the decode layer (64 tokens, top-8 of 128, 1536 x 2048 with SwiGLU, then 2048 x 768) on the routing
+    of random logits; the outputs of a sample of rows of W."""
+    cfg = synth.MOE_CONFIGS["decode"]
+    g = synth.rng(319)
+    T, E, k = cfg.T, cfg.E, cfg.k
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    ids, _, offs, sp = mx.route(torch.randn(T, E, generator=gen, device="cuda"), k)
+    idn = ids.cpu().numpy().reshape(-1)
+    for N, K, swiglu, shared in ((2 * cfg.I, cfg.H, True, True), (cfg.H, cfg.I, False, False)):
+        print(f"decode {fmt} {N} x {K}", flush=True)
+        w = (torch.randn(E * N, K, generator=gen, device="cuda") * 0.02).bfloat16()
+        gs = 448.0 / 0.02 if fmt == "nvfp4" else None
+        q, s = (mx.nvfp4_quantize(w, gs, tiled=False) if gs else mx.quantize(w, tiled=False))[:2]
+        q, s = q.view(E, N, -1), s.view(E, N, -1)
+        x = synth.to_bf16_bits(g.standard_normal((T if shared else T * k, K), dtype=np.float32))
+        gsd = None if gs is None else torch.full((E,), gs, device="cuda")
+        y = host(mx.fp4_expert_matvec(bf16_dev(x), q, s, offs, sp, fmt=FMTS[fmt], global_scales=gsd, top_k=k if shared else 1,
+                                      swiglu=swiglu, out_dtype=torch.float32))
+        n_out = N // 2 if swiglu else N
+        rows = np.unique(np.concatenate([[0, 15, 16, 31, 32, 63, 64, n_out - 1], g.integers(0, n_out, 12)]))
+        at = torch.from_numpy(np.concatenate([rows, rows + n_out]) if swiglu else rows).cuda()
+        qh, sh = q[:, at].cpu().numpy(), s[:, at].cpu().numpy()
+        h, mag = V.expert_matvec_ref(x, qh, sh, idn.reshape(T, k), shared, None, None if gs is None else np.full(E, gs))
+        ref, tol = with_swiglu(h, linear_bound(h, mag, K), swiglu)
+        tol = tol + U * np.abs(ref) + 2.0 ** -133
+        err = np.abs(y[:, rows] - ref)
+        assert y.shape == (T * k, n_out) and np.all(err <= tol), float((err / tol).max())
+
+
 @pytest.mark.parametrize("fmt", list(FMTS))
 def test_more_pairs_than_a_tile_on_one_expert(fmt):
     expert(37, 9, 2, 40, 128, fmt, True, True, True, torch.float32, 1, crowd=True)
