@@ -26,6 +26,13 @@ def _need(cond, msg):
         raise ValueError(msg)
 
 
+def _need_int32(*sizes):
+    """ctypes would pass the low 32 bits of a larger number on."""
+    for n in sizes:
+        if not -1 << 31 <= n < 1 << 31:
+            raise ValueError(f"a size of {n} does not fit the entry points' 32 bits")
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -133,8 +140,10 @@ def balance_loss(logits, topk_ids, token_mask=None):
     pass into a graph, drop every eager autograd graph of the same leaves first, as torch asks for any backward pass."""
     _gpu_of("logits", logits, topk_ids, token_mask)
     T, E, step = _check_logits(logits)
+    _need_int32(E)
     _need(topk_ids.dtype == torch.int32 and topk_ids.dim() == 2 and topk_ids.shape[0] == T and topk_ids.is_contiguous(),
           "topk_ids: contiguous int32 [T, k]")
+    _need_int32(topk_ids.shape[1])
     if token_mask is not None:
         _check_mask(token_mask, T)
     return _BalanceLoss.apply(logits, topk_ids, token_mask, T, E, step)
@@ -216,6 +225,7 @@ def fp4_expert_matvec(x, w_q, w_s, expert_offsets, sorted_pairs, bias=None, *, f
     for t in (expert_offsets, sorted_pairs):
         _need(t.dtype == torch.int32 and t.dim() == 1 and t.is_contiguous(),
               "expert_offsets and sorted_pairs: contiguous int32 1-D")
+    _need_int32(E, top_k)
     _need(expert_offsets.shape[0] == E + 1, "expert_offsets: E + 1 entries")
     P = sorted_pairs.shape[0]
     _need(top_k >= 1 and M * top_k == P, "x must have one row for every top_k pairs")
@@ -253,6 +263,7 @@ class PagedCache:
     def __init__(self, num_pages, page_size, heads, k_dim, v_dim=None, fmt=FMT_MXFP8, k_global_scale=1.0,
                  v_global_scale=1.0, storage=None, device=None):
         v_dim = k_dim if v_dim is None else v_dim
+        _need_int32(fmt, heads, k_dim, v_dim, page_size)
         self._dims = CacheDims(fmt, heads, k_dim, v_dim, page_size, num_pages, k_global_scale, v_global_scale)
         sizes = (ctypes.c_size_t * 4)()
         check("mxfp4_cache_bytes", _lib.lib().mxfp4_cache_bytes(ctypes.byref(self._dims), sizes))
@@ -292,6 +303,8 @@ class PagedCache:
         if page_table.dtype != torch.int32 or page_table.dim() != 2 or cu_rows.dtype != torch.int32:
             raise ValueError("page_table: int32 [B, pages], cu_rows: int32 [B + 1]")
         B, P = page_table.shape
+        if (B | P) >> 31:
+            _need_int32(B, P)
         if P > 1 and page_table.stride(1) != 1 or B > 1 and page_table.stride(0) < P:
             raise ValueError("page_table's last dimension must be contiguous, its rows must not overlap")
         if cu_rows.shape != (B + 1,) or not cu_rows.is_contiguous():

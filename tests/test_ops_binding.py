@@ -123,3 +123,32 @@ def test_the_caches_addresses_are_those_at_the_call(calls):
     new = write_and_read(c, calls)
     assert new == tuple(t.data_ptr() for t in (c.k_q, c.k_s, c.v_q, c.v_s)) and new[0] != held.data_ptr()
     assert new[1:3] == old[1:3]
+
+
+WIDE = (1 << 32) + 16  # 16 in 32 bits
+
+
+@pytest.mark.parametrize("kw", [dict(heads=WIDE), dict(page_size=WIDE), dict(k_dim=WIDE * 2), dict(v_dim=WIDE * 2),
+                                dict(fmt=(1 << 32) + 2), dict(page_size=1 << 31), dict(heads=-WIDE)])
+def test_cache_sizes_past_32_bits_are_refused(calls, kw):
+    args = dict(num_pages=1, page_size=16, heads=1, k_dim=32, v_dim=0, fmt=mx.FMT_MXFP8, device="meta")
+    mx.PagedCache(**args)
+    with pytest.raises((ValueError, mx.Mxfp4Error)):
+        mx.PagedCache(**{**args, **kw})
+
+
+def test_calls_with_sizes_past_32_bits_are_refused(calls):
+    z = lambda *s, d=torch.int32: torch.empty(*s, dtype=d, device="meta")  # noqa: E731
+    c = mx.PagedCache(1, 16, 1, 32, 0, mx.FMT_MXFP8, device="meta")
+    rows = z(3, 1, 32, d=torch.bfloat16)
+    calls.clear()
+    for bad in (lambda: mx.balance_loss(z(0, WIDE, d=torch.float32), z(0, 2)),
+                lambda: mx.balance_loss(z(1, 64, d=torch.float32), z(1, WIDE)),
+                lambda: c.write(rows, None, z(1, WIDE), z(2)), lambda: c.read(z(WIDE, 0), z(WIDE + 1), rows=3),
+                lambda: mx.fp4_expert_matvec(z(0, 32, d=torch.bfloat16), z(WIDE, 1, 16, d=torch.uint8),
+                                             z(WIDE, 1, 1, d=torch.uint8), z(WIDE + 1), z(0)),
+                lambda: mx.fp4_expert_matvec(z(0, 32, d=torch.bfloat16), z(2, 1, 16, d=torch.uint8),
+                                             z(2, 1, 1, d=torch.uint8), z(3), z(0), top_k=WIDE)):
+        with pytest.raises(ValueError):
+            bad()
+    assert not calls
