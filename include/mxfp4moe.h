@@ -297,7 +297,8 @@ int moe_mxfp4_forward_noalloc(const mxfp4_moe_dims* d, const void* packed_gfx950
  * loss device fp32 [1], counts device int32 [E], coef device fp32 [E] (d_e, for the backward pass).
  * workspace device, >= moe_balance_workspace_bytes(T, E), 256-byte aligned; nothing in it is kept
  * between calls.  Sums over tokens run in binary32 inside a workgroup and in binary64 across
- * workgroups, in a fixed order: repeated calls give the same bits.  T == 0 writes loss 0 and counts 0.
+ * workgroups, in a fixed order: repeated calls give the same bits.  Exponentials are the hardware's: a probability
+ * is off by about |logit - maximum| 2^-23 of itself besides its roundings.  T == 0 writes loss 0 and counts 0.
  * moe_balance_backward: grad_loss device fp32 [1]; grad_logits device fp32 [T, E] contiguous, every
  * element written.  Pointers of both need 4-byte alignment only (workspace aside).
  */
@@ -338,7 +339,8 @@ int fp4_matvec(int32_t fmt, const void* w_q, const void* w_s, float global_scale
  * layer, on weights in the standard layout]
  *   y[p] = W_e x[p / top_k] / global_scales[e] + b_e   for p in sorted_pairs[offsets[e], offsets[e+1]);
  *   swiglu != 0: the first N/2 rows of W_e are the gate, the others the up projection, and
- *   y[p] = silu(gate) * up has N/2 columns (rows [w1; w3], as in the MoE layer).
+ *   y[p] = silu(gate) * up has N/2 columns (rows [w1; w3], as in the MoE layer; the hardware's exponential: silu is off
+ *   by about |gate| 2^-24 of itself).
  * w_q [E, N, K/2], w_s [E, N, K/B], bias [E, N] or NULL, global_scales device fp32 [E] (NVFP4).
  * expert_offsets device int32 [E + 1] and sorted_pairs device int32 [n_pairs]: moe_mxfp4_route's outputs
  *   (offsets outside [0, n_pairs] are clamped, pairs outside it passed over; a pair that is not

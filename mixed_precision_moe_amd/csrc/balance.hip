@@ -9,10 +9,10 @@
 // the same columns from row to row: S_e needs no exchange inside the loop.  The forward pass runs as
 // partial sums of up to 256 workgroups and a second launch that joins them (8 columns a workgroup, binary64, fixed
 // order); the workgroup that is last to finish adds up the loss.  Few logits take one workgroup and one launch.
-// Measured: 65533 x 384 with a fifth of the rows masked: forward 22.5 us (80 MB of rows that count), join 9.5 us, backward
-// 34 us (181 MB, 5.3 TB/s); one row instead of two on its way 29.5 us; 8192 x 128: 5, 7.5 and 5.5 us.  The join is four
-// dependent trips to memory (partial sums, publishing, the number, the columns); with 512 partial sums and 32 columns a
-// workgroup it took 14 us.
+// Measured (averages): 65533 x 384 with a fifth of the rows masked: forward 22.6 us (80 MB of rows that count, 3.6 TB/s),
+// join 9.4 us, backward 34.5 us (181 MB, 5.3 TB/s); one row instead of two on its way 29.5 us; 8192 x 128: 5, 7 and 5.3 us.
+// The join is four dependent trips to memory (partial sums, publishing, the number, the columns); with 512 partial sums and
+// 32 columns a workgroup it took 14 us.
 #include <hip/hip_runtime.h>
 
 #include "ops.h"
@@ -238,7 +238,7 @@ __global__ __launch_bounds__(kThreads) void balance_forward_kernel(BalanceArgs a
 }
 
 // Joins the partial sums of `blocks` <= kMaxBlocks workgroups: kJoinCols columns a workgroup, the blocks spread over
-// its waves' halves.  The last workgroup to finish has the loss.
+// its groups of kJoinCols threads.  The last workgroup to finish has the loss.
 __global__ __launch_bounds__(kJoin) void balance_join_kernel(BalanceArgs a, int32_t blocks,
                                                              const Part* __restrict__ parts,
                                                              const int32_t* __restrict__ part_v, double* sums,

@@ -130,8 +130,9 @@ MX_DEV u32x4_t decode(const uint32_t* q, uint32_t s, float gs) {
 // Both directions are bound by memory: a value costs 2 bytes on one side and 1.03 (MXFP8), 0.56 or 0.53 on the other.
 // Measured: 93600 rows of 2 x 1024 values read back from MXFP8, 581 MB, 126 us (4.6 TB/s, 0.9 of a large copy's
 // rate); with a wave a row and 8-byte accesses in a loop 165 us, 8 rows a wave 146 us, 1 row 134 us, batches of 2 or 8
-// 170 and 143 us; streaming (nontemporal) accesses take 3 to 6 % off.  18400 rows of 8 x 320 to and from NVFP4, 147 MB
-// each way: written in 30 us, read back in 22 us.
+// 170 and 143 us; streaming (nontemporal) accesses take 3 to 6 % off.  18126 rows of 8 x 320 to and from NVFP4, 119 MB
+// each way: written in 32 us (3.7 TB/s; scales go out a byte at a time, and rows come in by ordinary loads), read back in
+// 23.6 us (5.0 TB/s).
 constexpr int kBatch = 4;
 
 template <int FMT, bool WRITE, bool SPREAD>  // SPREAD: heads apart in some plane's rows

@@ -7,12 +7,14 @@
 // rows, the waves of a workgroup share K and meet once, and nothing is set up or waited for before the first load of
 // weights but, in the expert form, the expert's number.  NVFP4's dequantization takes four instructions a pair of weights
 // (MXFP4: one) and then bounds small numbers of rows: there the scale goes behind the matrix instruction (tile_sums_nv).
-// Measured (one pass, kernel alone):
-//   1 x 7168 x 7168           MXFP4  7.8 us (3.5 TB/s), NVFP4 9.6 us (3.0 TB/s)
-//   1 x 28672 x 7168          MXFP4 24 us (4.5 TB/s), NVFP4 25 us (4.6 TB/s); loads of the same pieces alone 17.5 us
-//   16 x 7168 x 2048          MXFP4  5.6 us; 16 x 7168 x 7168 10.5 us
-//   64 tokens, top-8 of 128   2048 x 768: MXFP4 29 us, NVFP4 33 us; 1536 x 2048 with SwiGLU 46 and 57 us (4.5, 3.9 TB/s)
+// Measured (kernel alone, averages; weights from memory, in brackets from the last-level cache):
+//   1 x 7168 x 7168           MXFP4  8.5 us (7.8; 3.2 TB/s from memory), NVFP4 10.6 us (9.6; 2.7 TB/s)
+//   1 x 28672 x 7168          MXFP4 24.8 us (24.1; 4.4 TB/s), NVFP4 23.8 us (23.5; 4.9 TB/s)
+//   16 x 7168 x 2048          MXFP4  6.4 us (5.2)
+//   16 x 7168 x 7168          MXFP4 12.5 us (10.8), NVFP4 15.1 us (12.8): every workgroup reads all of x
+//   64 tokens, top-8 of 128   2048 x 768: MXFP4 28 us, NVFP4 32 us; 1536 x 2048 with SwiGLU 47 and 56 us (4.5, 4.0 TB/s)
 //   16 tokens, the latter     MXFP4 30 us, NVFP4 38 us
+//   1 token, the latter       MXFP4 8.3 us (1.6 TB/s), NVFP4 9.5 us: eight waves are launched for four blocks of K
 // Tried and slower: scales a byte at a time beside the codes (a third of the time); x 16 bytes a row from memory (half of
 // the time at 16 rows); scales and x of the whole workgroup in LDS behind a barrier (7168 x 7168: 11 to 14 us); a ring or a
 // second set of registers for the next block (spills, or fewer waves: 12 to 18 us).
@@ -519,7 +521,9 @@ int launch_rows(const MatvecArgs& a, hipStream_t stream) {
   const int kB = (XR > kFew ? kManySteps : SB) * kStep;
   const int64_t blocks = (a.K + kB - 1) / kB;
   // blocks of K a wave works through: as few as leave waves to fill the chip, and 16 waves a workgroup (8 for many rows
-  // of x, whose LDS they share); a wave less where the last round would be less than half full
+  // of x, whose LDS they share); a wave less where the last round would be less than half full (one row of 14000 x 5120,
+  // 9600 x 7168, 24000 x 1536: MXFP4 9.9 -> 9.1, 10.6 -> 10.1, 6.8 -> 6.7 us, but NVFP4 11.6 -> 12.0, 11.9 -> 12.3, 7.8 -> 8.2;
+  // 16 rows: no difference)
   int64_t each = tiles * groups * blocks / (R == 4 ? kFullWide : kFull);
   each = each < 1 ? 1 : each;
   const int64_t most = XR > kFew ? 8 : 16;
