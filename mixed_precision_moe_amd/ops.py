@@ -196,8 +196,9 @@ def fp4_matvec(x, w_q, w_s, bias=None, *, fmt=FMT_MXFP4, global_scale=None, out_
     """y = x W^T (/ global_scale) + b for one or a few rows of x: the decoding form of the W4A16 linear layer,
     on weights as `quantize` (FMT_MXFP4) or `nvfp4_quantize` (FMT_NVFP4, with its global_scale) returns them.
 
-    x bf16 [M, K] (rows may be strided), w_q uint8 [N, K/2], w_s uint8 flat scales [N, K/32] or [N, K/16], bias fp32
-    or bf16 [N] or None.  Returns y [M, N] in out_dtype (bfloat16 or float32)."""
+    x bf16 [M, K] (rows may be strided, by a multiple of 8 elements; they and w_q start on 16 bytes), w_q uint8
+    [N, K/2], w_s uint8 flat scales [N, K/32] or [N, K/16], bias fp32 or bf16 [N] or None.  Returns y [M, N] in
+    out_dtype (bfloat16 or float32)."""
     gpu = _gpu_of("x", x, w_q, w_s, bias)
     N, K = _check_weights(w_q, w_s, fmt, 2)
     M, ldx = _check_rows(x, K)
@@ -214,10 +215,10 @@ def fp4_expert_matvec(x, w_q, w_s, expert_offsets, sorted_pairs, bias=None, *, f
                       top_k=1, swiglu=False, out_dtype=torch.bfloat16, y=None):
     """Every routed pair's product with its expert's matrix, on weights in the standard layout.
 
-    x bf16 [P / top_k, K]: row p // top_k is the input of pair p (top_k as routed for the first product, 1 where
-    every pair has its own row).  w_q uint8 [E, N, K/2], w_s uint8 [E, N, K/32] (NVFP4: [E, N, K/16]), bias [E, N]
-    or None, global_scales fp32 [E] (NVFP4).  expert_offsets int32 [E + 1] and sorted_pairs int32 [P] as `route`
-    returns them.  Returns y [P, N], or [P, N/2] = silu(gate rows) * up rows with swiglu (rows [w1; w3]).  A pair
+    x bf16 [P / top_k, K], laid out as for `fp4_matvec`: row p // top_k is the input of pair p (top_k as routed for
+    the first product, 1 where every pair has its own row).  w_q uint8 [E, N, K/2], w_s uint8 [E, N, K/32] (NVFP4:
+    [E, N, K/16]), bias [E, N] or None, global_scales fp32 [E] (NVFP4).  expert_offsets int32 [E + 1] and
+    sorted_pairs int32 [P] as `route` returns them.  Returns y [P, N], or [P, N/2] = silu(gate rows) * up rows with swiglu (rows [w1; w3]).  A pair
     that sorted_pairs does not list keeps what its row of `y` held."""
     gpu = _gpu_of("x", x, w_q, w_s, bias, expert_offsets, sorted_pairs, global_scales, y)
     E, N, K = _check_weights(w_q, w_s, fmt, 3)
@@ -334,7 +335,7 @@ class PagedCache:
         [cu_rows[b], cu_rows[b+1]) are sequence b's positions start[b], start[b]+1, ... (start None: from 0);
         position i lives in page page_table[b, i // page_size].  Rows outside every sequence, and positions without
         a page (past the table, or a page number outside the cache), are passed over.  Two rows of one call must not
-        share a slot."""
+        share a slot.  Rows and heads may be strided, by multiples of 8 elements, and start on 16 bytes."""
         _gpu_of("the cache", self._storage[0], k, v, page_table, cu_rows, start)
         index = self._index(page_table, cu_rows, start)
         planes = self._planes(k, v)

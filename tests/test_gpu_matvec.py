@@ -270,7 +270,7 @@ PAIRS = {4: (4, 1, 3, 4, 0, 2, 4, 5, 4, 3), 8: (5, 8, 0, 6, 1, 7, 4), 16: (9, 16
 # Outputs end in the first, second and third of a workgroup's tiles, inside a tile and at its end; K ends inside a step.
 @pytest.mark.parametrize("fmt", list(FMTS))
 @pytest.mark.parametrize("E,n_out,K,most,swiglu,bias,out", [
-    (1024, 65, 1568, 4, False, None, torch.float32), (1024, 65, 1536, 4, True, "fp32", torch.bfloat16),
+    (1010, 65, 1568, 4, False, None, torch.float32), (1010, 65, 1536, 4, True, "fp32", torch.bfloat16),
     (820, 80, 1808, 8, False, "bf16", torch.bfloat16), (600, 100, 1584, 8, True, None, torch.float32),
     (512, 128, 2048, 16, False, "fp32", torch.float32), (300, 219, 1552, 16, True, "bf16", torch.bfloat16)])
 def test_four_tiles_a_wave(fmt, E, n_out, K, most, swiglu, bias, out):
