@@ -340,7 +340,7 @@ int fp4_matvec(int32_t fmt, const void* w_q, const void* w_s, float global_scale
  *   y[p] = W_e x[p / top_k] / global_scales[e] + b_e   for p in sorted_pairs[offsets[e], offsets[e+1]);
  *   swiglu != 0: the first N/2 rows of W_e are the gate, the others the up projection, and
  *   y[p] = silu(gate) * up has N/2 columns (rows [w1; w3], as in the MoE layer; the hardware's exponential: silu is off
- *   by about |gate| 2^-24 of itself).
+ *   by about |gate| 2^-24 of itself, and 0 for gates below -88.7, where it is less than 2^-121).
  * w_q [E, N, K/2], w_s [E, N, K/B], bias [E, N] or NULL, global_scales device fp32 [E] (NVFP4).
  * expert_offsets device int32 [E + 1] and sorted_pairs device int32 [n_pairs]: moe_mxfp4_route's outputs
  *   (offsets outside [0, n_pairs] are clamped, pairs outside it passed over; a pair that is not
