@@ -218,8 +218,9 @@ def fp4_expert_matvec(x, w_q, w_s, expert_offsets, sorted_pairs, bias=None, *, f
     x bf16 [P / top_k, K], laid out as for `fp4_matvec`: row p // top_k is the input of pair p (top_k as routed for
     the first product, 1 where every pair has its own row).  w_q uint8 [E, N, K/2], w_s uint8 [E, N, K/32] (NVFP4:
     [E, N, K/16]), bias [E, N] or None, global_scales fp32 [E] (NVFP4).  expert_offsets int32 [E + 1] and
-    sorted_pairs int32 [P] as `route` returns them.  Returns y [P, N], or [P, N/2] = silu(gate rows) * up rows with swiglu (rows [w1; w3]).  A pair
-    that sorted_pairs does not list keeps what its row of `y` held."""
+    sorted_pairs int32 [P] as `route` returns them.  Returns y [P, N], or [P, N/2] = silu(gate rows) * up rows with
+    swiglu (rows [w1; w3]).  A pair that sorted_pairs does not list keeps what its row of `y` held (without `y` the
+    row is undefined)."""
     gpu = _gpu_of("x", x, w_q, w_s, bias, expert_offsets, sorted_pairs, global_scales, y)
     E, N, K = _check_weights(w_q, w_s, fmt, 3)
     M, ldx = _check_rows(x, K)
