@@ -391,6 +391,100 @@ int mxfp4_cache_read(const mxfp4_cache_dims* d, const void* k_q, const void* k_s
                      int64_t ld_table, int32_t n_seqs, int32_t max_pages, void* k_bf16, int64_t k_ldt, int64_t k_ldh,
                      void* v_bf16, int64_t v_ldt, int64_t v_ldh, void* stream);
 
+/* ------------------------------------------------------------------------------------------------
+ * Attention over the paged cache, for rows whose keys and values the cache holds already: one new token, a
+ * chunk of a prompt, or a tree of drafted tokens.  [DEF]
+ *   out[t, h] = sum_j p_j V[j, g],  p = softmax over the positions j that row t sees of scale * q[t, h] . K[j, g],
+ *   g = h / (q_heads / heads), K and V the cache's values (code * scale, NVFP4: / global scale; not rounded to bf16).
+ * Rows are ragged as for mxfp4_cache_write, and given the same cu_rows, start and page_table: row t of sequence b is
+ * its draft i = t - cu_rows[b], at position start[b] + i.  It sees the positions below start[b], and of its sequence's
+ * n drafts those j with tree_mask[t * ld_mask + j] != 0 (j >= mask_cols: none), or, tree_mask NULL, those with j <= i.
+ * A position without a page (mxfp4_cache_write) is not seen; what lies there or in places that the mask hides is not
+ * looked at.  A row that sees nothing gets zeros.  Rows outside every sequence are not read and keep their output.
+ * q device bf16, element (row, head, i) at row * q_ldt + head * q_ldh + i, strides multiples of 8, 16-byte aligned,
+ *   q_heads a multiple of heads, q_heads <= 2^16.  k_dim and v_dim at most 256, v_dim > 0.  scale finite.
+ * out device bf16 or fp32 (out_is_fp32), element (row, head, i) at row * out_ldt + head * out_ldh + i, strides multiples
+ *   of 8, 16-byte aligned; its vectors must not overlap.
+ * tree_mask device uint8, row t of mask_cols entries at t * ld_mask, or NULL.
+ * Arithmetic: values are exact in bf16 (code * scale), products accumulate in fp32, the maximum and the sum of the
+ * softmax are fp32, the weights p are rounded to bf16 before the second product; parts of a long context are joined in
+ * fp32 in a fixed order, and the result is rounded once: repeated calls give the same bits.  Exponentials are the
+ * hardware's.  A value of 2^128 and more, scores past fp32's range and NaN inside what a row sees are outside the contract.
+ * workspace device, 256-byte aligned, >= mxfp4_cache_attend_workspace_bytes (0: invalid sizes); nothing in it is kept
+ * between calls. */
+size_t mxfp4_cache_attend_workspace_bytes(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows, int32_t n_seqs);
+int mxfp4_cache_attend(const mxfp4_cache_dims* d, const void* k_q, const void* k_s, const void* v_q, const void* v_s,
+                       const void* q_bf16, int64_t q_ldt, int64_t q_ldh, int32_t q_heads, int64_t rows,
+                       const int32_t* cu_rows, const int32_t* start, const int32_t* page_table, int64_t ld_table,
+                       int32_t n_seqs, int32_t max_pages, const uint8_t* tree_mask, int64_t ld_mask, int32_t mask_cols,
+                       float scale, void* out, int64_t out_ldt, int64_t out_ldh, int32_t out_is_fp32, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * Compaction: the accepted drafts of each sequence are moved together.  [DEF]
+ * path device int32 [n_seqs, ld_path], path_cols columns used: path[b] = the accepted drafts of sequence b in increasing
+ * order, ended by a negative entry, by one that does not increase, or by the last column.  Position start[b] + i takes the
+ * codes and scales of position start[b] + path[b][i], as they were before the call.  A position without a page is not
+ * written, and one whose source has no page keeps what it holds.  lengths device int32 [n_seqs] gets start[b] + the
+ * number of accepted drafts (may be NULL; must not be start).  Sequences must not share the slots that are moved. */
+int mxfp4_cache_compact(const mxfp4_cache_dims* d, const int32_t* start, const int32_t* path, int64_t ld_path,
+                        int32_t path_cols, const int32_t* page_table, int64_t ld_table, int32_t n_seqs,
+                        int32_t max_pages, int32_t* lengths, void* k_q, void* k_s, void* v_q, void* v_s, void* stream);
+
+/* The first rows[i] tokens (rows NULL: all) of page src[i] are copied to page dst[i], i < n.  A pair with a page outside
+ * [0, num_pages) is passed over.  No page may be the destination of two pairs, or a source and another pair's
+ * destination. */
+int mxfp4_cache_copy_pages(const mxfp4_cache_dims* d, const int32_t* src, const int32_t* dst, const int32_t* rows,
+                           int32_t n, void* k_q, void* k_s, void* v_q, void* v_s, void* stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * Page pool: which pages of a cache are in use, on the device.  [DEF]
+ * refs device int32 [num_pages]: how many rows of the page tables hold the page; a page with refs <= 0 is free.  The pages
+ * that row b of a table holds are its leading entries in [0, num_pages); the other entries are -1.
+ * Free pages are handed out in increasing order, to rows (pairs) in increasing order.
+ *
+ * mxfp4_pool_resize: row b then holds the ceil(lengths[b] / page_size) pages of lengths[b] tokens (at most max_pages;
+ * lengths[b] < 0: the row is left alone).  Pages past them are given back, missing ones are taken.  Where lengths[b] ends
+ * inside a page that the row held already and that is shared (refs > 1 after what this call gives back), the row gets a
+ * page of its own in its place.
+ *
+ * mxfp4_pool_fork: for each pair i < n, row dst[i] gives back its pages and gets the first lengths[i] tokens of row
+ * src[i]: whole pages are shared, the page that lengths[i] ends in, where row src[i] holds it, becomes a page of its own.
+ * A pair is passed over when a row is outside the table, lengths[i] < 0, dst[i] is a source of any pair, or an earlier
+ * pair has the same dst.
+ *
+ * copies device int32 [3, n_rows] (fork: [3, n]): the source page, new page and tokens of each row (pair) whose page has
+ * to be copied, as mxfp4_cache_copy_pages takes them; -1, -1, 0 where there is none.
+ * missing device int32 [1]: pages that were wanted when no page was free any more; their entries are -1 (a shared page
+ * that was to be replaced stays).
+ * workspace device, 256-byte aligned, >= mxfp4_pool_workspace_bytes(num_pages, n_rows or n, max_pages).
+ * num_pages < 2^31, page_size >= 1, n_rows <= 2^24, n <= 2^16, n_rows * max_pages and n * max_pages < 2^31. */
+size_t mxfp4_pool_workspace_bytes(int64_t num_pages, int32_t n, int32_t max_pages);
+int mxfp4_pool_resize(int64_t num_pages, int32_t page_size, int32_t* refs, int32_t* page_table, int64_t ld_table,
+                      int32_t n_rows, int32_t max_pages, const int32_t* lengths, int32_t* copies, int32_t* missing,
+                      void* workspace, size_t workspace_bytes, void* stream);
+int mxfp4_pool_fork(int64_t num_pages, int32_t page_size, int32_t* refs, int32_t* page_table, int64_t ld_table,
+                    int32_t n_rows, int32_t max_pages, const int32_t* src, const int32_t* dst, const int32_t* lengths,
+                    int32_t n, int32_t* copies, int32_t* missing, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * Rotary positions, on queries and keys at once.  [DEF]
+ * Elements [offset, offset + rot_dim) of each head_dim vector are pairs (a, b), pair i turned by the angle
+ * 2 pi positions[row] turns[i]:  a' = m (a cos - b sin), b' = m (b cos + a sin), m = magnitude; pair i is elements
+ * (i, i + rot_dim / 2), or (2i, 2i + 1) with interleaved.  The other elements are copied (not where input and output are
+ * the same memory).  inverse != 0 turns by the negative angle: with the same magnitude, the gradient.
+ * turns device double [rot_dim / 2]: turns per position.  positions device int32 [rows].
+ * q, k device bf16 or fp32 (is_fp32), element (row, head, i) at row * ldt + head * ldh + i; k NULL: queries only.  Output
+ * vectors must not overlap each other, nor an input but that of the same place.  rot_dim even, 2 <= rot_dim <= 2048,
+ * offset >= 0, offset + rot_dim <= head_dim <= 2^16, heads * head_dim <= 2^20.  Element alignment suffices.
+ * Arithmetic: the angle in binary64, less its whole turns; sine, cosine, magnitude and the sums in binary32; one rounding
+ * to the type. */
+int mxfp4_rotary(const double* turns, const int32_t* positions, int64_t rows, int32_t head_dim, int32_t rot_dim,
+                 int32_t offset, int32_t interleaved, float magnitude, int32_t inverse, int32_t is_fp32, const void* q,
+                 int64_t q_ldt, int64_t q_ldh, int32_t q_heads, void* q_out, int64_t q_out_ldt, int64_t q_out_ldh,
+                 const void* k, int64_t k_ldt, int64_t k_ldh, int32_t k_heads, void* k_out, int64_t k_out_ldt,
+                 int64_t k_out_ldh, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -62,6 +62,18 @@ _SIGS = {
     "mxfp4_cache_bytes": (ctypes.c_int, [ctypes.POINTER(CacheDims), ctypes.POINTER(c_sz)]),
     "mxfp4_cache_write": (ctypes.c_int, [ctypes.POINTER(CacheDims)] + _CACHE_ROWS + _CACHE_INDEX + [c_p] * 5),
     "mxfp4_cache_read": (ctypes.c_int, [ctypes.POINTER(CacheDims)] + [c_p] * 4 + _CACHE_INDEX + _CACHE_ROWS + [c_p]),
+    "mxfp4_cache_attend_workspace_bytes": (c_sz, [ctypes.POINTER(CacheDims), c_i32, c_i64, c_i32]),
+    "mxfp4_cache_attend": (ctypes.c_int, [ctypes.POINTER(CacheDims)] + [c_p] * 5 + [c_i64, c_i64, c_i32] + _CACHE_INDEX +
+                           [c_p, c_i64, c_i32, ctypes.c_float, c_p, c_i64, c_i64, c_i32, c_p, c_sz, c_p]),
+    "mxfp4_cache_compact": (ctypes.c_int, [ctypes.POINTER(CacheDims), c_p, c_p, c_i64, c_i32, c_p, c_i64, c_i32, c_i32] +
+                            [c_p] * 6),
+    "mxfp4_cache_copy_pages": (ctypes.c_int, [ctypes.POINTER(CacheDims), c_p, c_p, c_p, c_i32] + [c_p] * 5),
+    "mxfp4_pool_workspace_bytes": (c_sz, [c_i64, c_i32, c_i32]),
+    "mxfp4_pool_resize": (ctypes.c_int, [c_i64, c_i32, c_p, c_p, c_i64, c_i32, c_i32, c_p, c_p, c_p, c_p, c_sz, c_p]),
+    "mxfp4_pool_fork": (ctypes.c_int, [c_i64, c_i32, c_p, c_p, c_i64, c_i32, c_i32, c_p, c_p, c_p, c_i32, c_p, c_p, c_p,
+                                       c_sz, c_p]),
+    "mxfp4_rotary": (ctypes.c_int, [c_p, c_p, c_i64, c_i32, c_i32, c_i32, c_i32, ctypes.c_float, c_i32, c_i32] +
+                     [c_p, c_i64, c_i64, c_i32, c_p, c_i64, c_i64] * 2 + [c_p]),
 }
 
 EXPORTED = tuple(_SIGS)

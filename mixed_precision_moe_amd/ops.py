@@ -1,5 +1,5 @@
-"""The balance loss, the 4-bit matrix-vector products and the block-quantized paged cache: the torch binding of
-their C entry points.  Like the rest of the binding it checks dtypes, shapes and devices, allocates
+"""The balance loss, the 4-bit matrix-vector products, the block-quantized paged cache with the attention over it and
+its page pool: the torch binding of their C entry points.  Like the rest of the binding it checks dtypes, shapes and devices, allocates
 outputs and passes raw pointers; the work runs on the current stream of the tensors' device."""
 
 import ctypes
@@ -254,6 +254,34 @@ def fp4_expert_matvec(x, w_q, w_s, expert_offsets, sorted_pairs, bias=None, *, f
 # Paged cache.
 
 
+@functools.lru_cache(maxsize=1024)
+def _attend_workspace(fmt, heads, k_dim, v_dim, q_heads, rows, B):
+    dims = CacheDims(fmt, heads, k_dim, v_dim, 1, 0, 1.0, 1.0)
+    return _lib.lib().mxfp4_cache_attend_workspace_bytes(ctypes.byref(dims), q_heads, rows, B)
+
+
+def _vectors(t, name, heads, dim):
+    """(address, elements from row to row, from head to head; the stride of a dimension of one entry says nothing)."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.stride(2) != 1 and dim > 1:
+        raise ValueError(f"{name}: [rows, {heads}, {dim}], last dimension contiguous")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * dim, t.stride(1) if heads > 1 else dim
+
+
+def _check_table(page_table):
+    """(row stride, rows, columns)."""
+    if page_table.dtype != torch.int32 or page_table.dim() != 2:
+        raise ValueError("page_table: int32 [B, pages]")
+    B, P = page_table.shape
+    _need_int32(B, P)
+    if P > 1 and page_table.stride(1) != 1 or B > 1 and page_table.stride(0) < P:
+        raise ValueError("page_table's last dimension must be contiguous, its rows must not overlap")
+    return page_table.stride(0) if B > 1 else P, B, P
+
+
+def _check_list(t, name, n):
+    _need(t.dtype == torch.int32 and t.shape == (n,) and t.is_contiguous(), f"{name}: contiguous int32 [{n}]")
+
+
 class PagedCache:
     """A paged cache of keys and values (or one plane, v_dim=0) held in a block format.
 
@@ -358,3 +386,155 @@ class PagedCache:
         _need(rows is None or rows == k_out.shape[0], "rows must be the outputs' rows")
         _call(self._gpu, "mxfp4_cache_read", self._dref, *self._memory(), k_out.shape[0], *index, *planes)
         return k_out, v_out
+
+    def attend(self, q, page_table, cu_rows, start=None, tree_mask=None, scale=None, out=None, out_dtype=torch.bfloat16):
+        """Attention of rows whose keys and values `write` has put into the cache, with the same cu_rows, start and
+        page_table: one new token a sequence, a chunk of a prompt, or a tree of drafted tokens.
+
+        q bf16 [rows, q_heads, k_dim] (q_heads a multiple of heads; rows and heads may be strided, by multiples of 8
+        elements, and start on 16 bytes).  A row sees the positions below its sequence's start, and of the sequence's own
+        rows those up to itself, or with tree_mask (bool or uint8 [rows, W], rows may be strided) those j < W with
+        tree_mask[row, j] set: j counts from the sequence's first row.  Positions without a page are not seen.  scale
+        (None: k_dim ** -0.5) multiplies the scores.  Returns [rows, q_heads, v_dim] in out_dtype (bfloat16 or float32);
+        a row that sees nothing gets zeros.  Rows outside every sequence are undefined, or in `out` (strided like q)
+        left as they were.  Forward only: a q that asks for a gradient is refused."""
+        _gpu_of("the cache", self._storage[0], q, page_table, cu_rows, start, tree_mask, out)
+        if torch.is_grad_enabled() and q.requires_grad:
+            raise ValueError("attend has no backward pass: detach q, or call it under torch.no_grad()")
+        index = self._index(page_table, cu_rows, start)
+        _need(self._v_dim > 0, "attend needs a cache with keys and values (v_dim > 0)")
+        _need(q.dtype == torch.bfloat16 and q.dim() == 3, f"q: bf16 [rows, q_heads, {self._k_dim}]")
+        rows, q_heads = q.shape[:2]
+        _need(q_heads > 0 and q_heads % self._heads == 0, "q_heads must be a multiple of the cache's heads")
+        q_args = _vectors(q, "q", q_heads, self._k_dim)
+        if out is None:
+            out_fp32 = _check_out(out_dtype)
+            out = torch.empty((rows, q_heads, self._v_dim), dtype=out_dtype, device=self._device)
+        else:
+            out_fp32 = _check_out(out.dtype)
+            _need(out.shape[0] == rows, "out must have q's rows")
+        mask, ld_mask, W = None, 0, 0
+        if tree_mask is not None:
+            _need(tree_mask.dtype in (torch.bool, torch.uint8) and tree_mask.dim() == 2 and tree_mask.shape[0] == rows,
+                  "tree_mask: bool or uint8 [rows, W]")
+            W = tree_mask.shape[1]
+            _need_int32(W)
+            _need(W <= 1 or tree_mask.stride(1) == 1, "tree_mask's last dimension must be contiguous")
+            ld_mask = tree_mask.stride(0) if rows > 1 else W
+            _need(ld_mask >= W, "tree_mask's rows must not overlap")
+            # a mask without columns hides all drafts: it must not become the absent mask
+            mask = tree_mask.data_ptr() or q.data_ptr()
+        scale = self._k_dim ** -0.5 if scale is None else scale
+        nws = _attend_workspace(self._dims.fmt, self._heads, self._k_dim, self._v_dim, q_heads, rows, index[4])
+        if nws == 0:
+            raise ValueError("invalid attention arguments (k_dim and v_dim are at most 256)")
+        ws = torch.empty(nws, dtype=torch.uint8, device=self._device)
+        _call(self._gpu, "mxfp4_cache_attend", self._dref, *self._memory(), *q_args, q_heads, rows, *index, mask, ld_mask, W,
+              scale, *_vectors(out, "out", q_heads, self._v_dim), out_fp32, ws.data_ptr(), nws)
+        return out
+
+    def compact(self, page_table, start, path):
+        """Moves the accepted drafts of each sequence together: position start[b] + i takes what position
+        start[b] + path[b, i] held.  path int32 [B, W] (rows may be strided): indices of accepted drafts in increasing
+        order, ended by a negative entry, by one that does not increase, or by the last column; start int32 [B] as in
+        `write`.  Returns the new lengths int32 [B], start + the number of accepted drafts.  Positions without a page are
+        passed over.  Sequences must not share the pages that drafts lie in (`PagePool` gives each its own)."""
+        gpu = _gpu_of("the cache", self._storage[0], page_table, start, path)
+        ld, B, P = _check_table(page_table)
+        _check_list(start, "start", B)
+        _need(path.dtype == torch.int32 and path.dim() == 2 and path.shape[0] == B, "path: int32 [B, W]")
+        W = path.shape[1]
+        _need_int32(W)
+        _need(W <= 1 or path.stride(1) == 1, "path's last dimension must be contiguous")
+        ld_path = path.stride(0) if B > 1 else W
+        _need(ld_path >= W, "path's rows must not overlap")
+        lengths = torch.empty(B, dtype=torch.int32, device=self._device)
+        _call(gpu, "mxfp4_cache_compact", self._dref, start.data_ptr(), path.data_ptr(), ld_path, W, page_table.data_ptr(),
+              ld, B, P, lengths.data_ptr(), *self._memory())
+        return lengths
+
+    def copy_pages(self, src, dst, rows=None):
+        """Copies the first rows[i] tokens (None: all) of page src[i] to page dst[i]; all int32 [n].  A pair with a page
+        outside the cache is passed over.  A destination must not be in the lists a second time."""
+        gpu = _gpu_of("the cache", self._storage[0], src, dst, rows)
+        n = src.shape[0] if src.dim() == 1 else -1
+        _need_int32(n)
+        for t, name in ((src, "src"), (dst, "dst"), (rows, "rows")):
+            if t is not None:
+                _check_list(t, name, n)
+        _call(gpu, "mxfp4_cache_copy_pages", self._dref, src.data_ptr(), dst.data_ptr(), _ptr(rows), n, *self._memory())
+
+
+# ------------------------------------------------------------------------------------------------
+# Page pool.
+
+
+@functools.lru_cache(maxsize=256)
+def _pool_workspace(num_pages, n, columns):
+    return _lib.lib().mxfp4_pool_workspace_bytes(num_pages, n, columns)
+
+
+class PagePool:
+    """Which pages of one or more caches are in use (a model's layers share page tables, and so a pool), on the device.
+
+    refs int32 [num_pages]: how many rows of the page tables hold each page, 0: free; zeros, or given where pages are
+    held already.  A row of a page table holds its leading entries in [0, num_pages); the others are -1.  Free pages are
+    handed out in increasing order, to rows in increasing order.  Tables and refs are changed in place, and all caches'
+    pages that have to be copied are.  Calls on one pool must be ordered (one stream)."""
+
+    def __init__(self, *caches, refs=None):
+        _need(len(caches) > 0 and all(isinstance(c, PagedCache) for c in caches), "give the caches whose pages are pooled")
+        d = caches[0].dims
+        for c in caches[1:]:
+            other = c.dims
+            _need((other.num_pages, other.page_size) == (d.num_pages, d.page_size),
+                  "the caches must have the same number of pages and page size")
+        self._caches, self._pages, self._page_size = caches, d.num_pages, d.page_size
+        device = caches[0].k_q.device
+        if refs is None:
+            refs = torch.zeros(d.num_pages, dtype=torch.int32, device=device)
+        _check_list(refs, "refs", d.num_pages)
+        self._refs = refs
+        self._gpu = _gpu_of("the cache", *(c.k_q for c in caches), refs)
+        self._device = device
+
+    # what the kernels' bounds were checked against: read only
+    refs = property(lambda self: self._refs)
+    caches = property(lambda self: self._caches)
+
+    def _change(self, fn, page_table, n, lists):
+        ld, B, P = _check_table(page_table)
+        nws = _pool_workspace(self._pages, n, P)
+        if nws == 0:
+            raise ValueError("invalid page pool arguments")
+        ws = torch.empty(nws, dtype=torch.uint8, device=self._device)
+        # copies [3, n] and missing
+        made = torch.empty(3 * n + 1, dtype=torch.int32, device=self._device)
+        copies = made.data_ptr()
+        _call(self._gpu, fn, self._pages, self._page_size, self._refs.data_ptr(), page_table.data_ptr(), ld, B, P, *lists,
+              copies, copies + 12 * n, ws.data_ptr(), nws)
+        for c in self._caches:
+            _call(self._gpu, "mxfp4_cache_copy_pages", c._dref, copies, copies + 4 * n, copies + 8 * n, n, *c._memory())
+        return made[3 * n]
+
+    def resize(self, page_table, lengths):
+        """Row b of page_table (int32 [B, pages]) then holds the pages of lengths[b] tokens (int32 [B]; negative: the row
+        is left alone; as many pages as the table has columns at most): pages are taken, or given back (0: all).  Where
+        the length ends inside a page that the row shares, it gets a copy of its own.  Returns int32, 0-dim: the pages that
+        were wanted when none was free; their entries are -1, where `write` and `attend` pass over them."""
+        _gpu_of("the cache", self._refs, page_table, lengths)
+        n = page_table.shape[0] if page_table.dim() == 2 else 0
+        _check_list(lengths, "lengths", n)
+        return self._change("mxfp4_pool_resize", page_table, n, (lengths.data_ptr(),))
+
+    def fork(self, page_table, src, dst, lengths):
+        """Row dst[i] of page_table gives its pages back and continues from the first lengths[i] tokens of row src[i]
+        (all int32 [n]): whole pages are shared, the last one is copied where they end inside it.  A pair is passed over
+        when a row is outside the table, the length is negative, dst[i] is a source too, or an earlier pair has it.
+        Returns as `resize`."""
+        _gpu_of("the cache", self._refs, page_table, src, dst, lengths)
+        n = src.shape[0] if src.dim() == 1 else -1
+        _need_int32(n)
+        for t, name in ((src, "src"), (dst, "dst"), (lengths, "lengths")):
+            _check_list(t, name, n)
+        return self._change("mxfp4_pool_fork", page_table, n, (src.data_ptr(), dst.data_ptr(), lengths.data_ptr(), n))

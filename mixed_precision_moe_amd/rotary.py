@@ -1,0 +1,137 @@
+"""Rotary positions: the torch binding of mxfp4_rotary, and the frequencies of a layer's configuration."""
+
+import math
+
+import torch
+
+from .ops import _call, _gpu_of, _need, _need_int32, _vectors
+
+
+def rotary_frequencies(dim, base=10000.0, scaling=None):
+    """(angle per position of each of the dim / 2 pairs, float64 on the host; factor of the turned vectors).
+
+    base ** (-2 i / dim), changed by `scaling` for contexts that are longer than a model was trained on:
+      None                      as they are
+      kind="linear", factor     divided by factor
+      kind="base", factor       base * factor ** (dim / (dim - 2)): the slowest is divided by factor, the fastest kept
+      kind="ramp", factor, length, fast=32, slow=1, magnitude=1 + 0.1 ln(factor)
+          pairs that turn more than `fast` times over `length` positions are kept, those that turn fewer than `slow`
+          times divided by factor, with a ramp over the pairs between; queries and keys are multiplied by magnitude
+      kind="bands", factor, length, low=1, high=4
+          the same between length / high and length / low positions a turn, with a ramp over the turns themselves"""
+    _need(isinstance(dim, int) and dim >= 2 and dim % 2 == 0, "dim must be even")
+    _need(base > 0, "base must be positive")
+    s = dict(scaling or {})
+    kind, factor = s.pop("kind", None), s.pop("factor", 1.0)
+    _need(factor > 0, "factor must be positive")
+    if kind == "base":
+        _need(dim > 2, "kind='base' needs more than one pair")
+        base = base * factor ** (dim / (dim - 2))
+    f = base ** (-torch.arange(0, dim, 2, dtype=torch.float64) / dim)
+    magnitude = 1.0
+    if kind == "linear":
+        f = f / factor
+    elif kind == "ramp":
+        length, fast, slow = s.pop("length"), s.pop("fast", 32.0), s.pop("slow", 1.0)
+        magnitude = s.pop("magnitude", 1.0 + 0.1 * math.log(factor))
+        # the index of a pair that turns n times over the length
+        pair = lambda n: dim * math.log(length / (2 * math.pi * n)) / (2 * math.log(base))  # noqa: E731
+        low, high = max(0, math.floor(pair(fast))), min(dim - 1, math.ceil(pair(slow)))
+        ramp = ((torch.arange(dim // 2, dtype=torch.float64) - low) / max(high - low, 0.001)).clamp(0, 1)
+        f = f * (1 - ramp) + f / factor * ramp
+    elif kind == "bands":
+        length, low, high = s.pop("length"), s.pop("low", 1.0), s.pop("high", 4.0)
+        _need(high > low, "high must be above low")
+        kept = ((length * f / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
+        f = f * kept + f / factor * (1 - kept)
+    else:
+        _need(kind in (None, "base"), f"unknown scaling {kind!r}")
+    _need(not s, f"unknown scaling options {sorted(s)}")
+    return f, magnitude
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, handle, inverse, positions, *tensors):
+        ctx.handle, ctx.inverse = handle, inverse
+        ctx.save_for_backward(positions)
+        ctx.set_materialize_grads(False)
+        return tuple(handle._apply(tensors, positions, inverse))
+
+    @staticmethod
+    def backward(ctx, *grads):
+        # a rotation's gradient is the rotation back (by the same magnitude), itself differentiable
+        positions, = ctx.saved_tensors
+        given = [g if g.dim() == 3 and g.stride(2) == 1 else g.contiguous() for g in grads if g is not None]
+        back = iter(ctx.handle._turn(given, positions, not ctx.inverse) if given else ())
+        return (None, None, None, *(None if g is None else next(back) for g in grads))
+
+
+class Rotary:
+    """Rotary positions of a layer: its frequencies, on the device.
+
+    Elements [offset, offset + dim) of each head's vector are turned, pair i by positions * frequency i: elements
+    (i, i + dim / 2), or (2i, 2i + 1) with interleaved.  base and scaling as in `rotary_frequencies`, or freqs: the
+    frequencies themselves (float64 [dim / 2], with `magnitude`)."""
+
+    def __init__(self, dim, base=10000.0, *, interleaved=False, offset=0, scaling=None, freqs=None, magnitude=None,
+                 device=None):
+        if freqs is None:
+            freqs, own = rotary_frequencies(dim, base, scaling)
+            magnitude = own if magnitude is None else magnitude
+        else:
+            _need(scaling is None, "scaling changes frequencies that are made here: give it, or freqs")
+            freqs = torch.as_tensor(freqs, dtype=torch.float64)
+            _need(dim % 2 == 0 and freqs.shape == (dim // 2,), "freqs: one for each pair")
+        _need(2 <= dim <= 2048 and offset >= 0, "2 <= dim <= 2048, offset >= 0")
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        self._turns = (freqs / (2 * math.pi)).to(device).contiguous()
+        self._dim, self._offset, self._interleaved = dim, offset, 1 if interleaved else 0
+        self._magnitude = 1.0 if magnitude is None else float(magnitude)
+        _need(math.isfinite(self._magnitude), "magnitude must be finite")
+
+    def _check(self, t, name):
+        _need(t.dtype in (torch.bfloat16, torch.float32) and t.dim() == 3, f"{name}: bf16 or fp32 [rows, heads, head_dim]")
+        _need(t.stride(2) == 1 or t.shape[2] <= 1, f"{name}'s last dimension must be contiguous")
+
+    def _apply(self, tensors, positions, inverse, out=None):
+        first = tensors[0]
+        gpu = _gpu_of("q", first, positions, self._turns, *tensors[1:])
+        rows, dim, dtype = first.shape[0], first.shape[2], first.dtype
+        for t, name in zip(tensors, ("q", "k")):
+            self._check(t, name)
+            _need(t.shape[0] == rows and t.shape[2] == dim and t.dtype == dtype, "q and k must have the same rows, head_dim and dtype")
+            _need(t.shape[1] > 0, f"{name} must have a head")
+        _need_int32(dim, *(t.shape[1] for t in tensors))
+        _need(self._offset + self._dim <= dim, "the turned part must lie inside head_dim")
+        _need(positions.dtype == torch.int32 and positions.shape == (rows,) and positions.is_contiguous(),
+              "positions: contiguous int32 [rows]")
+        out = [torch.empty(t.shape, dtype=dtype, device=t.device) for t in tensors] if out is None else out
+        args = []
+        for t, name, o in zip(tensors, ("q", "k"), out):
+            args += [*_vectors(t, name, t.shape[1], dim), t.shape[1], *_vectors(o, name, t.shape[1], dim)]
+        if len(tensors) == 1:
+            args += [None, 0, 0, 0, None, 0, 0]
+        _call(gpu, "mxfp4_rotary", self._turns.data_ptr(), positions.data_ptr(), rows, dim, self._dim, self._offset,
+              self._interleaved, self._magnitude, 1 if inverse else 0, 1 if dtype == torch.float32 else 0, *args)
+        return out
+
+    def _turn(self, tensors, positions, inverse):
+        if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
+            return _Rotary.apply(self, inverse, positions, *tensors)
+        return self._apply(tensors, positions, inverse)
+
+    def __call__(self, q, k, positions, inplace=False):
+        """q [rows, q_heads, head_dim] and k [rows, k_heads, head_dim] (or None), bf16 or fp32, rows and heads strided as
+        they like; positions int32 [rows].  Returns both turned (contiguous), differentiable in q and k any number of
+        times; with inplace, in their own memory (not where a gradient is asked for; the elements outside the turned part
+        are then not touched).  To capture the backward pass into a graph, drop every eager autograd graph of the same
+        leaves first, as torch asks for any backward pass."""
+        tensors = (q,) if k is None else (q, k)
+        if inplace:
+            _need(not (torch.is_grad_enabled() and any(t.requires_grad for t in tensors)),
+                  "inplace has no backward pass: detach q and k, or call it under torch.no_grad()")
+            out = self._apply(tensors, positions, False, out=tensors)
+        else:
+            out = self._turn(tensors, positions, False)
+        return out[0], None if k is None else out[1]
