@@ -10,6 +10,7 @@ namespace {
 
 constexpr int kMaxDim = 256;        // attention: k_dim, v_dim
 constexpr int kMaxHeads = 1 << 16;
+constexpr int kCus = 256;
 constexpr int kMaxRot = 2048;
 constexpr int kMaxTableRows = 1 << 24;
 constexpr int kMaxPairs = 1 << 16;  // of a fork
@@ -86,6 +87,28 @@ int pool_args(PoolArgs& a, int64_t num_pages, int32_t page_size, int32_t* refs, 
   return MXFP4_OK;
 }
 
+// The sizes of the attention kernels: dims up to 64, 128, 192 and 128, or 256; tiles of 16 to 64 rows (256: to 32), the
+// smallest that holds what a sequence has on average.
+AttendPlan attend_plan(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows, int32_t n_seqs) {
+  AttendPlan p = {};
+  const int k = d->k_dim, v = d->v_dim;
+  p.dk = k <= 64 && v <= 64 ? 64 : k <= 128 && v <= 128 ? 128 : k <= 192 && v <= 128 ? 192 : 256;
+  p.dv = p.dk == 192 ? 128 : p.dk;
+  const int64_t per_seq = (rows + n_seqs - 1) / (n_seqs > 0 ? n_seqs : 1) * (q_heads / d->heads);
+  const int64_t nt = (per_seq + 15) / 16, most = p.dk == 256 ? 2 : 4;
+  p.nt = (int32_t)(nt < 1 ? 1 : nt > most ? most : nt);
+  const int64_t fill = (int64_t)kCus * attend_waves(p.dk, p.nt) / d->heads;
+  p.workers = (int32_t)(fill < 1 ? 1 : fill);
+  uint64_t at = 0;
+  auto take = [&](uint64_t bytes) { uint64_t o = at; at = up256(at + bytes); return o; };
+  const uint64_t all = (uint64_t)p.workers * (uint64_t)d->heads, part_rows = 2 * all * 16 * (uint64_t)p.nt;
+  p.part = take(4 * part_rows * (uint64_t)p.dv);
+  p.ml = take(8 * part_rows);
+  p.open = take(16 * all);
+  p.total = at;
+  return p;
+}
+
 int check_attend(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows, int32_t n_seqs) {
   int st = check_cache(d, true);
   if (st) return st;
@@ -103,7 +126,7 @@ int check_attend(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows, int32
 MX_API size_t mxfp4_cache_attend_workspace_bytes(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows,
                                                  int32_t n_seqs) {
   if (check_attend(d, q_heads, rows, n_seqs) != MXFP4_OK) return 0;
-  return (size_t)attend_workspace(d, q_heads, rows, n_seqs);
+  return (size_t)attend_plan(d, q_heads, rows, n_seqs).total;
 }
 
 MX_API int mxfp4_cache_attend(const mxfp4_cache_dims* d, const void* k_q, const void* k_s, const void* v_q,
@@ -129,7 +152,8 @@ MX_API int mxfp4_cache_attend(const mxfp4_cache_dims* d, const void* k_q, const 
   if (!aligned(q_bf16, 16) || !aligned(out, 16) || !aligned(k_q, 8) || !aligned(v_q, 8) || !aligned(cu_rows, 4) ||
       !aligned(start, 4) || !aligned(page_table, 4) || !aligned(workspace, 256))
     return MXFP4_ERR_ALIGN;
-  if (workspace_bytes < attend_workspace(d, q_heads, rows, n_seqs)) return MXFP4_ERR_WORKSPACE;
+  const AttendPlan plan = attend_plan(d, q_heads, rows, n_seqs);
+  if (workspace_bytes < plan.total) return MXFP4_ERR_WORKSPACE;
   AttendArgs a = {};
   CacheArgs& c = a.cache;
   c.plane[0] = CachePlane{(void*)q_bf16, q_ldt, q_ldh, (uint8_t*)k_q, (uint8_t*)k_s, d->k_dim, d->k_global_scale};
@@ -147,10 +171,13 @@ MX_API int mxfp4_cache_attend(const mxfp4_cache_dims* d, const void* k_q, const 
   a.mask = tree_mask;
   a.ld_mask = ld_mask;
   a.mask_cols = mask_cols;
-  a.q_heads = q_heads;
+  a.group = q_heads / d->heads;
   a.out_fp32 = out_is_fp32;
   a.scale = scale;
-  return launch_attend(d->fmt, a, workspace, S(stream));
+  uint8_t* ws = (uint8_t*)workspace;
+  if (d->fmt == MXFP4_FMT_MXFP4) return launch_attend_mxfp4(a, plan, ws, S(stream));
+  if (d->fmt == MXFP4_FMT_NVFP4) return launch_attend_nvfp4(a, plan, ws, S(stream));
+  return launch_attend_mxfp8(a, plan, ws, S(stream));
 }
 
 // ------------------------------------------------------------------------------------------------

@@ -11,11 +11,20 @@ struct AttendArgs {
   CacheArgs cache;  // plane[0].rows: q (bf16) and its strides, plane[1].rows: out and its strides
   const uint8_t* mask;
   int64_t ld_mask;
-  int32_t mask_cols, q_heads, out_fp32;
+  int32_t mask_cols, group, out_fp32;  // group: query heads of a key head
   float scale;
 };
-uint64_t attend_workspace(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows, int32_t n_seqs);
-int launch_attend(int fmt, const AttendArgs& a, void* workspace, hipStream_t stream);
+// How a call is cut up: tiles of 16 nt rows, elements of a key and a value in the kernel, workers of each head; the
+// workspace's parts.
+struct AttendPlan {
+  int32_t nt, dk, dv, workers;
+  uint64_t part, ml, open, total;
+};
+// Workgroups of a compute unit: what their registers leave room for.
+constexpr int attend_waves(int dk, int nt) { return dk <= 128 ? (nt == 1 ? 3 : nt == 2 ? 2 : 1) : nt == 1 ? 2 : 1; }
+int launch_attend_mxfp4(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream);
+int launch_attend_nvfp4(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream);
+int launch_attend_mxfp8(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream);
 
 // A plane of bytes: `row` bytes a token, moved in units of `unit` bytes.
 struct BytePlane {
