@@ -405,6 +405,7 @@ class PagedCache:
         _need(self._v_dim > 0, "attend needs a cache with keys and values (v_dim > 0)")
         _need(q.dtype == torch.bfloat16 and q.dim() == 3, f"q: bf16 [rows, q_heads, {self._k_dim}]")
         rows, q_heads = q.shape[:2]
+        _need_int32(q_heads)
         _need(q_heads > 0 and q_heads % self._heads == 0, "q_heads must be a multiple of the cache's heads")
         q_args = _vectors(q, "q", q_heads, self._k_dim)
         if out is None:

@@ -56,7 +56,7 @@ class _Rotary(torch.autograd.Function):
         ctx.handle, ctx.inverse = handle, inverse
         ctx.save_for_backward(positions)
         ctx.set_materialize_grads(False)
-        return tuple(handle._apply(tensors, positions, inverse))
+        return handle._apply(tensors, positions, inverse)
 
     @staticmethod
     def backward(ctx, *grads):
@@ -90,31 +90,35 @@ class Rotary:
         self._magnitude = 1.0 if magnitude is None else float(magnitude)
         _need(math.isfinite(self._magnitude), "magnitude must be finite")
 
-    def _check(self, t, name):
-        _need(t.dtype in (torch.bfloat16, torch.float32) and t.dim() == 3, f"{name}: bf16 or fp32 [rows, heads, head_dim]")
-        _need(t.stride(2) == 1 or t.shape[2] <= 1, f"{name}'s last dimension must be contiguous")
-
     def _apply(self, tensors, positions, inverse, out=None):
-        first = tensors[0]
-        gpu = _gpu_of("q", first, positions, self._turns, *tensors[1:])
-        rows, dim, dtype = first.shape[0], first.shape[2], first.dtype
-        for t, name in zip(tensors, ("q", "k")):
-            self._check(t, name)
-            _need(t.shape[0] == rows and t.shape[2] == dim and t.dtype == dtype, "q and k must have the same rows, head_dim and dtype")
-            _need(t.shape[1] > 0, f"{name} must have a head")
-        _need_int32(dim, *(t.shape[1] for t in tensors))
+        q, k = tensors if len(tensors) == 2 else (tensors[0], None)
+        gpu = _gpu_of("q", q, positions, self._turns, k)
+        dtype = q.dtype
+        _need(dtype == torch.bfloat16 or dtype == torch.float32, "q and k: bf16 or fp32")
+        _need(q.dim() == 3 and (k is None or k.dim() == 3), "q and k: [rows, heads, head_dim]")
+        rows, heads, dim = q.shape
+        if (dim | heads) >> 31:
+            _need_int32(dim, heads)
+        _need(heads > 0, "q must have a head")
         _need(self._offset + self._dim <= dim, "the turned part must lie inside head_dim")
         _need(positions.dtype == torch.int32 and positions.shape == (rows,) and positions.is_contiguous(),
               "positions: contiguous int32 [rows]")
-        out = [torch.empty(t.shape, dtype=dtype, device=t.device) for t in tensors] if out is None else out
-        args = []
-        for t, name, o in zip(tensors, ("q", "k"), out):
-            args += [*_vectors(t, name, t.shape[1], dim), t.shape[1], *_vectors(o, name, t.shape[1], dim)]
-        if len(tensors) == 1:
+        q_out = torch.empty((rows, heads, dim), dtype=dtype, device=q.device) if out is None else out[0]
+        args = [*_vectors(q, "q", heads, dim), heads, *_vectors(q_out, "q", heads, dim)]
+        if k is None:
             args += [None, 0, 0, 0, None, 0, 0]
+            made = (q_out,)
+        else:
+            k_heads = k.shape[1]
+            _need_int32(k_heads)
+            _need(k.dtype == dtype and k.shape[0] == rows, "q and k must have the same rows and dtype")
+            _need(k_heads > 0, "k must have a head")
+            k_out = torch.empty((rows, k_heads, dim), dtype=dtype, device=q.device) if out is None else out[1]
+            args += [*_vectors(k, "k", k_heads, dim), k_heads, *_vectors(k_out, "k", k_heads, dim)]
+            made = (q_out, k_out)
         _call(gpu, "mxfp4_rotary", self._turns.data_ptr(), positions.data_ptr(), rows, dim, self._dim, self._offset,
               self._interleaved, self._magnitude, 1 if inverse else 0, 1 if dtype == torch.float32 else 0, *args)
-        return out
+        return made
 
     def _turn(self, tensors, positions, inverse):
         if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
