@@ -20,6 +20,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "cache_slots.h"
 #include "drafts.h"
 
@@ -145,6 +147,10 @@ MX_DEV int64_t shfl64(int64_t v, int lane) {
   const int lo = __shfl((int)v, lane), hi = __shfl((int)(v >> 32), lane);
   return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
 }
+MX_DEV int64_t lane64(int64_t v, int lane) {  // the same for the whole wave, and known to be
+  const int lo = __builtin_amdgcn_readlane((int)v, lane), hi = __builtin_amdgcn_readlane((int)(v >> 32), lane);
+  return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
+}
 MX_DEV int64_t shfl64_up(int64_t v, int by) {
   const int lo = __shfl_up((int)v, by), hi = __shfl_up((int)(v >> 32), by);
   return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
@@ -210,11 +216,14 @@ struct Shape {
   static constexpr int kSums = DV + 4;     // of the joined sums' rows
 };
 
-template <int FMT, int DK, int DV, int NT, int WAVES>
+// PAGED: pages of whole tiles, and dimensions that are DK and DV.  A tile's page is then looked up once, and a lane's part
+// of the addresses does not change from tile to tile.
+template <int FMT, int DK, int DV, int NT, int WAVES, bool PAGED>
 __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, float* __restrict__ part,
                                                                  float2* __restrict__ part_ml, Open* __restrict__ open,
                                                                  int workers) {
   using Sh = Shape<FMT, DK, DV, NT>;
+  using Found = std::conditional_t<PAGED, int32_t, int64_t>;
   constexpr int MT = Sh::kRows;
   constexpr int kBytes = kWaves * kTile * Sh::kStride * 2;
   static_assert(MT * Sh::kSums * 4 <= kBytes, "the sums take the place of V");
@@ -222,13 +231,22 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, f
   __shared__ float ms[kWaves][MT], ls[kWaves][MT];
   const CacheArgs& c = a.cache;
   const CachePlane &pk = c.plane[0], &pv = c.plane[1];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, kg = lane >> 4;
-  const int g = blockIdx.x % c.heads, worker = blockIdx.x / c.heads;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, kg = lane >> 4;
+  // Workgroups go to the eight XCDs in turn: a worker's heads, which read pieces of the same tokens, share one.
+  int g, worker;
+  if (workers % 8 == 0) {
+    const int i = blockIdx.x / 8;
+    g = i % c.heads;
+    worker = i / c.heads * 8 + blockIdx.x % 8;
+  } else {
+    g = blockIdx.x % c.heads;
+    worker = blockIdx.x / c.heads;
+  }
   const int64_t at_worker = (int64_t)g * workers + worker;  // as the join counts them
 
   // this worker's units
   int64_t all = 0;
-  for (int b = 0; b < c.n_seqs; b += 64) all += shfl64(scan_units(a, b, lane, MT), 63);
+  for (int b = 0; b < c.n_seqs; b += 64) all += lane64(scan_units(a, b, lane, MT), 63);
   const int64_t used = min((int64_t)workers, all);
   if (threadIdx.x == 0) open[at_worker] = Open{0, 0, -1};
   if (worker >= used) return;
@@ -243,10 +261,10 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, f
     if (past) {
       const int l = __ffsll((unsigned long long)past) - 1;
       b = b0 + l;
-      if (l > 0) item = shfl64(sums, l - 1);
+      if (l > 0) item = lane64(sums, l - 1);
       break;
     }
-    item = shfl64(sums, 63);
+    item = lane64(sums, 63);
   }
   Seq s = sequence(a, b);
   int64_t tile = 0, units = tile_units(a, s, 0, MT), tiles = tiles_of(a, s, MT);
@@ -260,11 +278,14 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, f
     }
   }
 
-  const float sc = (a.scale == 0.0f ? 1.0f : fabsf(a.scale)) * 1.44269504f / (FMT == MXFP4_FMT_NVFP4 ? pk.gs : 1.0f);
+  // not 0, so that its product with a hidden position's -inf is one
+  const float sc = fmaxf((a.scale == 0.0f ? 1.0f : fabsf(a.scale)) * 1.44269504f / (FMT == MXFP4_FMT_NVFP4 ? pk.gs : 1.0f), 1e-38f);
+  const float per_sc = 1.0f / sc;
   // the scale's sign goes to q; with a scale of 0 all of it is 0
   const uint32_t q_and = a.scale == 0.0f ? 0u : ~0u, q_xor = a.scale < 0.0f ? 0x80008000u : 0u;
-  const int64_t k_bytes = pk.dim / kPerByte<FMT>, v_bytes = pv.dim / kPerByte<FMT>;
-  const int k_blocks = pk.dim / kBlock<FMT>, v_blocks = pv.dim / kBlock<FMT>;
+  const int k_dim = PAGED ? DK : pk.dim, v_dim = PAGED ? DV : pv.dim;
+  const int64_t k_bytes = k_dim / kPerByte<FMT>, v_bytes = v_dim / kPerByte<FMT>;
+  const int k_blocks = k_dim / kBlock<FMT>, v_blocks = v_dim / kBlock<FMT>;
   uint16_t* const vt = (uint16_t*)lds + wave * kTile * Sh::kStride;
 
   int64_t u = u0;
@@ -273,130 +294,161 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, f
     const int64_t end = tile_end(a, s, tile, MT);
     // the rows of this lane's columns
     bf16x8_t q[NT][Sh::kSteps];
-    int64_t row[NT];
-    int32_t draft[NT];
+    int32_t draft[NT];  // -1: no such row
 #pragma unroll
     for (int n = 0; n < NT; n++) {
       const int64_t r = tile * MT + 16 * n + col;
       const int64_t d = r / a.group;
       draft[n] = d < s.rows ? (int32_t)d : -1;
-      row[n] = s.first + d;
-      const uint16_t* src = (const uint16_t*)pk.rows + row[n] * pk.ldt + (g * a.group + (r - d * a.group)) * pk.ldh;
+      const uint16_t* src = (const uint16_t*)pk.rows + (s.first + d) * pk.ldt + (g * a.group + (r - d * a.group)) * pk.ldh;
 #pragma unroll
       for (int i = 0; i < Sh::kSteps; i++) {
         const int e = kg * Sh::kQuarter + 8 * i;
         u32x4_t x = {0, 0, 0, 0};
-        if (draft[n] >= 0 && e < pk.dim) x = *reinterpret_cast<const u32x4_t*>(src + e);
+        if (draft[n] >= 0 && e < k_dim) x = *reinterpret_cast<const u32x4_t*>(src + e);
 #pragma unroll
         for (int j = 0; j < 4; j++) x[j] = (x[j] & q_and) ^ q_xor;
         q[n][i] = __builtin_bit_cast(bf16x8_t, x);
       }
     }
-    f32x4_t o[NT][Sh::kVT];
-    float m[NT], l[NT];
+    // sums, of the weights too; the exponents' subtrahend m, and the score from which on it is raised
+    f32x4_t o[NT][Sh::kVT], l[NT];
+    float m[NT], limit[NT];
 #pragma unroll
     for (int n = 0; n < NT; n++) {
-      m[n] = -INFINITY;
-      l[n] = 0.0f;
+      m[n] = limit[n] = -INFINITY;
+      l[n] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
       for (int v = 0; v < Sh::kVT; v++) o[n][v] = f32x4_t{0, 0, 0, 0};
     }
 
-    // the cache's vector of position 32 * tile + (lane & 31), -1: none
-    auto find = [&](int64_t k) {
-      const int64_t pos = k * kUnit + wave * kTile + (lane & 31);
-      int64_t vec = -1;
+    // Where a tile's codes are.  PAGED: its page, in every lane; else the cache's vector of each of its positions, -1: none,
+    // in the lanes 0 to 31.
+    const auto find = [&](int64_t k) {
+      const int64_t pos = k * kUnit + wave * kTile + (PAGED ? 0 : lane & 31);
+      Found f = -1;
       if (pos < end) {
-        const uint32_t p = (uint32_t)pos / (uint32_t)c.page_size;
+        const uint32_t p = a.page_shift >= 0 ? (uint32_t)pos >> a.page_shift : (uint32_t)pos / (uint32_t)c.page_size;
         const int32_t page = c.table[(int64_t)b * c.ld_table + p];
-        if (page >= 0 && page < c.num_pages)
-          vec = ((int64_t)page * c.page_size + ((uint32_t)pos - p * (uint32_t)c.page_size)) * c.heads + g;
+        if (PAGED)
+          f = page;
+        else if (page >= 0 && page < c.num_pages)
+          f = ((int64_t)page * c.page_size + ((uint32_t)pos - p * (uint32_t)c.page_size)) * c.heads + g;
       }
-      return vec;
+      return f;
+    };
+    // PAGED: the tile's first vector, -1: none.  Its positions past the end lie in the page too.
+    const auto first_vector = [&](int64_t k, Found f) -> int64_t {
+      const int32_t page = __builtin_amdgcn_readfirstlane((int)f);
+      if (page < 0 || page >= c.num_pages) return -1;
+      const uint32_t pos = (uint32_t)k * kUnit + (uint32_t)wave * kTile;
+      const uint32_t in_page = a.page_shift >= 0 ? pos & (uint32_t)(c.page_size - 1) : pos % (uint32_t)c.page_size;
+      return ((int64_t)page * c.page_size + in_page) * c.heads + g;
     };
     uint32_t kc[2][Sh::kCodes], ks[2][Sh::kScales];
-    auto load_k = [&](int64_t vec) {
+    // a lane's quarter of a key, from the key's codes and scales
+    const auto load_key = [&](int t, const uint8_t* src, const uint8_t* scales) {
+      if (PAGED || pk.dim == DK) {
+        if constexpr (Sh::kCodes % 4 == 0) {
 #pragma unroll
-      for (int t = 0; t < 2; t++) {
-        const int64_t at = shfl64(vec, 16 * t + col);
-#pragma unroll
-        for (int i = 0; i < Sh::kCodes; i++) kc[t][i] = 0;
-#pragma unroll
-        for (int i = 0; i < Sh::kScales; i++) ks[t][i] = 0;
-        if (at < 0) continue;
-        const uint8_t* src = pk.q + at * k_bytes;
-        if (pk.dim == DK) {
-          src += kg * (Sh::kCodes * 4);
-          if constexpr (Sh::kCodes % 4 == 0) {
-#pragma unroll
-            for (int i = 0; i < Sh::kCodes; i += 4) {
-              const u32x4_t x = *reinterpret_cast<const u32x4_a8*>(src + 4 * i);
-              kc[t][i] = x[0];
-              kc[t][i + 1] = x[1];
-              kc[t][i + 2] = x[2];
-              kc[t][i + 3] = x[3];
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < Sh::kCodes; i += 2) {
-              const u32x2_t x = *reinterpret_cast<const u32x2_a8*>(src + 4 * i);
-              kc[t][i] = x[0];
-              kc[t][i + 1] = x[1];
-            }
+          for (int i = 0; i < Sh::kCodes; i += 4) {
+            const u32x4_t x = *reinterpret_cast<const u32x4_a8*>(src + kg * (Sh::kCodes * 4) + 4 * i);
+            kc[t][i] = x[0];
+            kc[t][i + 1] = x[1];
+            kc[t][i + 2] = x[2];
+            kc[t][i + 3] = x[3];
           }
         } else {
-          constexpr int per = FMT == MXFP4_FMT_MXFP8 ? 2 : 1;  // registers of eight codes
 #pragma unroll
-          for (int i = 0; i < Sh::kSteps; i++) {
-            const int e = kg * Sh::kQuarter + 8 * i;
-            if (e >= pk.dim) continue;
-#pragma unroll
-            for (int j = 0; j < per; j++)
-              kc[t][per * i + j] = *reinterpret_cast<const uint32_t*>(src + e / kPerByte<FMT> + 4 * j);
+          for (int i = 0; i < Sh::kCodes; i += 2) {
+            const u32x2_t x = *reinterpret_cast<const u32x2_a8*>(src + kg * (Sh::kCodes * 4) + 4 * i);
+            kc[t][i] = x[0];
+            kc[t][i + 1] = x[1];
           }
         }
-        const int b0 = kg * Sh::kQuarter / kBlock<FMT>;
+      } else {
+        constexpr int per = FMT == MXFP4_FMT_MXFP8 ? 2 : 1;  // registers of eight codes
 #pragma unroll
-        for (int i = 0; i < Sh::kScales; i++)
-          if (b0 + i < k_blocks) ks[t][i] = pk.s[at * k_blocks + b0 + i];
+        for (int i = 0; i < Sh::kSteps; i++) {
+          const int e = kg * Sh::kQuarter + 8 * i;
+#pragma unroll
+          for (int j = 0; j < per; j++) {
+            kc[t][per * i + j] = 0;
+            if (e < pk.dim) kc[t][per * i + j] = *reinterpret_cast<const uint32_t*>(src + e / kPerByte<FMT> + 4 * j);
+          }
+        }
+      }
+      const int b0 = kg * Sh::kQuarter / kBlock<FMT>;
+#pragma unroll
+      for (int i = 0; i < Sh::kScales; i++) {
+        ks[t][i] = 0;
+        if (PAGED || b0 + i < k_blocks) ks[t][i] = scales[b0 + i];
+      }
+    };
+    const auto load_k = [&](int64_t k, Found f) {
+      const int64_t first = PAGED ? first_vector(k, f) : 0;
+#pragma unroll
+      for (int t = 0; t < 2; t++) {
+        if (PAGED) {
+          const uint32_t key = (uint32_t)(16 * t + col) * (uint32_t)c.heads;
+          if (first >= 0) load_key(t, pk.q + first * k_bytes + key * (uint32_t)k_bytes, pk.s + first * k_blocks + key * (uint32_t)k_blocks);
+        } else {
+          const int64_t at = shfl64(f, 16 * t + col);
+          if (at >= 0) load_key(t, pk.q + at * k_bytes, pk.s + at * k_blocks);
+        }
       }
     };
     u32x4_t vc[Sh::kPieces];
     uint32_t vs[Sh::kPieces][Sh::kPieceScales];
-    auto load_v = [&](int64_t vec) {
+    const auto load_piece = [&](int i, int piece, const uint8_t* src, const uint8_t* scales) {
+      const int e = piece * Sh::kElems;
+      if (PAGED || e + Sh::kElems <= pv.dim) {
+        vc[i] = *reinterpret_cast<const u32x4_a8*>(src + 16 * piece);
+      } else if (e < pv.dim) {
+        const u32x2_t x = *reinterpret_cast<const u32x2_a8*>(src + 16 * piece);
+        vc[i] = u32x4_t{x[0], x[1], 0, 0};
+      }
+      const int b0 = e / kBlock<FMT>;
+#pragma unroll
+      for (int j = 0; j < Sh::kPieceScales; j++)
+        if (PAGED || b0 + j < v_blocks) vs[i][j] = scales[b0 + j];
+    };
+    const auto load_v = [&](int64_t k, Found f) {
+      const int64_t first = PAGED ? first_vector(k, f) : 0;
 #pragma unroll
       for (int i = 0; i < Sh::kPieces; i++) {
-        const int id = i * 64 + lane, piece = id % Sh::kPerKey;
-        const int64_t at = shfl64(vec, id / Sh::kPerKey);
-        vc[i] = u32x4_t{0, 0, 0, 0};
+        const int id = i * 64 + lane, key = id / Sh::kPerKey, piece = id % Sh::kPerKey;
+        if (!PAGED) {
+          vc[i] = u32x4_t{0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < Sh::kPieceScales; j++) vs[i][j] = 0;
-        const int e = piece * Sh::kElems;
-        if (at < 0 || e >= pv.dim) continue;
-        const uint8_t* src = pv.q + at * v_bytes + 16 * piece;
-        if (e + Sh::kElems <= pv.dim) {
-          vc[i] = *reinterpret_cast<const u32x4_a8*>(src);
-        } else {
-          const u32x2_t x = *reinterpret_cast<const u32x2_a8*>(src);
-          vc[i][0] = x[0];
-          vc[i][1] = x[1];
+          for (int j = 0; j < Sh::kPieceScales; j++) vs[i][j] = 0;
         }
-        const int b0 = e / kBlock<FMT>;
-#pragma unroll
-        for (int j = 0; j < Sh::kPieceScales; j++)
-          if (b0 + j < v_blocks) vs[i][j] = pv.s[at * v_blocks + b0 + j];
+        if (PAGED) {
+          const uint32_t by = (uint32_t)key * (uint32_t)c.heads;
+          if (first >= 0) load_piece(i, piece, pv.q + first * v_bytes + by * (uint32_t)v_bytes, pv.s + first * v_blocks + by * (uint32_t)v_blocks);
+        } else {
+          const int64_t at = shfl64(f, key);
+          if (at >= 0) load_piece(i, piece, pv.q + at * v_bytes, pv.s + at * v_blocks);
+        }
       }
     };
 
-    int64_t vec = find(k0);
-    load_k(vec);
-    load_v(vec);
+    Found found = find(k0);
+    load_k(k0, found);
+    load_v(k0, found);
     for (int64_t k = k0; k < k1; k++) {
       const int64_t base = k * kUnit + wave * kTile;
       // which of the tile's positions have a vector, and whether all rows see them all
-      const uint32_t there = (uint32_t)__ballot(vec >= 0);
+      uint32_t there;
+      if (PAGED) {
+        const int32_t page = __builtin_amdgcn_readfirstlane((int)found);
+        const int64_t left = end - base;
+        there = page < 0 || page >= c.num_pages || left <= 0 ? 0u : left >= kTile ? ~0u : (1u << left) - 1;
+      } else {
+        there = (uint32_t)__ballot(found >= 0);
+      }
       const bool whole = there == ~0u && base + kTile <= s.start;
-      const int64_t next = k + 1 < k1 ? find(k + 1) : -1;
+      const Found next = k + 1 < k1 ? find(k + 1) : -1;
 
       f32x4_t sv[NT][2];
 #pragma unroll
@@ -418,14 +470,11 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, f
           for (int n = 0; n < NT; n++) sv[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, q[n][i], sv[n][t], 0, 0, 0);
         }
       }
-      if (k + 1 < k1) load_k(next);
+      if (k + 1 < k1) load_k(k + 1, next);
 
-      uint32_t hidden[NT];  // bit 4 t + i: not seen
-#pragma unroll
-      for (int n = 0; n < NT; n++) hidden[n] = 0;
       if (!whole) {
-        // positions whose values are not finite must not meet the zero weights of rows that do not see them: they count as
-        // zeros, and make the score of rows that do see them NaN
+        // Positions whose values are not finite must not meet the zero weights of rows that do not see them: they count as
+        // zeros, and make the score of rows that do see them NaN.  Those without a page count as zeros.
         uint32_t bad = 0;
         if (base + kTile > s.start) {
 #pragma unroll
@@ -438,68 +487,84 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, f
             for (uint64_t who = __ballot(x); who; who &= who - 1)
               bad |= 1u << ((i * 64 + __ffsll((unsigned long long)who) - 1) / Sh::kPerKey);
           }
-          if (bad) {
+        }
+        if (const uint32_t zero = bad | ~there) {
 #pragma unroll
-            for (int i = 0; i < Sh::kPieces; i++)
-              if (bad >> ((i * 64 + lane) / Sh::kPerKey) & 1) {
-                vc[i] = u32x4_t{0, 0, 0, 0};
+          for (int i = 0; i < Sh::kPieces; i++)
+            if (zero >> ((i * 64 + lane) / Sh::kPerKey) & 1) {
+              vc[i] = u32x4_t{0, 0, 0, 0};
 #pragma unroll
-                for (int j = 0; j < Sh::kPieceScales; j++) vs[i][j] = 0;
-              }
-          }
+              for (int j = 0; j < Sh::kPieceScales; j++) vs[i][j] = 0;
+            }
         }
 #pragma unroll
-        for (int n = 0; n < NT; n++)
+        for (int n = 0; n < NT; n++) {
+          const uint8_t* mask = a.mask + (s.first + draft[n]) * a.ld_mask;
+          const int64_t most = a.mask ? min(s.drafts, a.mask_cols) : (int64_t)draft[n] + 1;  // drafts past it are not seen
 #pragma unroll
-          for (int t = 0; t < 2; t++)
+          for (int t = 0; t < 2; t++) {
+            asm volatile("");  // a few loads of the mask at a time: all at once cost the registers of the loop around
 #pragma unroll
             for (int i = 0; i < 4; i++) {
               const int key = 16 * t + 4 * kg + i;
               const int64_t j = base + key - s.start;
-              bool sees = draft[n] >= 0 && (there >> key & 1);
-              if (sees && j >= 0)
-                sees = a.mask ? j < s.drafts && j < a.mask_cols && a.mask[row[n] * a.ld_mask + j] : j <= draft[n];
-              if (!sees) {
-                hidden[n] |= 1u << (4 * t + i);
+              bool sees = draft[n] >= 0 && (there >> key & 1) && j < most;
+              if (sees && j >= 0 && a.mask) sees = mask[j];
+              if (!sees)
                 sv[n][t][i] = -INFINITY;
-              } else if (bad >> key & 1) {
+              else if (bad >> key & 1)
                 sv[n][t][i] = NAN;
-              }
             }
+          }
+        }
       }
 
-      bf16x8_t p[NT];
+      // m is raised, and all sums with it, where a score is over it by more than 8: weights stay below 2^8, and most tiles
+      // need no maximum over the row's four lanes and no rescaling
+      bool over = false;
 #pragma unroll
       for (int n = 0; n < NT; n++) {
         float top = sv[n][0][0];
 #pragma unroll
         for (int i = 1; i < 8; i++) top = fmaxf(top, sv[n][i >> 2][i & 3]);
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float now = fmaxf(m[n], top * sc);
-        const float use = now > -INFINITY ? now : 0.0f;  // nothing seen yet
-        if (__any(now > m[n])) {
-          const float keep = __builtin_amdgcn_exp2f(m[n] - use);
-          l[n] *= keep;
+        over = over || top > limit[n];
+      }
+      if (__any(over)) {
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+          float top = sv[n][0][0];
+#pragma unroll
+          for (int i = 1; i < 8; i++) top = fmaxf(top, sv[n][i >> 2][i & 3]);
+          top = fmaxf(top, __shfl_xor(top, 16));
+          top = fmaxf(top, __shfl_xor(top, 32));
+          const float now = fmaxf(m[n], top * sc);
+          const float keep = now > -INFINITY ? __builtin_amdgcn_exp2f(m[n] - now) : 1.0f;
+#pragma unroll
+          for (int i = 0; i < 4; i++) l[n][i] *= keep;
 #pragma unroll
           for (int v = 0; v < Sh::kVT; v++)
 #pragma unroll
             for (int i = 0; i < 4; i++) o[n][v][i] *= keep;
           m[n] = now;
+          limit[n] = (now + 8.0f) * per_sc;
         }
+      }
+      // the weights' sum is taken of them as they are rounded, by the matrix instruction
+      const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+      bf16x8_t p[NT];
+#pragma unroll
+      for (int n = 0; n < NT; n++) {
+        const float by = m[n] > -INFINITY ? -m[n] : 0.0f;  // nothing seen yet
         float w[8];
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-          w[i] = __builtin_amdgcn_exp2f(fmaf(sv[n][i >> 2][i & 3], sc, -use));
-          if (hidden[n] >> i & 1) w[i] = 0.0f;
-          l[n] += w[i];
-        }
+        for (int i = 0; i < 8; i++) w[i] = __builtin_amdgcn_exp2f(fmaf(sv[n][i >> 2][i & 3], sc, by));
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
           const bf16x2_t two = __builtin_convertvector(f32x2_t{w[i], w[i + 1]}, bf16x2_t);
           p[n][i] = two[0];
           p[n][i + 1] = two[1];
         }
+        l[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, p[n], l[n], 0, 0, 0);
       }
 
       // V into LDS, a row a position
@@ -514,7 +579,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, f
           *reinterpret_cast<bf16x8_t*>(dst + 8 * j) = x;
         }
       }
-      if (k + 1 < k1) load_v(next);
+      if (k + 1 < k1) load_v(k + 1, next);
       __builtin_amdgcn_wave_barrier();
       // two blocks of four positions by sixteen elements a group of sixteen lanes, transposed
       typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
@@ -528,17 +593,15 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, f
         for (int n = 0; n < NT; n++) o[n][v] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, p[n], o[n][v], 0, 0, 0);
       }
       __builtin_amdgcn_wave_barrier();
-      vec = next;
+      found = next;
     }
 
     // the waves' sums, joined
 #pragma unroll
     for (int n = 0; n < NT; n++) {
-      l[n] += __shfl_xor(l[n], 16);
-      l[n] += __shfl_xor(l[n], 32);
       if (kg == 0) {
         ms[wave][16 * n + col] = m[n];
-        ls[wave][16 * n + col] = l[n];
+        ls[wave][16 * n + col] = l[n][0];
       }
     }
     float* sums = (float*)lds;
@@ -583,7 +646,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, f
         dst[0] = x;
         dst[1] = y;
         if (e == 0) part_ml[slot * MT + r] = float2{top, sum};
-      } else if (e < pv.dim) {
+      } else if (e < v_dim) {
         write_row<FMT>(a, s, tile * MT + r, g, e, x, y, sum);
       }
     }
@@ -655,8 +718,13 @@ int launch_shape(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStrea
   float2* ml = (float2*)(ws + p.ml);
   Open* open = (Open*)(ws + p.open);
   const unsigned n = (unsigned)p.workers * (unsigned)a.cache.heads;
-  hipLaunchKernelGGL((attend_kernel<FMT, DK, DV, NT, WAVES>), dim3(n), dim3(kThreads), 0, stream, a, part, ml, open,
-                     p.workers);
+  const CacheArgs& c = a.cache;
+  if (c.page_size % kTile == 0 && c.plane[0].dim == DK && c.plane[1].dim == DV)
+    hipLaunchKernelGGL((attend_kernel<FMT, DK, DV, NT, WAVES, true>), dim3(n), dim3(kThreads), 0, stream, a, part, ml, open,
+                       p.workers);
+  else
+    hipLaunchKernelGGL((attend_kernel<FMT, DK, DV, NT, WAVES, false>), dim3(n), dim3(kThreads), 0, stream, a, part, ml, open,
+                       p.workers);
   // one unit holds the longest context that the table can: nothing to join
   if (hipGetLastError() != hipSuccess) return MXFP4_ERR_DEVICE;
   if ((int64_t)a.cache.max_pages * a.cache.page_size <= kUnit) return MXFP4_OK;

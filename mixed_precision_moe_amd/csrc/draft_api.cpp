@@ -98,7 +98,7 @@ AttendPlan attend_plan(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows,
   const int64_t nt = (per_seq + 15) / 16, most = p.dk == 256 ? 2 : 4;
   p.nt = (int32_t)(nt < 1 ? 1 : nt > most ? most : nt);
   const int64_t fill = (int64_t)kCus * attend_waves(p.dk, p.nt) / d->heads;
-  p.workers = (int32_t)(fill < 1 ? 1 : fill);
+  p.workers = (int32_t)(fill < 1 ? 1 : fill < 8 ? fill : fill & ~int64_t(7));  // as many on each XCD
   uint64_t at = 0;
   auto take = [&](uint64_t bytes) { uint64_t o = at; at = up256(at + bytes); return o; };
   const uint64_t all = (uint64_t)p.workers * (uint64_t)d->heads, part_rows = 2 * all * 16 * (uint64_t)p.nt;
@@ -173,6 +173,7 @@ MX_API int mxfp4_cache_attend(const mxfp4_cache_dims* d, const void* k_q, const 
   a.mask_cols = mask_cols;
   a.group = q_heads / d->heads;
   a.out_fp32 = out_is_fp32;
+  a.page_shift = d->page_size & (d->page_size - 1) ? -1 : __builtin_ctz((unsigned)d->page_size);
   a.scale = scale;
   uint8_t* ws = (uint8_t*)workspace;
   if (d->fmt == MXFP4_FMT_MXFP4) return launch_attend_mxfp4(a, plan, ws, S(stream));
