@@ -51,8 +51,7 @@ constexpr int kPerByte = FMT == MXFP4_FMT_MXFP8 ? 1 : 2;
 
 // What a worker leaves for the join, next to its sums: the item that it begins and another worker ends.
 struct Open {
-  int64_t tile;
-  int32_t seq, last;  // last: the worker that ends it; -1: none
+  int32_t tile, seq, last;  // last: the worker that ends it; -1: none
 };
 
 // ---------------------------------------------------------------------------------------------
@@ -100,46 +99,59 @@ MX_DEV bool has_nan_code(uint32_t c) {  // a byte whose lower seven bits are all
 // Sequences, items and units.
 
 struct Seq {
-  int64_t first;    // its first row
-  int32_t drafts;   // of its own
-  int32_t rows;     // of them that q holds
-  int64_t start, cap;
+  int32_t first;   // its first row
+  int32_t drafts;  // of its own
+  int32_t rows;    // of them that q holds
+  int32_t start;
 };
 
 MX_DEV Seq sequence(const AttendArgs& a, int b) {
   const CacheArgs& c = a.cache;
-  Seq s;
-  s.first = c.cu[b];
-  const int64_t end = c.cu[b + 1], there = min(end, c.rows);
-  const bool some = s.first >= 0 && there > s.first;
-  s.drafts = some ? (int32_t)min(end - s.first, (int64_t)INT32_MAX) : 0;
-  s.rows = some ? (int32_t)(there - s.first) : 0;
-  s.start = c.start ? c.start[b] : 0;
-  s.cap = (int64_t)c.max_pages * c.page_size;
-  return s;
+  const int32_t at = c.cu[b], end = c.cu[b + 1], there = min((int64_t)end, c.rows);
+  const bool some = at >= 0 && there > at;
+  return Seq{at, some ? end - at : 0, some ? there - at : 0, c.start ? c.start[b] : 0};
 }
 
-// Positions that some row of a tile sees are below this.
-MX_DEV int64_t tile_end(const AttendArgs& a, const Seq& s, int64_t tile, int mt) {
-  int64_t n = s.drafts;
-  if (!a.mask) n = min((int64_t)s.rows, ((tile + 1) * mt - 1) / a.group + 1);
-  const int64_t end = min(s.start + n, s.cap);
-  return end < 0 ? 0 : end;
-}
+// Of a sequence, tile by tile: the positions that some row of the tile sees are below `end`, 128 of them are a unit; a tile
+// has one at least, since its rows are written where nothing is seen too.
+struct Tiles {
+  int32_t tile, tiles, end, units;
+  int32_t row, part;  // without a mask: the draft of the row behind the tile, and that row's place in its group
 
-MX_DEV int64_t tiles_of(const AttendArgs& a, const Seq& s, int mt) { return ((int64_t)s.rows * a.group + mt - 1) / mt; }
-
-// Units of a tile: one at least, since its rows are written where nothing is seen too.
-MX_DEV int64_t tile_units(const AttendArgs& a, const Seq& s, int64_t tile, int mt) {
-  const int64_t end = tile_end(a, s, tile, mt);
-  return end <= kUnit ? 1 : (end + kUnit - 1) / kUnit;
-}
+  MX_DEV void set(const AttendArgs& a, const Seq& s) {
+    const int64_t n = a.mask ? s.drafts : min(s.rows, row + (part > 0));
+    const int64_t e = min(s.start + n, (int64_t)a.cache.max_pages * a.cache.page_size);
+    end = e < 0 ? 0 : (int32_t)e;
+    units = end <= kUnit ? 1 : (end + kUnit - 1) / kUnit;
+  }
+  MX_DEV void begin(const AttendArgs& a, const Seq& s, int mt) {
+    tile = 0;
+    tiles = (s.rows * a.group + mt - 1) / mt;
+    row = a.rows_of_tile;
+    part = a.part_of_tile;
+    set(a, s);
+  }
+  MX_DEV void next(const AttendArgs& a, const Seq& s) {
+    tile++;
+    row += a.rows_of_tile;
+    part += a.part_of_tile;
+    if (part >= a.group) {
+      part -= a.group;
+      row++;
+    }
+    set(a, s);
+  }
+};
 
 MX_DEV int64_t seq_units(const AttendArgs& a, const Seq& s, int mt) {
-  const int64_t tiles = tiles_of(a, s, mt);
-  if (a.mask) return tiles * tile_units(a, s, 0, mt);
+  Tiles t;
+  t.begin(a, s, mt);
+  if (a.mask) return (int64_t)t.tiles * t.units;
   int64_t n = 0;
-  for (int64_t i = 0; i < tiles; i++) n += tile_units(a, s, i, mt);
+  while (t.tile < t.tiles) {
+    n += t.units;
+    t.next(a, s);
+  }
   return n;
 }
 
@@ -170,10 +182,10 @@ MX_DEV int64_t scan_units(const AttendArgs& a, int b0, int lane, int mt) {
 
 // Eight elements of a row of the result from its sums x, y and the sum of its weights.
 template <int FMT>
-MX_DEV void write_row(const AttendArgs& a, const Seq& s, int64_t r, int g, int e, f32x4_t x, f32x4_t y, float sum) {
+MX_DEV void write_row(const AttendArgs& a, const Seq& s, int32_t r, int g, int e, f32x4_t x, f32x4_t y, float sum) {
   const CachePlane& pv = a.cache.plane[1];
-  const int64_t d = r / a.group;
-  const int64_t at = (s.first + d) * pv.ldt + (g * a.group + (r - d * a.group)) * pv.ldh + e;
+  const int32_t d = (uint32_t)r / (uint32_t)a.group;
+  const int64_t at = (int64_t)(s.first + d) * pv.ldt + (g * a.group + (r - d * a.group)) * pv.ldh + e;
   const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
   for (int i = 0; i < 4; i++) {
@@ -267,15 +279,11 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, f
     item = lane64(sums, 63);
   }
   Seq s = sequence(a, b);
-  int64_t tile = 0, units = tile_units(a, s, 0, MT), tiles = tiles_of(a, s, MT);
-  if (a.mask) {
-    tile = (u0 - item) / units;
-    item += tile * units;
-  } else {
-    while (item + units <= u0) {
-      item += units;
-      units = tile_units(a, s, ++tile, MT);
-    }
+  Tiles ti;
+  ti.begin(a, s, MT);
+  while (item + ti.units <= u0) {
+    item += ti.units;
+    ti.next(a, s);
   }
 
   // not 0, so that its product with a hidden position's -inf is one
@@ -286,21 +294,25 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, f
   const int k_dim = PAGED ? DK : pk.dim, v_dim = PAGED ? DV : pv.dim;
   const int64_t k_bytes = k_dim / kPerByte<FMT>, v_bytes = v_dim / kPerByte<FMT>;
   const int k_blocks = k_dim / kBlock<FMT>, v_blocks = v_dim / kBlock<FMT>;
+  // PAGED: this lane's part of the addresses of codes and scales
+  const uint32_t k_at = (uint32_t)(col * c.heads) * (DK / kPerByte<FMT>) + kg * (Sh::kCodes * 4);
+  const uint32_t ks_at = (uint32_t)(col * c.heads) * (DK / kBlock<FMT>) + kg * Sh::kQuarter / kBlock<FMT>;
+  const uint32_t v_at = (uint32_t)(lane / Sh::kPerKey * c.heads) * (DV / kPerByte<FMT>) + 16 * (lane % Sh::kPerKey);
+  const uint32_t vs_at = (uint32_t)(lane / Sh::kPerKey * c.heads) * (DV / kBlock<FMT>) + lane % Sh::kPerKey * Sh::kElems / kBlock<FMT>;
   uint16_t* const vt = (uint16_t*)lds + wave * kTile * Sh::kStride;
 
   int64_t u = u0;
   while (u < u1) {
-    const int64_t k0 = u - item, k1 = min(units, u1 - item);
-    const int64_t end = tile_end(a, s, tile, MT);
+    const int32_t k0 = (int32_t)(u - item), k1 = (int32_t)min((int64_t)ti.units, u1 - item), end = ti.end;
     // the rows of this lane's columns
     bf16x8_t q[NT][Sh::kSteps];
     int32_t draft[NT];  // -1: no such row
 #pragma unroll
     for (int n = 0; n < NT; n++) {
-      const int64_t r = tile * MT + 16 * n + col;
-      const int64_t d = r / a.group;
-      draft[n] = d < s.rows ? (int32_t)d : -1;
-      const uint16_t* src = (const uint16_t*)pk.rows + (s.first + d) * pk.ldt + (g * a.group + (r - d * a.group)) * pk.ldh;
+      const int32_t r = ti.tile * MT + 16 * n + col;
+      const int32_t d = (uint32_t)r / (uint32_t)a.group;
+      draft[n] = d < s.rows ? d : -1;
+      const uint16_t* src = (const uint16_t*)pk.rows + (int64_t)(s.first + d) * pk.ldt + (g * a.group + (r - d * a.group)) * pk.ldh;
 #pragma unroll
       for (int i = 0; i < Sh::kSteps; i++) {
         const int e = kg * Sh::kQuarter + 8 * i;
@@ -324,12 +336,13 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, f
 
     // Where a tile's codes are.  PAGED: its page, in every lane; else the cache's vector of each of its positions, -1: none,
     // in the lanes 0 to 31.
-    const auto find = [&](int64_t k) {
-      const int64_t pos = k * kUnit + wave * kTile + (PAGED ? 0 : lane & 31);
+    const int32_t* const pages = c.table + (int64_t)b * c.ld_table;
+    const auto find = [&](int32_t k) {
+      const int32_t pos = k * kUnit + wave * kTile + (PAGED ? 0 : lane & 31);
       Found f = -1;
       if (pos < end) {
         const uint32_t p = a.page_shift >= 0 ? (uint32_t)pos >> a.page_shift : (uint32_t)pos / (uint32_t)c.page_size;
-        const int32_t page = c.table[(int64_t)b * c.ld_table + p];
+        const int32_t page = pages[p];
         if (PAGED)
           f = page;
         else if (page >= 0 && page < c.num_pages)
@@ -338,7 +351,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, f
       return f;
     };
     // PAGED: the tile's first vector, -1: none.  Its positions past the end lie in the page too.
-    const auto first_vector = [&](int64_t k, Found f) -> int64_t {
+    const auto first_vector = [&](int32_t k, Found f) -> int64_t {
       const int32_t page = __builtin_amdgcn_readfirstlane((int)f);
       if (page < 0 || page >= c.num_pages) return -1;
       const uint32_t pos = (uint32_t)k * kUnit + (uint32_t)wave * kTile;
@@ -346,13 +359,13 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, f
       return ((int64_t)page * c.page_size + in_page) * c.heads + g;
     };
     uint32_t kc[2][Sh::kCodes], ks[2][Sh::kScales];
-    // a lane's quarter of a key, from the key's codes and scales
+    // a lane's quarter of a key
     const auto load_key = [&](int t, const uint8_t* src, const uint8_t* scales) {
       if (PAGED || pk.dim == DK) {
         if constexpr (Sh::kCodes % 4 == 0) {
 #pragma unroll
           for (int i = 0; i < Sh::kCodes; i += 4) {
-            const u32x4_t x = *reinterpret_cast<const u32x4_a8*>(src + kg * (Sh::kCodes * 4) + 4 * i);
+            const u32x4_t x = *reinterpret_cast<const u32x4_a8*>(src + 4 * i);
             kc[t][i] = x[0];
             kc[t][i + 1] = x[1];
             kc[t][i + 2] = x[2];
@@ -361,7 +374,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, f
         } else {
 #pragma unroll
           for (int i = 0; i < Sh::kCodes; i += 2) {
-            const u32x2_t x = *reinterpret_cast<const u32x2_a8*>(src + kg * (Sh::kCodes * 4) + 4 * i);
+            const u32x2_t x = *reinterpret_cast<const u32x2_a8*>(src + 4 * i);
             kc[t][i] = x[0];
             kc[t][i + 1] = x[1];
           }
@@ -374,7 +387,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, f
 #pragma unroll
           for (int j = 0; j < per; j++) {
             kc[t][per * i + j] = 0;
-            if (e < pk.dim) kc[t][per * i + j] = *reinterpret_cast<const uint32_t*>(src + e / kPerByte<FMT> + 4 * j);
+            if (e < pk.dim) kc[t][per * i + j] = *reinterpret_cast<const uint32_t*>(src + 4 * (per * i + j));
           }
         }
       }
@@ -382,53 +395,52 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, f
 #pragma unroll
       for (int i = 0; i < Sh::kScales; i++) {
         ks[t][i] = 0;
-        if (PAGED || b0 + i < k_blocks) ks[t][i] = scales[b0 + i];
+        if (PAGED || b0 + i < k_blocks) ks[t][i] = scales[i];
       }
     };
-    const auto load_k = [&](int64_t k, Found f) {
+    const auto load_k = [&](int32_t k, Found f) {
       const int64_t first = PAGED ? first_vector(k, f) : 0;
 #pragma unroll
       for (int t = 0; t < 2; t++) {
-        if (PAGED) {
-          const uint32_t key = (uint32_t)(16 * t + col) * (uint32_t)c.heads;
-          if (first >= 0) load_key(t, pk.q + first * k_bytes + key * (uint32_t)k_bytes, pk.s + first * k_blocks + key * (uint32_t)k_blocks);
+        if (PAGED) {  // the tile's part of the addresses is the same for all lanes, the lane's for all tiles
+          const int64_t at = first + 16 * t * c.heads;
+          if (first >= 0) load_key(t, pk.q + at * k_bytes + k_at, pk.s + at * k_blocks + ks_at);
         } else {
           const int64_t at = shfl64(f, 16 * t + col);
-          if (at >= 0) load_key(t, pk.q + at * k_bytes, pk.s + at * k_blocks);
+          if (at >= 0) load_key(t, pk.q + at * k_bytes + kg * (Sh::kCodes * 4), pk.s + at * k_blocks + kg * Sh::kQuarter / kBlock<FMT>);
         }
       }
     };
     u32x4_t vc[Sh::kPieces];
     uint32_t vs[Sh::kPieces][Sh::kPieceScales];
-    const auto load_piece = [&](int i, int piece, const uint8_t* src, const uint8_t* scales) {
-      const int e = piece * Sh::kElems;
+    const auto load_piece = [&](int i, const uint8_t* src, const uint8_t* scales) {
+      const int e = lane % Sh::kPerKey * Sh::kElems;
       if (PAGED || e + Sh::kElems <= pv.dim) {
-        vc[i] = *reinterpret_cast<const u32x4_a8*>(src + 16 * piece);
+        vc[i] = *reinterpret_cast<const u32x4_a8*>(src);
       } else if (e < pv.dim) {
-        const u32x2_t x = *reinterpret_cast<const u32x2_a8*>(src + 16 * piece);
+        const u32x2_t x = *reinterpret_cast<const u32x2_a8*>(src);
         vc[i] = u32x4_t{x[0], x[1], 0, 0};
       }
       const int b0 = e / kBlock<FMT>;
 #pragma unroll
       for (int j = 0; j < Sh::kPieceScales; j++)
-        if (PAGED || b0 + j < v_blocks) vs[i][j] = scales[b0 + j];
+        if (PAGED || b0 + j < v_blocks) vs[i][j] = scales[j];
     };
-    const auto load_v = [&](int64_t k, Found f) {
+    const auto load_v = [&](int32_t k, Found f) {
       const int64_t first = PAGED ? first_vector(k, f) : 0;
 #pragma unroll
       for (int i = 0; i < Sh::kPieces; i++) {
-        const int id = i * 64 + lane, key = id / Sh::kPerKey, piece = id % Sh::kPerKey;
-        if (!PAGED) {
+        constexpr int keys = 64 / Sh::kPerKey;  // of 64 pieces
+        if (PAGED) {
+          const int64_t at = first + keys * i * c.heads;
+          if (first >= 0) load_piece(i, pv.q + at * v_bytes + v_at, pv.s + at * v_blocks + vs_at);
+        } else {
           vc[i] = u32x4_t{0, 0, 0, 0};
 #pragma unroll
           for (int j = 0; j < Sh::kPieceScales; j++) vs[i][j] = 0;
-        }
-        if (PAGED) {
-          const uint32_t by = (uint32_t)key * (uint32_t)c.heads;
-          if (first >= 0) load_piece(i, piece, pv.q + first * v_bytes + by * (uint32_t)v_bytes, pv.s + first * v_blocks + by * (uint32_t)v_blocks);
-        } else {
-          const int64_t at = shfl64(f, key);
-          if (at >= 0) load_piece(i, piece, pv.q + at * v_bytes, pv.s + at * v_blocks);
+          const int64_t at = shfl64(f, keys * i + lane / Sh::kPerKey);
+          const int piece = lane % Sh::kPerKey;
+          if (at >= 0) load_piece(i, pv.q + at * v_bytes + 16 * piece, pv.s + at * v_blocks + piece * Sh::kElems / kBlock<FMT>);
         }
       }
     };
@@ -436,13 +448,13 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, f
     Found found = find(k0);
     load_k(k0, found);
     load_v(k0, found);
-    for (int64_t k = k0; k < k1; k++) {
-      const int64_t base = k * kUnit + wave * kTile;
+    for (int32_t k = k0; k < k1; k++) {
+      const int32_t base = k * kUnit + wave * kTile;
       // which of the tile's positions have a vector, and whether all rows see them all
       uint32_t there;
       if (PAGED) {
         const int32_t page = __builtin_amdgcn_readfirstlane((int)found);
-        const int64_t left = end - base;
+        const int32_t left = end - base;
         there = page < 0 || page >= c.num_pages || left <= 0 ? 0u : left >= kTile ? ~0u : (1u << left) - 1;
       } else {
         there = (uint32_t)__ballot(found >= 0);
@@ -499,7 +511,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, f
         }
 #pragma unroll
         for (int n = 0; n < NT; n++) {
-          const uint8_t* mask = a.mask + (s.first + draft[n]) * a.ld_mask;
+          const uint8_t* mask = a.mask + (int64_t)(s.first + draft[n]) * a.ld_mask;
           const int64_t most = a.mask ? min(s.drafts, a.mask_cols) : (int64_t)draft[n] + 1;  // drafts past it are not seen
 #pragma unroll
           for (int t = 0; t < 2; t++) {
@@ -507,7 +519,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, f
 #pragma unroll
             for (int i = 0; i < 4; i++) {
               const int key = 16 * t + 4 * kg + i;
-              const int64_t j = base + key - s.start;
+              const int64_t j = (int64_t)base + key - s.start;
               bool sees = draft[n] >= 0 && (there >> key & 1) && j < most;
               if (sees && j >= 0 && a.mask) sees = mask[j];
               if (!sees)
@@ -631,8 +643,8 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, f
     }
     __syncthreads();
     // rows of the tile that exist, eight elements a thread
-    const int there = (int)min((int64_t)MT, (int64_t)s.rows * a.group - tile * MT);
-    const bool whole_item = k0 == 0 && k1 == units;
+    const int there = min(MT, s.rows * a.group - ti.tile * MT);
+    const bool whole_item = k0 == 0 && k1 == ti.units;
     const int64_t slot = 2 * at_worker + (k0 == 0 ? 1 : 0);
     for (int id = threadIdx.x; id < there * (DV / 8); id += kThreads) {
       const int r = id / (DV / 8), e = id % (DV / 8) * 8;
@@ -647,27 +659,26 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_kernel(AttendArgs a, f
         dst[1] = y;
         if (e == 0) part_ml[slot * MT + r] = float2{top, sum};
       } else if (e < v_dim) {
-        write_row<FMT>(a, s, tile * MT + r, g, e, x, y, sum);
+        write_row<FMT>(a, s, ti.tile * MT + r, g, e, x, y, sum);
       }
     }
-    if (threadIdx.x == 0 && k0 == 0 && k1 < units) {
+    if (threadIdx.x == 0 && k0 == 0 && k1 < ti.units) {
       // the worker of the item's last unit
-      const int64_t last = item + units - 1;
+      const int64_t last = item + ti.units - 1;
       const int64_t w = ((last + 1) * used - 1) / all;
-      open[at_worker] = Open{tile, b, (int32_t)w};
+      open[at_worker] = Open{ti.tile, b, (int32_t)w};
     }
     __syncthreads();
 
     u += k1 - k0;
-    item += units;
+    item += ti.units;
     if (u >= u1) break;
-    if (++tile >= tiles) {
+    ti.next(a, s);
+    if (ti.tile >= ti.tiles) {
       do s = sequence(a, ++b);
       while (s.rows == 0);
-      tile = 0;
-      tiles = tiles_of(a, s, MT);
+      ti.begin(a, s, MT);
     }
-    units = tile_units(a, s, tile, MT);
   }
 }
 
@@ -681,7 +692,7 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendArgs a, con
   if (it.last < 0) return;
   const int g = blockIdx.x / workers, worker = blockIdx.x % workers;
   const Seq s = sequence(a, it.seq);
-  const int there = (int)min((int64_t)MT, (int64_t)s.rows * a.group - it.tile * MT);
+  const int there = min(MT, s.rows * a.group - it.tile * MT);
   for (int id = threadIdx.x; id < 16 * (DV / 8); id += kThreads) {
     const int r = 16 * blockIdx.y + id / (DV / 8), e = id % (DV / 8) * 8;
     if (r >= there || e >= a.cache.plane[1].dim) continue;

@@ -104,7 +104,7 @@ AttendPlan attend_plan(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows,
   const uint64_t all = (uint64_t)p.workers * (uint64_t)d->heads, part_rows = 2 * all * 16 * (uint64_t)p.nt;
   p.part = take(4 * part_rows * (uint64_t)p.dv);
   p.ml = take(8 * part_rows);
-  p.open = take(16 * all);
+  p.open = take(12 * all);
   p.total = at;
   return p;
 }
@@ -114,7 +114,8 @@ int check_attend(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows, int32
   if (st) return st;
   if (d->v_dim < 1 || d->k_dim > kMaxDim || d->v_dim > kMaxDim) return MXFP4_ERR_SHAPE;
   if (q_heads < 1 || q_heads > kMaxHeads || q_heads % d->heads) return MXFP4_ERR_SHAPE;
-  if (rows < 0 || rows >= kMaxRows || rows * q_heads >= kMaxLd || n_seqs < 0) return MXFP4_ERR_SHAPE;
+  // rows of a key head, and positions, are counted in 32 bits
+  if (rows < 0 || rows >= kMaxRows || n_seqs < 0 || rows * (q_heads / d->heads) >= kMaxRows - 64) return MXFP4_ERR_SHAPE;
   return MXFP4_OK;
 }
 
@@ -138,7 +139,7 @@ MX_API int mxfp4_cache_attend(const mxfp4_cache_dims* d, const void* k_q, const 
                               void* stream) {
   int st = check_attend(d, q_heads, rows, n_seqs);
   if (st || (st = check_flags(out_is_fp32, 0, 0))) return st;
-  if (!table_fits(ld_table, n_seqs, max_pages)) return MXFP4_ERR_SHAPE;
+  if (!table_fits(ld_table, n_seqs, max_pages) || (int64_t)max_pages * d->page_size > kMaxRows - 256) return MXFP4_ERR_SHAPE;
   if (!(scale >= -3.40282347e38f && scale <= 3.40282347e38f)) return MXFP4_ERR_SHAPE;
   auto bad_ld = [&](int64_t ldt, int64_t ldh, int32_t dim) {
     return ldt < 0 || ldt % 8 || ldt > kMaxLd || ldh < 0 || ldh % 8 || ldh > kMaxLd || (q_heads > 1 && ldh < dim) ||
@@ -174,6 +175,8 @@ MX_API int mxfp4_cache_attend(const mxfp4_cache_dims* d, const void* k_q, const 
   a.group = q_heads / d->heads;
   a.out_fp32 = out_is_fp32;
   a.page_shift = d->page_size & (d->page_size - 1) ? -1 : __builtin_ctz((unsigned)d->page_size);
+  a.rows_of_tile = 16 * plan.nt / a.group;
+  a.part_of_tile = 16 * plan.nt % a.group;
   a.scale = scale;
   uint8_t* ws = (uint8_t*)workspace;
   if (d->fmt == MXFP4_FMT_MXFP4) return launch_attend_mxfp4(a, plan, ws, S(stream));

@@ -13,6 +13,7 @@ struct AttendArgs {
   int64_t ld_mask;
   int32_t mask_cols, group, out_fp32;  // group: query heads of a key head
   int32_t page_shift;                  // of a page size that is a power of two, else -1
+  int32_t rows_of_tile, part_of_tile;  // tile rows / group, and the remainder
   float scale;
 };
 // How a call is cut up: tiles of 16 nt rows, elements of a key and a value in the kernel, workers of each head; the
