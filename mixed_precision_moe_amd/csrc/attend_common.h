@@ -1,0 +1,470 @@
+// Attention over the block-quantized paged cache: rows see the positions before their sequence's drafts, and of the
+// drafts those that a mask or their order leaves.
+//
+//   out[t, h] = sum_j p_j V[j, g] / sum_j p_j,  p_j = exp2(s_j - m),  s_j = scale log2(e) q[t, h] . K[j, g],  m >= s_j - 8
+//
+// Work.  The rows of a sequence that share a key head (drafts times query heads of the group) are cut into tiles.  A tile
+// and the positions it sees are an item; items are cut into units of positions, and a head's units are dealt out evenly to
+// its workers (workgroups), each a contiguous range: a worker's first and last item may be parts, which go to the
+// workspace as sums with their maximum and are joined by a second launch, in worker order.  Every worker finds its range
+// from the lengths on the device, so nothing about them has to be known on the host.
+//
+// Both kernels form S^T = K Q^T and O^T = V^T P^T: a row of q is a column of both, so its maximum, sum and rescaling stay in
+// one lane (and three others, which hold other positions), and S^T leaves the matrix instruction as P^T enters the next one.
+// Values are exact in bf16 (at most six significant bits), so both products are of what the cache holds; V is read back from
+// LDS transposed.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "cache_slots.h"
+#include "drafts.h"
+
+#define MX_DEV __device__ __forceinline__
+
+namespace {
+
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2_t __attribute__((ext_vector_type(2)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef u32x4_t u32x4_a8 __attribute__((aligned(8)));  // vectors of codes start on 8 bytes
+typedef u32x2_t u32x2_a8 __attribute__((aligned(8)));
+
+constexpr int kThreads = 256;
+constexpr int kWaves = 4;
+
+template <int FMT>
+constexpr int kBlock = FMT == MXFP4_FMT_NVFP4 ? 16 : 32;
+template <int FMT>
+constexpr int kPerByte = FMT == MXFP4_FMT_MXFP8 ? 1 : 2;
+
+// What a worker leaves for the join, next to its sums: the item that it begins and another worker ends.
+struct Open {
+  int32_t tile, seq, last;  // last: the worker that ends it; -1: none
+};
+
+// ---------------------------------------------------------------------------------------------
+// Eight values as bf16: c their codes (4-bit formats: c[0]), s the block's scale byte.
+template <int FMT>
+MX_DEV bf16x8_t values8(uint32_t c0, uint32_t c1, uint32_t s) {
+  u32x4_t o;
+  if (FMT == MXFP4_FMT_MXFP8) {
+    const float f = __uint_as_float(s << 23);
+    o[0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c0, f, false));
+    o[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c0, f, true));
+    o[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c1, f, false));
+    o[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c1, f, true));
+  } else if (FMT == MXFP4_FMT_MXFP4) {
+    const float f = __uint_as_float(s << 23);
+    o[0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c0, f, 0));
+    o[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c0, f, 1));
+    o[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c0, f, 2));
+    o[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c0, f, 3));
+  } else {
+    // the product has at most six significant bits, so the upper halves of its binary32 form are all of it
+    const float f = __builtin_amdgcn_cvt_f32_fp8((int)s, 0);
+    auto two = [&](auto v) {
+      return __builtin_amdgcn_perm(__float_as_uint(v[1] * f), __float_as_uint(v[0] * f), 0x07060302u);
+    };
+    o[0] = two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c0, 1.0f, 0));
+    o[1] = two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c0, 1.0f, 1));
+    o[2] = two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c0, 1.0f, 2));
+    o[3] = two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c0, 1.0f, 3));
+  }
+  return __builtin_bit_cast(bf16x8_t, o);
+}
+
+// Whether a block with this scale (and for MXFP8 these codes) may hold values that are not finite in bf16.
+template <int FMT>
+MX_DEV bool not_finite(uint32_t s) {
+  return FMT == MXFP4_FMT_NVFP4 ? (s & 0x7Fu) == 0x7Fu : FMT == MXFP4_FMT_MXFP8 ? s > 246u : s > 252u;
+}
+MX_DEV bool has_nan_code(uint32_t c) {  // a byte whose lower seven bits are all set
+  const uint32_t x = ~c & 0x7F7F7F7Fu;
+  return ((x - 0x01010101u) & ~x & 0x80808080u) != 0;
+}
+
+// ---------------------------------------------------------------------------------------------
+// Sequences, items and units.
+
+struct Seq {
+  int32_t first;   // its first row
+  int32_t drafts;  // of its own
+  int32_t rows;    // of them that q holds
+  int32_t start;
+};
+
+MX_DEV Seq sequence(const AttendArgs& a, int b) {
+  const CacheArgs& c = a.cache;
+  const int32_t at = c.cu[b], end = c.cu[b + 1], there = min((int64_t)end, c.rows);
+  const bool some = at >= 0 && there > at;
+  return Seq{at, some ? end - at : 0, some ? there - at : 0, c.start ? c.start[b] : 0};
+}
+
+// Of a sequence, tile by tile of MT rows: the positions that some row of the tile sees are below `end`, UNIT of them are a
+// unit; a tile has one at least, since its rows are written where nothing is seen too.
+template <int MT, int UNIT>
+struct Tiles {
+  int32_t tile, tiles, end, units;
+  int32_t row, part;  // without a mask: the draft of the row behind the tile, and that row's place in its group
+
+  MX_DEV void set(const AttendArgs& a, const Seq& s) {
+    const int64_t n = a.mask ? s.drafts : min(s.rows, row + (part > 0));
+    const int64_t e = min(s.start + n, (int64_t)a.cache.max_pages * a.cache.page_size);
+    end = e < 0 ? 0 : (int32_t)e;
+    units = end <= UNIT ? 1 : (end + UNIT - 1) / UNIT;
+  }
+  MX_DEV void begin(const AttendArgs& a, const Seq& s) {
+    tile = 0;
+    tiles = (s.rows * a.group + MT - 1) / MT;
+    row = a.rows_of_tile;
+    part = a.part_of_tile;
+    set(a, s);
+  }
+  MX_DEV void next(const AttendArgs& a, const Seq& s) {
+    tile++;
+    row += a.rows_of_tile;
+    part += a.part_of_tile;
+    if (part >= a.group) {
+      part -= a.group;
+      row++;
+    }
+    set(a, s);
+  }
+};
+
+template <int MT, int UNIT>
+MX_DEV int64_t seq_units(const AttendArgs& a, const Seq& s) {
+  Tiles<MT, UNIT> t;
+  t.begin(a, s);
+  if (a.mask) return (int64_t)t.tiles * t.units;
+  int64_t n = 0;
+  while (t.tile < t.tiles) {
+    n += t.units;
+    t.next(a, s);
+  }
+  return n;
+}
+
+MX_DEV int64_t shfl64(int64_t v, int lane) {
+  const int lo = __shfl((int)v, lane), hi = __shfl((int)(v >> 32), lane);
+  return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
+}
+MX_DEV int64_t lane64(int64_t v, int lane) {  // the same for the whole wave, and known to be
+  const int lo = __builtin_amdgcn_readlane((int)v, lane), hi = __builtin_amdgcn_readlane((int)(v >> 32), lane);
+  return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
+}
+MX_DEV int64_t shfl64_up(int64_t v, int by) {
+  const int lo = __shfl_up((int)v, by), hi = __shfl_up((int)(v >> 32), by);
+  return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
+}
+
+// Units of the 64 sequences from b0 on, summed up to and including each lane's.
+template <int MT, int UNIT>
+MX_DEV int64_t scan_units(const AttendArgs& a, int b0, int lane) {
+  int64_t n = 0;
+  if (b0 + lane < a.cache.n_seqs) n = seq_units<MT, UNIT>(a, sequence(a, b0 + lane));
+#pragma unroll
+  for (int h = 1; h < 64; h <<= 1) {
+    const int64_t o = shfl64_up(n, h);
+    if (lane >= h) n += o;
+  }
+  return n;
+}
+
+// Eight elements of a row of the result from its sums x, y and the sum of its weights.
+template <int FMT>
+MX_DEV void write_row(const AttendArgs& a, const Seq& s, int32_t r, int g, int e, f32x4_t x, f32x4_t y, float sum) {
+  const CachePlane& pv = a.cache.plane[1];
+  const int32_t d = (uint32_t)r / (uint32_t)a.group;
+  const int64_t at = (int64_t)(s.first + d) * pv.ldt + (g * a.group + (r - d * a.group)) * pv.ldh + e;
+  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    x[i] *= f;
+    y[i] *= f;
+    if (FMT == MXFP4_FMT_NVFP4) {
+      x[i] /= pv.gs;
+      y[i] /= pv.gs;
+    }
+  }
+  if (a.out_fp32) {
+    f32x4_t* dst = reinterpret_cast<f32x4_t*>((float*)pv.rows + at);
+    dst[0] = x;
+    dst[1] = y;
+  } else {
+    bf16x8_t v;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      v[i] = (__bf16)x[i];
+      v[4 + i] = (__bf16)y[i];
+    }
+    *reinterpret_cast<bf16x8_t*>((uint16_t*)pv.rows + at) = v;
+  }
+}
+
+// A worker's range of units and where it is in it; every wave has the same.
+template <int MT, int UNIT>
+struct Work {
+  int g, worker, b;
+  int64_t at;               // of the worker, as the join counts them
+  int64_t all, used;        // units of the head, workers that have some
+  int64_t u, u1, item;      // next unit, end of the range, the item's first unit
+  Seq s;
+  Tiles<MT, UNIT> ti;
+
+  // False: nothing to do.
+  MX_DEV bool begin(const AttendArgs& a, int workers, Open* open, int lane) {
+    const CacheArgs& c = a.cache;
+    // Workgroups go to the eight XCDs in turn: a worker's heads, which read pieces of the same tokens, share one.
+    if (workers % 8 == 0) {
+      const int i = blockIdx.x / 8;
+      g = i % c.heads;
+      worker = i / c.heads * 8 + blockIdx.x % 8;
+    } else {
+      g = blockIdx.x % c.heads;
+      worker = blockIdx.x / c.heads;
+    }
+    at = (int64_t)g * workers + worker;
+    all = 0;
+    for (int b0 = 0; b0 < c.n_seqs; b0 += 64) all += lane64(scan_units<MT, UNIT>(a, b0, lane), 63);
+    used = min((int64_t)workers, all);
+    if (threadIdx.x == 0) open[at] = Open{0, 0, -1};
+    if (worker >= used) return false;
+    u = all / used * worker + all % used * worker / used;
+    u1 = all / used * (worker + 1) + all % used * (worker + 1) / used;
+    b = 0;
+    item = 0;
+    for (int b0 = 0; b0 < c.n_seqs; b0 += 64) {
+      const int64_t sums = item + scan_units<MT, UNIT>(a, b0, lane);
+      const uint64_t past = __ballot(sums > u);
+      if (past) {
+        const int l = __ffsll((unsigned long long)past) - 1;
+        b = b0 + l;
+        if (l > 0) item = lane64(sums, l - 1);
+        break;
+      }
+      item = lane64(sums, 63);
+    }
+    s = sequence(a, b);
+    ti.begin(a, s);
+    while (item + ti.units <= u) {
+      item += ti.units;
+      ti.next(a, s);
+    }
+    return true;
+  }
+  // On to the next item, `done` units on.  False: the range ends.
+  MX_DEV bool next(const AttendArgs& a, int done) {
+    u += done;
+    item += ti.units;
+    if (u >= u1) return false;
+    ti.next(a, s);
+    if (ti.tile >= ti.tiles) {
+      do s = sequence(a, ++b);
+      while (s.rows == 0);
+      ti.begin(a, s);
+    }
+    return true;
+  }
+  // What the join needs to know, if units k0 to k1 begin an item that goes on.
+  MX_DEV void leave_open(Open* open, int k0, int k1) const {
+    if (threadIdx.x == 0 && k0 == 0 && k1 < ti.units)
+      open[at] = Open{ti.tile, b, (int32_t)(((item + ti.units) * used - 1) / all)};  // the worker of the last unit
+  }
+};
+
+// ---------------------------------------------------------------------------------------------
+// Softmax.
+
+// What the scores are multiplied by before exp2.  Not 0, so that its product with a hidden position's -inf is one.
+template <int FMT>
+MX_DEV float score_scale(const AttendArgs& a) {
+  const float s = a.scale == 0.0f ? 1.0f : fabsf(a.scale);
+  return fmaxf(s * 1.44269504f / (FMT == MXFP4_FMT_NVFP4 ? a.cache.plane[0].gs : 1.0f), 1e-38f);
+}
+
+// Eight elements of a row of q: the scale's sign goes to them, and with a scale of 0 they are 0.
+MX_DEV bf16x8_t query8(const AttendArgs& a, const uint16_t* src) {
+  u32x4_t x = *reinterpret_cast<const u32x4_t*>(src);
+  const uint32_t keep = a.scale == 0.0f ? 0u : ~0u, sign = a.scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+  for (int j = 0; j < 4; j++) x[j] = (x[j] & keep) ^ sign;
+  return __builtin_bit_cast(bf16x8_t, x);
+}
+
+// The sums of a wave's 16 NT rows, of their weights too; the exponents' subtrahend m, and the score from which on it is
+// raised.
+template <int NT, int VT>
+struct Rows {
+  f32x4_t o[NT][VT], l[NT];
+  float m[NT], limit[NT];
+
+  MX_DEV void clear() {
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+      m[n] = limit[n] = -INFINITY;
+      l[n] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int v = 0; v < VT; v++) o[n][v] = f32x4_t{0, 0, 0, 0};
+    }
+  }
+
+  // Scores of 16 KT positions to weights in bf16.  m is raised, and all sums with it, where a score is over it by more than
+  // 8: weights stay below 2^8, and most tiles need no maximum over the row's four lanes and no rescaling.
+  template <int KT>
+  MX_DEV void weights(const f32x4_t (&s)[NT][KT], float sc, bf16x8_t (&p)[NT][KT / 2]) {
+    bool over = false;
+    float top[NT];
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+      top[n] = s[n][0][0];
+#pragma unroll
+      for (int i = 1; i < 4 * KT; i++) top[n] = fmaxf(top[n], s[n][i >> 2][i & 3]);
+      over = over || top[n] > limit[n];
+    }
+    if (__any(over)) {
+#pragma unroll
+      for (int n = 0; n < NT; n++) {
+        top[n] = fmaxf(top[n], __shfl_xor(top[n], 16));
+        top[n] = fmaxf(top[n], __shfl_xor(top[n], 32));
+        const float now = fmaxf(m[n], top[n] * sc);
+        const float keep = now > -INFINITY ? __builtin_amdgcn_exp2f(m[n] - now) : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 4; i++) l[n][i] *= keep;
+#pragma unroll
+        for (int v = 0; v < VT; v++)
+#pragma unroll
+          for (int i = 0; i < 4; i++) o[n][v][i] *= keep;
+        m[n] = now;
+        limit[n] = (now + 8.0f) / sc;
+      }
+    }
+    // the weights' sum is taken of them as they are rounded, by the matrix instruction
+    const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+      const float by = m[n] > -INFINITY ? -m[n] : 0.0f;  // nothing seen yet
+#pragma unroll
+      for (int h = 0; h < KT / 2; h++) {
+        float w[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) w[i] = __builtin_amdgcn_exp2f(fmaf(s[n][2 * h + (i >> 2)][i & 3], sc, by));
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const bf16x2_t two = __builtin_convertvector(f32x2_t{w[i], w[i + 1]}, bf16x2_t);
+          p[n][h][i] = two[0];
+          p[n][h][i + 1] = two[1];
+        }
+        l[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, p[n][h], l[n], 0, 0, 0);
+      }
+    }
+  }
+
+  // O^T += V^T P^T for 32 positions: their values are rows of LDS, `stride` elements apart.
+  template <int KT>
+  MX_DEV void add_values(const uint16_t* v0, int stride, const bf16x8_t (&p)[NT][KT], int h, int lane) {
+    // two blocks of four positions by sixteen elements a group of sixteen lanes, transposed
+    typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
+    const int col = lane & 15, kg = lane >> 4;
+    const uint16_t* src = v0 + (4 * kg + (col >> 2)) * stride + 4 * (col & 3);
+#pragma unroll
+    for (int v = 0; v < VT; v++) {
+      const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src + 16 * v));
+      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src + 16 * stride + 16 * v));
+      const bf16x8_t x = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+      for (int n = 0; n < NT; n++) o[n][v] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, p[n][h], o[n][v], 0, 0, 0);
+    }
+  }
+
+  // Adds the rows' sums, brought to the maxima `top`, to those in LDS (first: puts them there).
+  MX_DEV void join(float* sums, int stride, const float (&top)[NT], bool first, int lane) const {
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+      const float f = top[n] > -INFINITY ? __builtin_amdgcn_exp2f(m[n] - top[n]) : 0.0f;
+      float* dst = sums + (16 * n + (lane & 15)) * stride + 4 * (lane >> 4);
+#pragma unroll
+      for (int v = 0; v < VT; v++) {
+        f32x4_t x = o[n][v];
+#pragma unroll
+        for (int i = 0; i < 4; i++) x[i] *= f;
+        if (!first) {
+          const f32x4_t y = *reinterpret_cast<const f32x4_t*>(dst + 16 * v);
+#pragma unroll
+          for (int i = 0; i < 4; i++) x[i] += y[i];
+        }
+        *reinterpret_cast<f32x4_t*>(dst + 16 * v) = x;
+      }
+    }
+  }
+};
+
+// Takes from the scores of a tile's 16 KT positions from `base` on what the rows do not see: there, bad: bits of positions
+// that have a page, and whose values are not finite.
+template <int NT, int KT>
+MX_DEV void hide(const AttendArgs& a, const Seq& s, const int32_t (&draft)[NT], int32_t base, uint64_t there, uint64_t bad, int kg,
+                 f32x4_t (&sv)[NT][KT]) {
+  const int64_t first = (int64_t)base - s.start + 4 * kg;  // as a draft: the first position of this lane
+#pragma unroll
+  for (int n = 0; n < NT; n++) {
+    // drafts from `most` on are not seen
+    const int64_t most = draft[n] < 0 ? INT64_MIN : a.mask ? min(s.drafts, a.mask_cols) : (int64_t)draft[n] + 1;
+    const uint8_t* mask = a.mask + (int64_t)(s.first + max(draft[n], 0)) * a.ld_mask;
+    uint32_t seen = 0, nan = 0;  // bit 4 t + i; a loop, which costs no registers of the one around
+#pragma unroll 1
+    for (int t = 0; t < KT; t++) {
+      uint32_t four = (uint32_t)(there >> (16 * t + 4 * kg)) & 15u;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const int64_t j = first + 16 * t + i;
+        if (j >= most || (j >= 0 && a.mask && !mask[j])) four &= ~(1u << i);
+      }
+      seen |= four << (4 * t);
+      nan |= ((uint32_t)(bad >> (16 * t + 4 * kg)) & four) << (4 * t);
+    }
+#pragma unroll
+    for (int t = 0; t < KT; t++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        if (nan >> (4 * t + i) & 1) sv[n][t][i] = NAN;
+        if (!(seen >> (4 * t + i) & 1)) sv[n][t][i] = -INFINITY;
+      }
+  }
+}
+
+// The result of `n` of an item's rows from `r0` on, or its part for the join: their sums in LDS, and the maxima and sums of
+// weights of the PARTS waves that had them.
+template <int FMT, int DV, int MT, int PARTS, int UNIT>
+MX_DEV void write_item(const AttendArgs& a, const Work<MT, UNIT>& w, int k0, int k1, int r0, int n, const float* sums, const float (&ms)[PARTS][MT],
+                       const float (&ls)[PARTS][MT], float* part, float2* part_ml) {
+  const int there = min(n, w.s.rows * a.group - w.ti.tile * MT - r0);
+  const bool whole = k0 == 0 && k1 == w.ti.units;
+  const int64_t slot = 2 * w.at + (k0 == 0 ? 1 : 0);
+  for (int id = threadIdx.x; id < there * (DV / 8); id += kThreads) {
+    const int r = r0 + id / (DV / 8), e = id % (DV / 8) * 8;
+    float top = ms[0][r], sum = 0.0f;
+#pragma unroll
+    for (int x = 1; x < PARTS; x++) top = fmaxf(top, ms[x][r]);
+#pragma unroll
+    for (int x = 0; x < PARTS; x++) sum += top > -INFINITY ? ls[x][r] * __builtin_amdgcn_exp2f(ms[x][r] - top) : 0.0f;
+    const f32x4_t* src = reinterpret_cast<const f32x4_t*>(sums + (r - r0) * (DV + 4) + e);
+    const f32x4_t x = src[0], y = src[1];
+    if (!whole) {
+      f32x4_t* dst = reinterpret_cast<f32x4_t*>(part + (slot * MT + r) * DV + e);
+      dst[0] = x;
+      dst[1] = y;
+      if (e == 0) part_ml[slot * MT + r] = float2{top, sum};
+    } else if (e < a.cache.plane[1].dim) {
+      write_row<FMT>(a, w.s, w.ti.tile * MT + r, w.g, e, x, y, sum);
+    }
+  }
+}
+
+}  // namespace

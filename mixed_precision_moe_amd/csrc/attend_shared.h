@@ -1,0 +1,241 @@
+// Attention for many rows a key head: a worker's waves share tiles of K and V, dequantized into LDS.
+//
+// A worker takes 32 WR rows, WR waves of 32 rows each; with WR = 2 the waves come in two groups that have half of each
+// tile's positions.  Per tile every thread dequantizes its pieces of 16 bytes of codes, so that is paid once for all rows, and
+// codes leave the caches once for all of them.  Two tiles of K and V are in LDS: while one is worked on, the codes of the next
+// are on their way to registers, and they are dequantized into the other behind it, with one barrier a tile.  Pages are
+// looked up three tiles ahead.
+#pragma once
+
+#include "attend_common.h"
+
+namespace {
+
+template <int FMT, int DK, int DV, int WR, int KEYS>
+struct Shared {
+  static constexpr int kWK = kWaves / WR;       // groups of waves that share the positions
+  static constexpr int kRows = 32 * WR;
+  static constexpr int kKT = KEYS / kWK / 16;   // tiles of 16 positions of a wave
+  static constexpr int kElems = 16 * kPerByte<FMT>;
+  static constexpr int kScales = kElems / kBlock<FMT> ? kElems / kBlock<FMT> : 1;
+  static constexpr int kStrideK = DK + 16, kStrideV = DV + 16;  // rows 32 bytes on: eight of them meet no bank twice
+  static constexpr int kTileBytes = 2 * KEYS * (kStrideK + kStrideV);
+};
+
+// A thread's pieces of a plane's tile.
+template <int FMT, int KEYS, int D>
+struct Pieces {
+  static constexpr int kElems = 16 * kPerByte<FMT>, kPerKey = D / kElems, kAll = KEYS * kPerKey;
+  static constexpr int kN = (kAll + kThreads - 1) / kThreads;
+  static constexpr int kScales = kElems / kBlock<FMT> ? kElems / kBlock<FMT> : 1;
+  u32x4_t codes[kN];
+  uint32_t scales[kN][kScales];
+
+  // vectors: the cache's vector of each position, -1: none
+  MX_DEV void load(const CachePlane& p, const int64_t* vectors) {
+    const int64_t bytes = p.dim / kPerByte<FMT>;
+    const int blocks = p.dim / kBlock<FMT>;
+#pragma unroll
+    for (int i = 0; i < kN; i++) {
+      const int id = i * kThreads + threadIdx.x, key = id / kPerKey, piece = id % kPerKey, e = piece * kElems;
+      codes[i] = u32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < kScales; j++) scales[i][j] = 0;
+      if (kAll % kThreads && id >= kAll) continue;
+      const int64_t at = vectors[key];
+      if (at < 0 || e >= p.dim) continue;
+      const uint8_t* src = p.q + at * bytes + 16 * piece;
+      const uint8_t* s = p.s + at * blocks + e / kBlock<FMT>;
+      if (e + kElems <= p.dim) {
+        codes[i] = *reinterpret_cast<const u32x4_a8*>(src);
+      } else {
+        const u32x2_t x = *reinterpret_cast<const u32x2_a8*>(src);
+        codes[i][0] = x[0];
+        codes[i][1] = x[1];
+      }
+#pragma unroll
+      for (int j = 0; j < kScales; j++)
+        if (e + j * kBlock<FMT> < p.dim) scales[i][j] = s[j];
+    }
+  }
+
+  // Dequantized, to rows of LDS.
+  MX_DEV void store(uint16_t* dst, int stride) const {
+#pragma unroll
+    for (int i = 0; i < kN; i++) {
+      const int id = i * kThreads + threadIdx.x, key = id / kPerKey, piece = id % kPerKey;
+      if (kAll % kThreads && id >= kAll) continue;
+      uint16_t* to = dst + key * stride + piece * kElems;
+#pragma unroll
+      for (int j = 0; j < kElems / 8; j++)
+        *reinterpret_cast<bf16x8_t*>(to + 8 * j) = FMT == MXFP4_FMT_MXFP8 ? values8<FMT>(codes[i][2 * j], codes[i][2 * j + 1], scales[i][0])
+                                                                          : values8<FMT>(codes[i][j], 0, scales[i][8 * j / kBlock<FMT>]);
+    }
+  }
+
+  // Positions whose values are not finite become zeros and leave their bit in `bad`.
+  MX_DEV void drop_not_finite(uint32_t* bad) {
+#pragma unroll
+    for (int i = 0; i < kN; i++) {
+      const int id = i * kThreads + threadIdx.x, key = id / kPerKey;
+      bool x = false;
+#pragma unroll
+      for (int j = 0; j < kScales; j++) x = x || not_finite<FMT>(scales[i][j]);
+      if (FMT == MXFP4_FMT_MXFP8)
+        x = x || has_nan_code(codes[i][0]) || has_nan_code(codes[i][1]) || has_nan_code(codes[i][2]) || has_nan_code(codes[i][3]);
+      if (!x) continue;
+      codes[i] = u32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < kScales; j++) scales[i][j] = 0;
+      atomicOr(&bad[key >> 5], 1u << (key & 31));
+    }
+  }
+};
+
+template <int FMT, int DK, int DV, int WR, int KEYS, int WAVES>
+__global__ __launch_bounds__(kThreads, WAVES) void attend_shared_kernel(AttendArgs a, float* __restrict__ part,
+                                                                        float2* __restrict__ part_ml,
+                                                                        Open* __restrict__ open, int workers) {
+  using Sh = Shared<FMT, DK, DV, WR, KEYS>;
+  constexpr int MT = Sh::kRows, NT = 2, KT = Sh::kKT;
+  static_assert(KT % 2 == 0 && KEYS <= 64, "32 positions a matrix instruction, and 64 a lookup");
+  constexpr int kBytes = 2 * Sh::kTileBytes;
+  // the sums take the place of the tiles, as many groups of 32 rows at a time as fit
+  constexpr int kFit = kBytes / (32 * (DV + 4) * 4), kGroups = kFit < WR ? kFit : WR;
+  static_assert(kGroups > 0 && WR % kGroups == 0, "whole passes");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kBytes];
+  __shared__ int64_t vectors[4][KEYS];
+  __shared__ uint64_t valid[4];
+  __shared__ uint32_t bad[4][2];
+  __shared__ float ms[Sh::kWK][MT], ls[Sh::kWK][MT];
+  const CacheArgs& c = a.cache;
+  const CachePlane &pk = c.plane[0], &pv = c.plane[1];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, kg = lane >> 4;
+  const int wr = wave % WR, wk = wave / WR;
+  Work<MT, KEYS> w;
+  if (!w.begin(a, workers, open, lane)) return;
+  const float sc = score_scale<FMT>(a);
+
+  for (;;) {
+    const Seq& s = w.s;
+    const int32_t k0 = (int32_t)(w.u - w.item), k1 = (int32_t)min((int64_t)w.ti.units, w.u1 - w.item), end = w.ti.end;
+    bf16x8_t q[NT][DK / 32];
+    int32_t draft[NT];  // -1: no such row
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+      const int32_t r = w.ti.tile * MT + 32 * wr + 16 * n + col;
+      const int32_t d = (uint32_t)r / (uint32_t)a.group;
+      draft[n] = d < s.rows ? d : -1;
+      const uint16_t* src = (const uint16_t*)pk.rows + (int64_t)(s.first + d) * pk.ldt + (w.g * a.group + (r - d * a.group)) * pk.ldh;
+#pragma unroll
+      for (int i = 0; i < DK / 32; i++) {
+        const int e = 32 * i + 8 * kg;
+        q[n][i] = __builtin_bit_cast(bf16x8_t, u32x4_t{0, 0, 0, 0});
+        if (draft[n] >= 0 && e < pk.dim) q[n][i] = query8(a, src + e);
+      }
+    }
+    Rows<NT, DV / 16> rows;
+    rows.clear();
+
+    const int32_t* const pages = c.table + (int64_t)w.b * c.ld_table;
+    // the vector of this lane's position of tile k
+    const auto find = [&](int32_t k) -> int64_t {
+      const int32_t pos = k * KEYS + lane;
+      if (lane >= KEYS || pos >= end) return -1;
+      const uint32_t p = a.page_shift >= 0 ? (uint32_t)pos >> a.page_shift : (uint32_t)pos / (uint32_t)c.page_size;
+      const int32_t page = pages[p];
+      if (page < 0 || page >= c.num_pages) return -1;
+      return ((int64_t)page * c.page_size + ((uint32_t)pos - p * (uint32_t)c.page_size)) * c.heads + w.g;
+    };
+    const auto note = [&](int32_t k, int64_t vector) {
+      if (lane < KEYS) vectors[k & 3][lane] = vector;
+      const uint64_t there = __ballot(vector >= 0);
+      if (lane == 0) valid[k & 3] = there;
+    };
+    Pieces<FMT, KEYS, DK> kp;
+    Pieces<FMT, KEYS, DV> vp;
+    const auto tile_k = [&](int32_t k) { return (uint16_t*)(lds + (k & 1) * Sh::kTileBytes); };
+    const auto tile_v = [&](int32_t k) { return (uint16_t*)(lds + (k & 1) * Sh::kTileBytes) + KEYS * Sh::kStrideK; };
+    const auto load = [&](int32_t k) {
+      kp.load(pk, vectors[k & 3]);
+      vp.load(pv, vectors[k & 3]);
+    };
+    const auto store = [&](int32_t k) {
+      // hidden drafts' values must not meet zero weights unless they are numbers
+      if ((int64_t)k * KEYS + KEYS > s.start) vp.drop_not_finite(bad[k & 3]);
+      kp.store(tile_k(k), Sh::kStrideK);
+      vp.store(tile_v(k), Sh::kStrideV);
+    };
+
+    if (threadIdx.x < 8) (&bad[0][0])[threadIdx.x] = 0;
+    if (wave < 3) note(k0 + wave, find(k0 + wave));
+    __syncthreads();
+    load(k0);
+    store(k0);
+    if (k0 + 1 < k1) load(k0 + 1);
+    __syncthreads();
+    for (int32_t k = k0; k < k1; k++) {
+      const int32_t base = k * KEYS + 16 * KT * wk;
+      int64_t ahead = -1;
+      if (wave == 0 && k + 3 < k1) ahead = find(k + 3);
+      f32x4_t sv[NT][KT];
+      const uint16_t* keys = tile_k(k) + (16 * KT * wk + col) * Sh::kStrideK + 8 * kg;
+#pragma unroll
+      for (int t = 0; t < KT; t++) {
+#pragma unroll
+        for (int n = 0; n < NT; n++) sv[n][t] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < DK / 32; i++) {
+          const bf16x8_t x = *reinterpret_cast<const bf16x8_t*>(keys + 16 * t * Sh::kStrideK + 32 * i);
+#pragma unroll
+          for (int n = 0; n < NT; n++) sv[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, q[n][i], sv[n][t], 0, 0, 0);
+        }
+      }
+      constexpr uint64_t kFull = KT == 4 ? ~0ull : ~0u;
+      const uint64_t there = valid[k & 3] >> (16 * KT * wk) & kFull;
+      if (there != kFull || (int64_t)base + 16 * KT > s.start) {
+        const uint64_t b = (uint64_t)bad[k & 3][1] << 32 | bad[k & 3][0];
+        hide<NT, KT>(a, s, draft, base, there, b >> (16 * KT * wk), kg, sv);
+      }
+      bf16x8_t p[NT][KT / 2];
+      rows.template weights<KT>(sv, sc, p);
+#pragma unroll
+      for (int h = 0; h < KT / 2; h++)
+        rows.template add_values<KT / 2>(tile_v(k) + (16 * KT * wk + 32 * h) * Sh::kStrideV, Sh::kStrideV, p, h, lane);
+      // the other tiles' turn
+      if (k + 1 < k1) store(k + 1);
+      if (k + 2 < k1) load(k + 2);
+      if (wave == 0 && k + 3 < k1) note(k + 3, ahead);
+      if (threadIdx.x < 2) bad[(k + 2) & 3][threadIdx.x] = 0;
+      __syncthreads();
+    }
+
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+      if (kg == 0) {
+        ms[wk][32 * wr + 16 * n + col] = rows.m[n];
+        ls[wk][32 * wr + 16 * n + col] = rows.l[n][0];
+      }
+    for (int first = 0; first < WR; first += kGroups) {
+      for (int x = 0; x < Sh::kWK; x++) {
+        __syncthreads();
+        if (x != wk || wr < first || wr >= first + kGroups) continue;
+        float top[NT];
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+          top[n] = ms[0][32 * wr + 16 * n + col];
+#pragma unroll
+          for (int y = 1; y < Sh::kWK; y++) top[n] = fmaxf(top[n], ms[y][32 * wr + 16 * n + col]);
+        }
+        rows.join((float*)lds + 32 * (wr - first) * (DV + 4), DV + 4, top, x == 0, lane);
+      }
+      __syncthreads();
+      write_item<FMT, DV, MT, Sh::kWK, KEYS>(a, w, k0, k1, 32 * first, 32 * kGroups, (const float*)lds, ms, ls, part, part_ml);
+    }
+    w.leave_open(open, k0, k1);
+    __syncthreads();
+    if (!w.next(a, k1 - k0)) break;
+  }
+}
+
+}  // namespace

@@ -1,0 +1,309 @@
+// Attention for few rows a key head: the four waves of a worker take 32 positions of a unit each and meet once an item.
+//
+// Codes of K go from memory to registers as they are needed there (a lane: a quarter of a key's elements); V's are
+// dequantized into the wave's own piece of LDS.  The next tile's codes are on their way while a tile is worked on: K's
+// during its softmax and second product, V's during the next tile's first product.
+#pragma once
+
+#include "attend_common.h"
+
+namespace {
+
+constexpr int kTile = 32;               // positions of a wave at a time
+constexpr int kUnit = kTile * kWaves;   // and of a worker
+
+template <int FMT, int DK, int DV, int NT>
+struct Shape {
+  static constexpr int kRows = 16 * NT;
+  static constexpr int kSteps = DK / 32;                       // matrix instructions a 16 x 16 tile of S
+  static constexpr int kQuarter = DK / 4;                      // elements of a key in a lane
+  static constexpr int kCodes = kQuarter / kPerByte<FMT> / 4;  // registers of their codes
+  // scales of a lane's quarter: it may begin inside a block
+  static constexpr int kScales = kQuarter <= kBlock<FMT> ? 1 : (kQuarter + kBlock<FMT> - 1) / kBlock<FMT>;
+  static constexpr int kElems = 16 * kPerByte<FMT>;            // elements of a 16-byte piece of V
+  static constexpr int kPerKey = DV / kElems;
+  static constexpr int kPieces = kTile * kPerKey / 64;
+  static constexpr int kPieceScales = kElems / kBlock<FMT> ? kElems / kBlock<FMT> : 1;
+  static constexpr int kVT = DV / 16;
+  static constexpr int kStride = DV + 16;  // of V's rows in LDS: 32 bytes on, so that eight rows meet no bank twice
+};
+
+// PAGED: pages of whole tiles, and dimensions that are DK and DV.  A tile's page is then looked up once, and a lane's part
+// of the addresses does not change from tile to tile.
+template <int FMT, int DK, int DV, int NT, int WAVES, bool PAGED>
+__global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArgs a, float* __restrict__ part,
+                                                                 float2* __restrict__ part_ml, Open* __restrict__ open,
+                                                                 int workers) {
+  using Sh = Shape<FMT, DK, DV, NT>;
+  using Found = std::conditional_t<PAGED, int32_t, int64_t>;
+  constexpr int MT = Sh::kRows;
+  constexpr int kBytes = kWaves * kTile * Sh::kStride * 2;
+  static_assert(MT * (DV + 4) * 4 <= kBytes, "the sums take the place of V");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kBytes];
+  __shared__ float ms[kWaves][MT], ls[kWaves][MT];
+  const CacheArgs& c = a.cache;
+  const CachePlane &pk = c.plane[0], &pv = c.plane[1];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, kg = lane >> 4;
+  Work<MT, kUnit> w;
+  if (!w.begin(a, workers, open, lane)) return;
+  const float sc = score_scale<FMT>(a);
+  const int k_dim = PAGED ? DK : pk.dim, v_dim = PAGED ? DV : pv.dim;
+  const int64_t k_bytes = k_dim / kPerByte<FMT>, v_bytes = v_dim / kPerByte<FMT>;
+  const int k_blocks = k_dim / kBlock<FMT>, v_blocks = v_dim / kBlock<FMT>;
+  // PAGED: this lane's part of the addresses of codes and scales
+  const uint32_t k_at = (uint32_t)(col * c.heads) * (DK / kPerByte<FMT>) + kg * (Sh::kCodes * 4);
+  const uint32_t ks_at = (uint32_t)(col * c.heads) * (DK / kBlock<FMT>) + kg * Sh::kQuarter / kBlock<FMT>;
+  const uint32_t v_at = (uint32_t)(lane / Sh::kPerKey * c.heads) * (DV / kPerByte<FMT>) + 16 * (lane % Sh::kPerKey);
+  const uint32_t vs_at = (uint32_t)(lane / Sh::kPerKey * c.heads) * (DV / kBlock<FMT>) + lane % Sh::kPerKey * Sh::kElems / kBlock<FMT>;
+  uint16_t* const vt = (uint16_t*)lds + wave * kTile * Sh::kStride;
+
+  for (;;) {
+    const Seq& s = w.s;
+    const int32_t k0 = (int32_t)(w.u - w.item), k1 = (int32_t)min((int64_t)w.ti.units, w.u1 - w.item), end = w.ti.end;
+    // the rows of this lane's columns
+    bf16x8_t q[NT][Sh::kSteps];
+    int32_t draft[NT];  // -1: no such row
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+      const int32_t r = w.ti.tile * MT + 16 * n + col;
+      const int32_t d = (uint32_t)r / (uint32_t)a.group;
+      draft[n] = d < s.rows ? d : -1;
+      const uint16_t* src = (const uint16_t*)pk.rows + (int64_t)(s.first + d) * pk.ldt + (w.g * a.group + (r - d * a.group)) * pk.ldh;
+#pragma unroll
+      for (int i = 0; i < Sh::kSteps; i++) {
+        const int e = kg * Sh::kQuarter + 8 * i;
+        q[n][i] = __builtin_bit_cast(bf16x8_t, u32x4_t{0, 0, 0, 0});
+        if (draft[n] >= 0 && e < k_dim) q[n][i] = query8(a, src + e);
+      }
+    }
+    Rows<NT, Sh::kVT> rows;
+    rows.clear();
+
+    // Where a tile's codes are.  PAGED: its page, in every lane; else the cache's vector of each of its positions, -1: none,
+    // in the lanes 0 to 31.
+    const int32_t* const pages = c.table + (int64_t)w.b * c.ld_table;
+    const auto find = [&](int32_t k) {
+      const int32_t pos = k * kUnit + wave * kTile + (PAGED ? 0 : lane & 31);
+      Found f = -1;
+      if (pos < end) {
+        const uint32_t p = a.page_shift >= 0 ? (uint32_t)pos >> a.page_shift : (uint32_t)pos / (uint32_t)c.page_size;
+        const int32_t page = pages[p];
+        if (PAGED)
+          f = page;
+        else if (page >= 0 && page < c.num_pages)
+          f = ((int64_t)page * c.page_size + ((uint32_t)pos - p * (uint32_t)c.page_size)) * c.heads + w.g;
+      }
+      return f;
+    };
+    // PAGED: the tile's first vector, -1: none.  Its positions past the end lie in the page too.
+    const auto first_vector = [&](int32_t k, Found f) -> int64_t {
+      const int32_t page = __builtin_amdgcn_readfirstlane((int)f);
+      if (page < 0 || page >= c.num_pages) return -1;
+      const uint32_t pos = (uint32_t)k * kUnit + (uint32_t)wave * kTile;
+      const uint32_t in_page = a.page_shift >= 0 ? pos & (uint32_t)(c.page_size - 1) : pos % (uint32_t)c.page_size;
+      return ((int64_t)page * c.page_size + in_page) * c.heads + w.g;
+    };
+    uint32_t kc[2][Sh::kCodes], ks[2][Sh::kScales];
+    // a lane's quarter of a key
+    const auto load_key = [&](int t, const uint8_t* src, const uint8_t* scales) {
+      if (PAGED || pk.dim == DK) {
+        if constexpr (Sh::kCodes % 4 == 0) {
+#pragma unroll
+          for (int i = 0; i < Sh::kCodes; i += 4) {
+            const u32x4_t x = *reinterpret_cast<const u32x4_a8*>(src + 4 * i);
+            kc[t][i] = x[0];
+            kc[t][i + 1] = x[1];
+            kc[t][i + 2] = x[2];
+            kc[t][i + 3] = x[3];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < Sh::kCodes; i += 2) {
+            const u32x2_t x = *reinterpret_cast<const u32x2_a8*>(src + 4 * i);
+            kc[t][i] = x[0];
+            kc[t][i + 1] = x[1];
+          }
+        }
+      } else {
+        constexpr int per = FMT == MXFP4_FMT_MXFP8 ? 2 : 1;  // registers of eight codes
+#pragma unroll
+        for (int i = 0; i < Sh::kSteps; i++) {
+          const int e = kg * Sh::kQuarter + 8 * i;
+#pragma unroll
+          for (int j = 0; j < per; j++) {
+            kc[t][per * i + j] = 0;
+            if (e < pk.dim) kc[t][per * i + j] = *reinterpret_cast<const uint32_t*>(src + 4 * (per * i + j));
+          }
+        }
+      }
+      const int b0 = kg * Sh::kQuarter / kBlock<FMT>;
+#pragma unroll
+      for (int i = 0; i < Sh::kScales; i++) {
+        ks[t][i] = 0;
+        if (PAGED || b0 + i < k_blocks) ks[t][i] = scales[i];
+      }
+    };
+    const auto load_k = [&](int32_t k, Found f) {
+      const int64_t first = PAGED ? first_vector(k, f) : 0;
+#pragma unroll
+      for (int t = 0; t < 2; t++) {
+        if (PAGED) {  // the tile's part of the addresses is the same for all lanes, the lane's for all tiles
+          const int64_t at = first + 16 * t * c.heads;
+          if (first >= 0) load_key(t, pk.q + at * k_bytes + k_at, pk.s + at * k_blocks + ks_at);
+        } else {
+          const int64_t at = shfl64(f, 16 * t + col);
+          if (at >= 0) load_key(t, pk.q + at * k_bytes + kg * (Sh::kCodes * 4), pk.s + at * k_blocks + kg * Sh::kQuarter / kBlock<FMT>);
+        }
+      }
+    };
+    u32x4_t vc[Sh::kPieces];
+    uint32_t vs[Sh::kPieces][Sh::kPieceScales];
+    const auto load_piece = [&](int i, const uint8_t* src, const uint8_t* scales) {
+      const int e = lane % Sh::kPerKey * Sh::kElems;
+      if (PAGED || e + Sh::kElems <= pv.dim) {
+        vc[i] = *reinterpret_cast<const u32x4_a8*>(src);
+      } else if (e < pv.dim) {
+        const u32x2_t x = *reinterpret_cast<const u32x2_a8*>(src);
+        vc[i] = u32x4_t{x[0], x[1], 0, 0};
+      }
+      const int b0 = e / kBlock<FMT>;
+#pragma unroll
+      for (int j = 0; j < Sh::kPieceScales; j++)
+        if (PAGED || b0 + j < v_blocks) vs[i][j] = scales[j];
+    };
+    const auto load_v = [&](int32_t k, Found f) {
+      const int64_t first = PAGED ? first_vector(k, f) : 0;
+#pragma unroll
+      for (int i = 0; i < Sh::kPieces; i++) {
+        constexpr int keys = 64 / Sh::kPerKey;  // of 64 pieces
+        if (PAGED) {
+          const int64_t at = first + keys * i * c.heads;
+          if (first >= 0) load_piece(i, pv.q + at * v_bytes + v_at, pv.s + at * v_blocks + vs_at);
+        } else {
+          vc[i] = u32x4_t{0, 0, 0, 0};
+#pragma unroll
+          for (int j = 0; j < Sh::kPieceScales; j++) vs[i][j] = 0;
+          const int64_t at = shfl64(f, keys * i + lane / Sh::kPerKey);
+          const int piece = lane % Sh::kPerKey;
+          if (at >= 0) load_piece(i, pv.q + at * v_bytes + 16 * piece, pv.s + at * v_blocks + piece * Sh::kElems / kBlock<FMT>);
+        }
+      }
+    };
+
+    Found found = find(k0);
+    load_k(k0, found);
+    load_v(k0, found);
+    for (int32_t k = k0; k < k1; k++) {
+      const int32_t base = k * kUnit + wave * kTile;
+      // which of the tile's positions have a vector, and whether all rows see them all
+      uint32_t there;
+      if (PAGED) {
+        const int32_t page = __builtin_amdgcn_readfirstlane((int)found);
+        const int32_t left = end - base;
+        there = page < 0 || page >= c.num_pages || left <= 0 ? 0u : left >= kTile ? ~0u : (1u << left) - 1;
+      } else {
+        there = (uint32_t)__ballot(found >= 0);
+      }
+      const bool whole = there == ~0u && base + kTile <= s.start;
+      const Found next = k + 1 < k1 ? find(k + 1) : -1;
+
+      f32x4_t sv[NT][2];
+#pragma unroll
+      for (int t = 0; t < 2; t++) {
+#pragma unroll
+        for (int n = 0; n < NT; n++) sv[n][t] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < Sh::kSteps; i++) {
+          constexpr int per = FMT == MXFP4_FMT_MXFP8 ? 2 : 1;
+          uint32_t scale = ks[t][0];
+          if constexpr (Sh::kScales > 1) {
+            // the block of this chunk, counted from the quarter's first; the quarter may begin inside one
+            constexpr int B = kBlock<FMT>;
+            const int even = 8 * i / B, odd = (Sh::kQuarter % B + 8 * i) / B;  // kg even, kg odd
+            scale = Sh::kQuarter % B && (kg & 1) ? ks[t][odd < Sh::kScales ? odd : Sh::kScales - 1] : ks[t][even];
+          }
+          const bf16x8_t x = values8<FMT>(kc[t][per * i], kc[t][per * i + per - 1], scale);
+#pragma unroll
+          for (int n = 0; n < NT; n++) sv[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, q[n][i], sv[n][t], 0, 0, 0);
+        }
+      }
+      if (k + 1 < k1) load_k(k + 1, next);
+
+      if (!whole) {
+        // Positions whose values are not finite must not meet the zero weights of rows that do not see them: they count as
+        // zeros, and make the score of rows that do see them NaN.  Those without a page count as zeros.
+        uint32_t bad = 0;
+        if (base + kTile > s.start) {
+#pragma unroll
+          for (int i = 0; i < Sh::kPieces; i++) {
+            bool x = false;
+#pragma unroll
+            for (int j = 0; j < Sh::kPieceScales; j++) x = x || not_finite<FMT>(vs[i][j]);
+            if (FMT == MXFP4_FMT_MXFP8)
+              x = x || has_nan_code(vc[i][0]) || has_nan_code(vc[i][1]) || has_nan_code(vc[i][2]) || has_nan_code(vc[i][3]);
+            for (uint64_t who = __ballot(x); who; who &= who - 1)
+              bad |= 1u << ((i * 64 + __ffsll((unsigned long long)who) - 1) / Sh::kPerKey);
+          }
+        }
+        if (const uint32_t zero = bad | ~there) {
+#pragma unroll
+          for (int i = 0; i < Sh::kPieces; i++)
+            if (zero >> ((i * 64 + lane) / Sh::kPerKey) & 1) {
+              vc[i] = u32x4_t{0, 0, 0, 0};
+#pragma unroll
+              for (int j = 0; j < Sh::kPieceScales; j++) vs[i][j] = 0;
+            }
+        }
+        hide<NT, 2>(a, s, draft, base, there, bad, kg, sv);
+      }
+
+      bf16x8_t p[NT][1];
+      rows.template weights<2>(sv, sc, p);
+
+      // V into LDS, a row a position
+#pragma unroll
+      for (int i = 0; i < Sh::kPieces; i++) {
+        const int id = i * 64 + lane;
+        uint16_t* dst = vt + id / Sh::kPerKey * Sh::kStride + id % Sh::kPerKey * Sh::kElems;
+#pragma unroll
+        for (int j = 0; j < Sh::kElems / 8; j++) {
+          const bf16x8_t x = FMT == MXFP4_FMT_MXFP8 ? values8<FMT>(vc[i][2 * j], vc[i][2 * j + 1], vs[i][0])
+                                                    : values8<FMT>(vc[i][j], 0, vs[i][8 * j / kBlock<FMT>]);
+          *reinterpret_cast<bf16x8_t*>(dst + 8 * j) = x;
+        }
+      }
+      if (k + 1 < k1) load_v(k + 1, next);
+      __builtin_amdgcn_wave_barrier();
+      rows.template add_values<1>(vt, Sh::kStride, p, 0, lane);
+      __builtin_amdgcn_wave_barrier();
+      found = next;
+    }
+
+    // the waves' sums, joined
+    float top[NT];
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+      if (kg == 0) {
+        ms[wave][16 * n + col] = rows.m[n];
+        ls[wave][16 * n + col] = rows.l[n][0];
+      }
+    for (int x = 0; x < kWaves; x++) {
+      __syncthreads();
+      if (x != wave) continue;
+#pragma unroll
+      for (int n = 0; n < NT; n++) {
+        top[n] = ms[0][16 * n + col];
+#pragma unroll
+        for (int y = 1; y < kWaves; y++) top[n] = fmaxf(top[n], ms[y][16 * n + col]);
+      }
+      rows.join((float*)lds, DV + 4, top, x == 0, lane);
+    }
+    __syncthreads();
+    write_item<FMT, DV, MT, kWaves, kUnit>(a, w, k0, k1, 0, MT, (const float*)lds, ms, ls, part, part_ml);
+    w.leave_open(open, k0, k1);
+    __syncthreads();
+    if (!w.next(a, k1 - k0)) break;
+  }
+}
+
+}  // namespace

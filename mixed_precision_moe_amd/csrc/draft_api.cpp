@@ -87,16 +87,16 @@ int pool_args(PoolArgs& a, int64_t num_pages, int32_t page_size, int32_t* refs, 
   return MXFP4_OK;
 }
 
-// The sizes of the attention kernels: dims up to 64, 128, 192 and 128, or 256; tiles of 16 to 64 rows (256: to 32), the
-// smallest that holds what a sequence has on average.
+// The sizes of the attention kernels: dims up to 64, 128, 192 and 128, or 256; tiles of rows by what a sequence has on average:
+// up to 16 and 32 the kernel whose waves split the positions, up to 64 (where it exists) and from there on the shared one.
 AttendPlan attend_plan(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows, int32_t n_seqs) {
   AttendPlan p = {};
   const int k = d->k_dim, v = d->v_dim;
   p.dk = k <= 64 && v <= 64 ? 64 : k <= 128 && v <= 128 ? 128 : k <= 192 && v <= 128 ? 192 : 256;
   p.dv = p.dk == 192 ? 128 : p.dk;
   const int64_t per_seq = (rows + n_seqs - 1) / (n_seqs > 0 ? n_seqs : 1) * (q_heads / d->heads);
-  const int64_t nt = (per_seq + 15) / 16, most = p.dk == 256 ? 2 : 4;
-  p.nt = (int32_t)(nt < 1 ? 1 : nt > most ? most : nt);
+  p.nt = per_seq <= 16 ? 1 : per_seq <= 32 ? 2 : per_seq <= 64 && attend_keys(p.dk) == 64 ? 4 : 8;
+  p.unit = p.nt <= 2 ? 128 : attend_keys(p.dk);
   const int64_t fill = (int64_t)kCus * attend_waves(p.dk, p.nt) / d->heads;
   p.workers = (int32_t)(fill < 1 ? 1 : fill < 8 ? fill : fill & ~int64_t(7));  // as many on each XCD
   uint64_t at = 0;

@@ -16,14 +16,16 @@ struct AttendArgs {
   int32_t rows_of_tile, part_of_tile;  // tile rows / group, and the remainder
   float scale;
 };
-// How a call is cut up: tiles of 16 nt rows, elements of a key and a value in the kernel, workers of each head; the
-// workspace's parts.
+// How a call is cut up: tiles of 16 nt rows, units of positions, elements of a key and a value in the kernel, workers of each
+// head; the workspace's parts.
 struct AttendPlan {
-  int32_t nt, dk, dv, workers;
+  int32_t nt, unit, dk, dv, workers;
   uint64_t part, ml, open, total;
 };
-// Workgroups of a compute unit: what their registers leave room for.
-constexpr int attend_waves(int dk, int nt) { return dk <= 128 ? (nt == 1 ? 3 : nt == 2 ? 2 : 1) : nt == 1 ? 2 : 1; }
+// Workgroups of a compute unit: what their registers and LDS leave room for.
+constexpr int attend_waves(int dk, int nt) { return nt == 1 ? (dk <= 128 ? 3 : 2) : dk <= 192 ? 2 : 1; }
+// Positions of a tile of the shared kernel.
+constexpr int attend_keys(int dk) { return dk <= 128 ? 64 : 32; }
 int launch_attend_mxfp4(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream);
 int launch_attend_nvfp4(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream);
 int launch_attend_mxfp8(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream);
