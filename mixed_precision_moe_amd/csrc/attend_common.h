@@ -44,10 +44,22 @@ constexpr int kBlock = FMT == MXFP4_FMT_NVFP4 ? 16 : 32;
 template <int FMT>
 constexpr int kPerByte = FMT == MXFP4_FMT_MXFP8 ? 1 : 2;
 
-// What a worker leaves for the join, next to its sums: the item that it begins and another worker ends.
+// What a worker leaves for the join, next to its sums: the item that it begins and others go on with.
 struct Open {
-  int32_t tile, seq, last;  // last: the worker that ends it; -1: none
+  int32_t tile, seq, rest;  // rest: units of the item behind the worker's range, 0: none
 };
+
+// The kernels' first argument, read again where it is needed: what the kernels use of it is more than the scalar registers
+// hold over their loops, and reading it back from where those are spilled costs vector instructions.
+MX_DEV AttendArgs arguments() {
+#ifdef __HIP_DEVICE_COMPILE__
+  auto* p = (const __attribute__((address_space(4))) AttendArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *p;
+#else
+  return AttendArgs{};
+#endif
+}
 
 // ---------------------------------------------------------------------------------------------
 // Eight values as bf16: c their codes (4-bit formats: c[0]), s the block's scale byte.
@@ -152,6 +164,7 @@ MX_DEV int64_t seq_units(const AttendArgs& a, const Seq& s) {
   return n;
 }
 
+MX_DEV int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }  // known to be the same for the wave
 MX_DEV int64_t shfl64(int64_t v, int lane) {
   const int lo = __shfl((int)v, lane), hi = __shfl((int)(v >> 32), lane);
   return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
@@ -209,18 +222,25 @@ MX_DEV void write_row(const AttendArgs& a, const Seq& s, int32_t r, int g, int e
   }
 }
 
-// A worker's range of units and where it is in it; every wave has the same.
+// The units [first, end) of a head's `all` that a worker has.
+MX_DEV void worker_range(int64_t all, int workers, int worker, int64_t& first, int64_t& end) {
+  const int64_t used = min((int64_t)workers, all);
+  first = end = 0;
+  if (worker >= used) return;
+  first = all / used * worker + all % used * worker / used;
+  end = all / used * (worker + 1) + all % used * (worker + 1) / used;
+}
+
+// Where a worker is in its range of units; every wave has the same.
 template <int MT, int UNIT>
 struct Work {
-  int g, worker, b;
-  int64_t at;               // of the worker, as the join counts them
-  int64_t all, used;        // units of the head, workers that have some
-  int64_t u, u1, item;      // next unit, end of the range, the item's first unit
+  int32_t g, worker, b, k0;  // k0: the first of the item's units that are the worker's
+  int64_t left;              // units from there on
   Seq s;
   Tiles<MT, UNIT> ti;
 
   // False: nothing to do.
-  MX_DEV bool begin(const AttendArgs& a, int workers, Open* open, int lane) {
+  MX_DEV bool begin(const AttendArgs& a, int workers, Open* open, int64_t* totals, int lane) {
     const CacheArgs& c = a.cache;
     // Workgroups go to the eight XCDs in turn: a worker's heads, which read pieces of the same tokens, share one.
     if (workers % 8 == 0) {
@@ -231,16 +251,16 @@ struct Work {
       g = blockIdx.x % c.heads;
       worker = blockIdx.x / c.heads;
     }
-    at = (int64_t)g * workers + worker;
-    all = 0;
+    int64_t all = 0, u, u1;
     for (int b0 = 0; b0 < c.n_seqs; b0 += 64) all += lane64(scan_units<MT, UNIT>(a, b0, lane), 63);
-    used = min((int64_t)workers, all);
-    if (threadIdx.x == 0) open[at] = Open{0, 0, -1};
-    if (worker >= used) return false;
-    u = all / used * worker + all % used * worker / used;
-    u1 = all / used * (worker + 1) + all % used * (worker + 1) / used;
+    if (threadIdx.x == 0) {
+      open[(int64_t)g * workers + worker] = Open{0, 0, 0};
+      if (worker == 0 && g == 0) *totals = all;  // the heads' units are alike
+    }
+    worker_range(all, workers, worker, u, u1);
+    if (u == u1) return false;
     b = 0;
-    item = 0;
+    int64_t item = 0;
     for (int b0 = 0; b0 < c.n_seqs; b0 += 64) {
       const int64_t sums = item + scan_units<MT, UNIT>(a, b0, lane);
       const uint64_t past = __ballot(sums > u);
@@ -258,13 +278,32 @@ struct Work {
       item += ti.units;
       ti.next(a, s);
     }
+    k0 = (int32_t)(u - item);
+    left = u1 - u;
     return true;
   }
-  // On to the next item, `done` units on.  False: the range ends.
-  MX_DEV bool next(const AttendArgs& a, int done) {
-    u += done;
-    item += ti.units;
-    if (u >= u1) return false;
+  // The end of the item's units that are the worker's.
+  MX_DEV int32_t k1() const { return (int32_t)min((int64_t)ti.units, k0 + left); }
+  // The same, in scalar registers again after a loop's end that the compiler takes to differ between lanes.
+  MX_DEV void settle() {
+    g = uniform(g);
+    worker = uniform(worker);
+    b = uniform(b);
+    k0 = uniform(k0);
+    left = lane64(left, 0);
+    s = Seq{uniform(s.first), uniform(s.drafts), uniform(s.rows), uniform(s.start)};
+    ti.tile = uniform(ti.tile);
+    ti.tiles = uniform(ti.tiles);
+    ti.end = uniform(ti.end);
+    ti.units = uniform(ti.units);
+    ti.row = uniform(ti.row);
+    ti.part = uniform(ti.part);
+  }
+  // On to the next item.  False: the range ends.
+  MX_DEV bool next(const AttendArgs& a) {
+    left -= k1() - k0;
+    if (left <= 0) return false;
+    k0 = 0;
     ti.next(a, s);
     if (ti.tile >= ti.tiles) {
       do s = sequence(a, ++b);
@@ -273,10 +312,9 @@ struct Work {
     }
     return true;
   }
-  // What the join needs to know, if units k0 to k1 begin an item that goes on.
-  MX_DEV void leave_open(Open* open, int k0, int k1) const {
-    if (threadIdx.x == 0 && k0 == 0 && k1 < ti.units)
-      open[at] = Open{ti.tile, b, (int32_t)(((item + ti.units) * used - 1) / all)};  // the worker of the last unit
+  // What the join needs to know, if the item begins here and goes on.
+  MX_DEV void leave_open(Open* open, int workers) const {
+    if (threadIdx.x == 0 && k0 == 0 && k1() < ti.units) open[(int64_t)g * workers + worker] = Open{ti.tile, b, ti.units - k1()};
   }
 };
 
@@ -442,11 +480,11 @@ MX_DEV void hide(const AttendArgs& a, const Seq& s, const int32_t (&draft)[NT], 
 // The result of `n` of an item's rows from `r0` on, or its part for the join: their sums in LDS, and the maxima and sums of
 // weights of the PARTS waves that had them.
 template <int FMT, int DV, int MT, int PARTS, int UNIT>
-MX_DEV void write_item(const AttendArgs& a, const Work<MT, UNIT>& w, int k0, int k1, int r0, int n, const float* sums, const float (&ms)[PARTS][MT],
+MX_DEV void write_item(const AttendArgs& a, const Work<MT, UNIT>& w, int workers, int r0, int n, const float* sums, const float (&ms)[PARTS][MT],
                        const float (&ls)[PARTS][MT], float* part, float2* part_ml) {
   const int there = min(n, w.s.rows * a.group - w.ti.tile * MT - r0);
-  const bool whole = k0 == 0 && k1 == w.ti.units;
-  const int64_t slot = 2 * w.at + (k0 == 0 ? 1 : 0);
+  const bool whole = w.k0 == 0 && w.k1() == w.ti.units;
+  const int64_t slot = 2 * ((int64_t)w.g * workers + w.worker) + (w.k0 == 0 ? 1 : 0);
   for (int id = threadIdx.x; id < there * (DV / 8); id += kThreads) {
     const int r = r0 + id / (DV / 8), e = id % (DV / 8) * 8;
     float top = ms[0][r], sum = 0.0f;

@@ -93,9 +93,9 @@ struct Pieces {
 };
 
 template <int FMT, int DK, int DV, int WR, int KEYS, int WAVES>
-__global__ __launch_bounds__(kThreads, WAVES) void attend_shared_kernel(AttendArgs a, float* __restrict__ part,
+__global__ __launch_bounds__(kThreads, WAVES) void attend_shared_kernel(AttendArgs given, float* __restrict__ part,
                                                                         float2* __restrict__ part_ml,
-                                                                        Open* __restrict__ open, int workers) {
+                                                                        Open* __restrict__ open, int64_t* __restrict__ totals, int workers) {
   using Sh = Shared<FMT, DK, DV, WR, KEYS>;
   constexpr int MT = Sh::kRows, NT = 2, KT = Sh::kKT;
   static_assert(KT % 2 == 0 && KEYS <= 64, "32 positions a matrix instruction, and 64 a lookup");
@@ -108,19 +108,20 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_shared_kernel(AttendAr
   __shared__ uint64_t valid[4];
   __shared__ uint32_t bad[4][2];
   __shared__ float ms[Sh::kWK][MT], ls[Sh::kWK][MT];
-  const CacheArgs& c = a.cache;
-  const CachePlane &pk = c.plane[0], &pv = c.plane[1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, kg = lane >> 4;
   const int wr = wave % WR, wk = wave / WR;
   Work<MT, KEYS> w;
-  if (!w.begin(a, workers, open, lane)) return;
-  const float sc = score_scale<FMT>(a);
+  if (!w.begin(given, workers, open, totals, lane)) return;
+  const float sc = score_scale<FMT>(given);
 
   for (;;) {
+    w.settle();
     const Seq& s = w.s;
-    const int32_t k0 = (int32_t)(w.u - w.item), k1 = (int32_t)min((int64_t)w.ti.units, w.u1 - w.item), end = w.ti.end;
+    const int32_t k0 = w.k0, k1 = w.k1(), end = w.ti.end;
     bf16x8_t q[NT][DK / 32];
     int32_t draft[NT];  // -1: no such row
+    const AttendArgs a = arguments();
+    const CachePlane& pk = a.cache.plane[0];
 #pragma unroll
     for (int n = 0; n < NT; n++) {
       const int32_t r = w.ti.tile * MT + 32 * wr + 16 * n + col;
@@ -137,13 +138,14 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_shared_kernel(AttendAr
     Rows<NT, DV / 16> rows;
     rows.clear();
 
-    const int32_t* const pages = c.table + (int64_t)w.b * c.ld_table;
     // the vector of this lane's position of tile k
     const auto find = [&](int32_t k) -> int64_t {
+      const AttendArgs a = arguments();
+      const CacheArgs& c = a.cache;
       const int32_t pos = k * KEYS + lane;
       if (lane >= KEYS || pos >= end) return -1;
-      const uint32_t p = a.page_shift >= 0 ? (uint32_t)pos >> a.page_shift : (uint32_t)pos / (uint32_t)c.page_size;
-      const int32_t page = pages[p];
+      const uint32_t p = a.page_of((uint32_t)pos);
+      const int32_t page = c.table[(int64_t)w.b * c.ld_table + p];
       if (page < 0 || page >= c.num_pages) return -1;
       return ((int64_t)page * c.page_size + ((uint32_t)pos - p * (uint32_t)c.page_size)) * c.heads + w.g;
     };
@@ -157,8 +159,9 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_shared_kernel(AttendAr
     const auto tile_k = [&](int32_t k) { return (uint16_t*)(lds + (k & 1) * Sh::kTileBytes); };
     const auto tile_v = [&](int32_t k) { return (uint16_t*)(lds + (k & 1) * Sh::kTileBytes) + KEYS * Sh::kStrideK; };
     const auto load = [&](int32_t k) {
-      kp.load(pk, vectors[k & 3]);
-      vp.load(pv, vectors[k & 3]);
+      const AttendArgs a = arguments();
+      kp.load(a.cache.plane[0], vectors[k & 3]);
+      vp.load(a.cache.plane[1], vectors[k & 3]);
     };
     const auto store = [&](int32_t k) {
       // hidden drafts' values must not meet zero weights unless they are numbers
@@ -195,7 +198,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_shared_kernel(AttendAr
       const uint64_t there = valid[k & 3] >> (16 * KT * wk) & kFull;
       if (there != kFull || (int64_t)base + 16 * KT > s.start) {
         const uint64_t b = (uint64_t)bad[k & 3][1] << 32 | bad[k & 3][0];
-        hide<NT, KT>(a, s, draft, base, there, b >> (16 * KT * wk), kg, sv);
+        hide<NT, KT>(arguments(), s, draft, base, there, b >> (16 * KT * wk), kg, sv);
       }
       bf16x8_t p[NT][KT / 2];
       rows.template weights<KT>(sv, sc, p);
@@ -230,11 +233,11 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_shared_kernel(AttendAr
         rows.join((float*)lds + 32 * (wr - first) * (DV + 4), DV + 4, top, x == 0, lane);
       }
       __syncthreads();
-      write_item<FMT, DV, MT, Sh::kWK, KEYS>(a, w, k0, k1, 32 * first, 32 * kGroups, (const float*)lds, ms, ls, part, part_ml);
+      write_item<FMT, DV, MT, Sh::kWK, KEYS>(arguments(), w, workers, 32 * first, 32 * kGroups, (const float*)lds, ms, ls, part, part_ml);
     }
-    w.leave_open(open, k0, k1);
+    w.leave_open(open, workers);
     __syncthreads();
-    if (!w.next(a, k1 - k0)) break;
+    if (!w.next(arguments())) break;
   }
 }
 

@@ -31,9 +31,9 @@ struct Shape {
 // PAGED: pages of whole tiles, and dimensions that are DK and DV.  A tile's page is then looked up once, and a lane's part
 // of the addresses does not change from tile to tile.
 template <int FMT, int DK, int DV, int NT, int WAVES, bool PAGED>
-__global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArgs a, float* __restrict__ part,
+__global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArgs given, float* __restrict__ part,
                                                                  float2* __restrict__ part_ml, Open* __restrict__ open,
-                                                                 int workers) {
+                                                                 int64_t* __restrict__ totals, int workers) {
   using Sh = Shape<FMT, DK, DV, NT>;
   using Found = std::conditional_t<PAGED, int32_t, int64_t>;
   constexpr int MT = Sh::kRows;
@@ -41,72 +41,53 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArg
   static_assert(MT * (DV + 4) * 4 <= kBytes, "the sums take the place of V");
   __shared__ __attribute__((aligned(16))) uint8_t lds[kBytes];
   __shared__ float ms[kWaves][MT], ls[kWaves][MT];
-  const CacheArgs& c = a.cache;
-  const CachePlane &pk = c.plane[0], &pv = c.plane[1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, kg = lane >> 4;
   Work<MT, kUnit> w;
-  if (!w.begin(a, workers, open, lane)) return;
-  const float sc = score_scale<FMT>(a);
-  const int k_dim = PAGED ? DK : pk.dim, v_dim = PAGED ? DV : pv.dim;
+  if (!w.begin(given, workers, open, totals, lane)) return;
+  const CacheArgs& c = given.cache;
+  const float sc = score_scale<FMT>(given);
+  const int heads = c.heads, k_dim = PAGED ? DK : c.plane[0].dim, v_dim = PAGED ? DV : c.plane[1].dim;
   const int64_t k_bytes = k_dim / kPerByte<FMT>, v_bytes = v_dim / kPerByte<FMT>;
   const int k_blocks = k_dim / kBlock<FMT>, v_blocks = v_dim / kBlock<FMT>;
-  // PAGED: this lane's part of the addresses of codes and scales
-  const uint32_t k_at = (uint32_t)(col * c.heads) * (DK / kPerByte<FMT>) + kg * (Sh::kCodes * 4);
-  const uint32_t ks_at = (uint32_t)(col * c.heads) * (DK / kBlock<FMT>) + kg * Sh::kQuarter / kBlock<FMT>;
-  const uint32_t v_at = (uint32_t)(lane / Sh::kPerKey * c.heads) * (DV / kPerByte<FMT>) + 16 * (lane % Sh::kPerKey);
-  const uint32_t vs_at = (uint32_t)(lane / Sh::kPerKey * c.heads) * (DV / kBlock<FMT>) + lane % Sh::kPerKey * Sh::kElems / kBlock<FMT>;
+  // this lane's part of a key's and of a value's codes and scales; PAGED: among the tile's
+  const uint32_t in_tile = PAGED ? col * heads : 0, v_in_tile = PAGED ? lane / Sh::kPerKey * heads : 0;
+  const uint32_t k_at = in_tile * (DK / kPerByte<FMT>) + kg * (Sh::kCodes * 4);
+  const uint32_t ks_at = in_tile * (DK / kBlock<FMT>) + kg * Sh::kQuarter / kBlock<FMT>;
+  const uint32_t v_at = v_in_tile * (DV / kPerByte<FMT>) + 16 * (lane % Sh::kPerKey);
+  const uint32_t vs_at = v_in_tile * (DV / kBlock<FMT>) + lane % Sh::kPerKey * Sh::kElems / kBlock<FMT>;
   uint16_t* const vt = (uint16_t*)lds + wave * kTile * Sh::kStride;
 
   for (;;) {
+    w.settle();
     const Seq& s = w.s;
-    const int32_t k0 = (int32_t)(w.u - w.item), k1 = (int32_t)min((int64_t)w.ti.units, w.u1 - w.item), end = w.ti.end;
-    // the rows of this lane's columns
-    bf16x8_t q[NT][Sh::kSteps];
-    int32_t draft[NT];  // -1: no such row
-#pragma unroll
-    for (int n = 0; n < NT; n++) {
-      const int32_t r = w.ti.tile * MT + 16 * n + col;
-      const int32_t d = (uint32_t)r / (uint32_t)a.group;
-      draft[n] = d < s.rows ? d : -1;
-      const uint16_t* src = (const uint16_t*)pk.rows + (int64_t)(s.first + d) * pk.ldt + (w.g * a.group + (r - d * a.group)) * pk.ldh;
-#pragma unroll
-      for (int i = 0; i < Sh::kSteps; i++) {
-        const int e = kg * Sh::kQuarter + 8 * i;
-        q[n][i] = __builtin_bit_cast(bf16x8_t, u32x4_t{0, 0, 0, 0});
-        if (draft[n] >= 0 && e < k_dim) q[n][i] = query8(a, src + e);
-      }
-    }
-    Rows<NT, Sh::kVT> rows;
-    rows.clear();
-
-    // Where a tile's codes are.  PAGED: its page, in every lane; else the cache's vector of each of its positions, -1: none,
-    // in the lanes 0 to 31.
+    const int32_t k0 = w.k0, k1 = w.k1(), end = w.ti.end;
     const int32_t* const pages = c.table + (int64_t)w.b * c.ld_table;
+
+    // Where a tile's codes are.  PAGED: its page, in every lane; else in the lanes 0 to 31 the cache's vector of each of its
+    // positions, -1: none.  No load waits for another, or hangs on a branch, which would make the waits for it wait for
+    // those behind it as well: places past the end, without a page or past a vector are replaced by some that are there, and
+    // what comes from them is dropped.
     const auto find = [&](int32_t k) {
-      const int32_t pos = k * kUnit + wave * kTile + (PAGED ? 0 : lane & 31);
-      Found f = -1;
-      if (pos < end) {
-        const uint32_t p = a.page_shift >= 0 ? (uint32_t)pos >> a.page_shift : (uint32_t)pos / (uint32_t)c.page_size;
-        const int32_t page = pages[p];
-        if (PAGED)
-          f = page;
-        else if (page >= 0 && page < c.num_pages)
-          f = ((int64_t)page * c.page_size + ((uint32_t)pos - p * (uint32_t)c.page_size)) * c.heads + w.g;
-      }
+      const int32_t pos = k * kUnit + wave * kTile + (PAGED ? 0 : lane & 31), there = min(pos, end - 1);
+      const uint32_t p = given.page_of((uint32_t)there);
+      const int32_t page = pages[p];
+      Found f = page;
+      if (!PAGED)
+        f = pos < end && page >= 0 && page < c.num_pages
+                ? ((int64_t)page * c.page_size + ((uint32_t)there - p * (uint32_t)c.page_size)) * heads + w.g
+                : -1;
       return f;
     };
-    // PAGED: the tile's first vector, -1: none.  Its positions past the end lie in the page too.
+    // PAGED: the tile's first vector.  Its positions past the end lie in the page too.
     const auto first_vector = [&](int32_t k, Found f) -> int64_t {
-      const int32_t page = __builtin_amdgcn_readfirstlane((int)f);
-      if (page < 0 || page >= c.num_pages) return -1;
+      const int32_t page = uniform((int)f), there = page < 0 || page >= c.num_pages ? 0 : page;
       const uint32_t pos = (uint32_t)k * kUnit + (uint32_t)wave * kTile;
-      const uint32_t in_page = a.page_shift >= 0 ? pos & (uint32_t)(c.page_size - 1) : pos % (uint32_t)c.page_size;
-      return ((int64_t)page * c.page_size + in_page) * c.heads + w.g;
+      return ((int64_t)there * c.page_size + (pos - given.page_of(pos) * (uint32_t)c.page_size)) * heads + w.g;
     };
     uint32_t kc[2][Sh::kCodes], ks[2][Sh::kScales];
     // a lane's quarter of a key
     const auto load_key = [&](int t, const uint8_t* src, const uint8_t* scales) {
-      if (PAGED || pk.dim == DK) {
+      if constexpr (PAGED) {
         if constexpr (Sh::kCodes % 4 == 0) {
 #pragma unroll
           for (int i = 0; i < Sh::kCodes; i += 4) {
@@ -124,23 +105,25 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArg
             kc[t][i + 1] = x[1];
           }
         }
+#pragma unroll
+        for (int i = 0; i < Sh::kScales; i++) ks[t][i] = scales[i];
       } else {
         constexpr int per = FMT == MXFP4_FMT_MXFP8 ? 2 : 1;  // registers of eight codes
 #pragma unroll
         for (int i = 0; i < Sh::kSteps; i++) {
-          const int e = kg * Sh::kQuarter + 8 * i;
-#pragma unroll
-          for (int j = 0; j < per; j++) {
-            kc[t][per * i + j] = 0;
-            if (e < pk.dim) kc[t][per * i + j] = *reinterpret_cast<const uint32_t*>(src + 4 * (per * i + j));
+          const bool in = kg * Sh::kQuarter + 8 * i < k_dim;
+          const uint8_t* from = src + (in ? (int)k_at + 4 * per * i : 0);
+          if constexpr (per == 2) {
+            const u32x2_t x = *reinterpret_cast<const u32x2_a8*>(from);
+            kc[t][2 * i] = in ? x[0] : 0;
+            kc[t][2 * i + 1] = in ? x[1] : 0;
+          } else {
+            const uint32_t x = *reinterpret_cast<const uint32_t*>(from);
+            kc[t][i] = in ? x : 0;
           }
         }
-      }
-      const int b0 = kg * Sh::kQuarter / kBlock<FMT>;
 #pragma unroll
-      for (int i = 0; i < Sh::kScales; i++) {
-        ks[t][i] = 0;
-        if (PAGED || b0 + i < k_blocks) ks[t][i] = scales[i];
+        for (int i = 0; i < Sh::kScales; i++) ks[t][i] = scales[min((int)ks_at + i, k_blocks - 1)];
       }
     };
     const auto load_k = [&](int32_t k, Found f) {
@@ -148,72 +131,94 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArg
 #pragma unroll
       for (int t = 0; t < 2; t++) {
         if (PAGED) {  // the tile's part of the addresses is the same for all lanes, the lane's for all tiles
-          const int64_t at = first + 16 * t * c.heads;
-          if (first >= 0) load_key(t, pk.q + at * k_bytes + k_at, pk.s + at * k_blocks + ks_at);
+          const int64_t at = first + 16 * t * heads;
+          load_key(t, c.plane[0].q + at * k_bytes + k_at, c.plane[0].s + at * k_blocks + ks_at);
         } else {
-          const int64_t at = shfl64(f, 16 * t + col);
-          if (at >= 0) load_key(t, pk.q + at * k_bytes + kg * (Sh::kCodes * 4), pk.s + at * k_blocks + kg * Sh::kQuarter / kBlock<FMT>);
+          const int64_t at = shfl64(f, 16 * t + col), there = at < 0 ? 0 : at;
+          load_key(t, c.plane[0].q + there * k_bytes, c.plane[0].s + there * k_blocks);
         }
       }
     };
     u32x4_t vc[Sh::kPieces];
     uint32_t vs[Sh::kPieces][Sh::kPieceScales];
-    const auto load_piece = [&](int i, const uint8_t* src, const uint8_t* scales) {
-      const int e = lane % Sh::kPerKey * Sh::kElems;
-      if (PAGED || e + Sh::kElems <= pv.dim) {
-        vc[i] = *reinterpret_cast<const u32x4_a8*>(src);
-      } else if (e < pv.dim) {
-        const u32x2_t x = *reinterpret_cast<const u32x2_a8*>(src);
-        vc[i] = u32x4_t{x[0], x[1], 0, 0};
-      }
-      const int b0 = e / kBlock<FMT>;
-#pragma unroll
-      for (int j = 0; j < Sh::kPieceScales; j++)
-        if (PAGED || b0 + j < v_blocks) vs[i][j] = scales[j];
-    };
     const auto load_v = [&](int32_t k, Found f) {
       const int64_t first = PAGED ? first_vector(k, f) : 0;
 #pragma unroll
       for (int i = 0; i < Sh::kPieces; i++) {
         constexpr int keys = 64 / Sh::kPerKey;  // of 64 pieces
         if (PAGED) {
-          const int64_t at = first + keys * i * c.heads;
-          if (first >= 0) load_piece(i, pv.q + at * v_bytes + v_at, pv.s + at * v_blocks + vs_at);
-        } else {
-          vc[i] = u32x4_t{0, 0, 0, 0};
+          const int64_t at = first + keys * i * heads;
+          vc[i] = *reinterpret_cast<const u32x4_a8*>(c.plane[1].q + at * v_bytes + v_at);
+          const uint8_t* scales = c.plane[1].s + at * v_blocks + vs_at;
 #pragma unroll
-          for (int j = 0; j < Sh::kPieceScales; j++) vs[i][j] = 0;
-          const int64_t at = shfl64(f, keys * i + lane / Sh::kPerKey);
-          const int piece = lane % Sh::kPerKey;
-          if (at >= 0) load_piece(i, pv.q + at * v_bytes + 16 * piece, pv.s + at * v_blocks + piece * Sh::kElems / kBlock<FMT>);
+          for (int j = 0; j < Sh::kPieceScales; j++) vs[i][j] = scales[j];
+        } else {
+          const int64_t at = shfl64(f, keys * i + lane / Sh::kPerKey), there = at < 0 ? 0 : at;
+          // in halves: the last piece of a vector may be one
+          const int e = lane % Sh::kPerKey * Sh::kElems;
+          const bool in = e < v_dim, all = e + Sh::kElems <= v_dim;
+          const uint8_t* src = c.plane[1].q + there * v_bytes;
+          const u32x2_t x = *reinterpret_cast<const u32x2_a8*>(src + (in ? v_at : 0)), y = *reinterpret_cast<const u32x2_a8*>(src + (all ? v_at + 8 : 0));
+          vc[i] = u32x4_t{in ? x[0] : 0, in ? x[1] : 0, all ? y[0] : 0, all ? y[1] : 0};
+          const uint8_t* scales = c.plane[1].s + there * v_blocks;
+#pragma unroll
+          for (int j = 0; j < Sh::kPieceScales; j++) vs[i][j] = scales[min((int)vs_at + j, v_blocks - 1)];
         }
       }
     };
 
-    Found found = find(k0);
-    load_k(k0, found);
-    load_v(k0, found);
-    for (int32_t k = k0; k < k1; k++) {
+    Found found = -1, next = -1;
+    if (end > 0) {
+      found = find(k0);
+      next = find(k0 + 1);
+    }
+    // the rows of this lane's columns
+    bf16x8_t q[NT][Sh::kSteps];
+    int32_t draft[NT];  // -1: no such row
+    {
+      const AttendArgs a = arguments();
+      const CachePlane& query = a.cache.plane[0];
+#pragma unroll
+      for (int n = 0; n < NT; n++) {
+        const int32_t r = w.ti.tile * MT + 16 * n + col;
+        const int32_t d = (uint32_t)r / (uint32_t)a.group;
+        draft[n] = d < s.rows ? d : -1;
+        const uint16_t* src = (const uint16_t*)query.rows + (int64_t)(s.first + d) * query.ldt + (w.g * a.group + (r - d * a.group)) * query.ldh;
+#pragma unroll
+        for (int i = 0; i < Sh::kSteps; i++) {
+          const int e = kg * Sh::kQuarter + 8 * i;
+          q[n][i] = __builtin_bit_cast(bf16x8_t, u32x4_t{0, 0, 0, 0});
+          if (draft[n] >= 0 && e < k_dim) q[n][i] = query8(a, src + e);
+        }
+      }
+    }
+    Rows<NT, Sh::kVT> rows;
+    rows.clear();
+
+    const auto step = [&](int32_t k, auto more) {
+      constexpr bool kMore = decltype(more)::value;  // another tile follows
       const int32_t base = k * kUnit + wave * kTile;
       // which of the tile's positions have a vector, and whether all rows see them all
       uint32_t there;
       if (PAGED) {
-        const int32_t page = __builtin_amdgcn_readfirstlane((int)found);
-        const int32_t left = end - base;
+        const int32_t page = uniform((int)found), left = end - base;
         there = page < 0 || page >= c.num_pages || left <= 0 ? 0u : left >= kTile ? ~0u : (1u << left) - 1;
       } else {
         there = (uint32_t)__ballot(found >= 0);
       }
       const bool whole = there == ~0u && base + kTile <= s.start;
-      const Found next = k + 1 < k1 ? find(k + 1) : -1;
+      Found after = -1;
+      if (kMore) after = find(k + 2);
 
       f32x4_t sv[NT][2];
 #pragma unroll
-      for (int t = 0; t < 2; t++) {
+      for (int t = 0; t < 2; t++)
 #pragma unroll
         for (int n = 0; n < NT; n++) sv[n][t] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < Sh::kSteps; i++) {
+      for (int i = 0; i < Sh::kSteps; i++)
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
           constexpr int per = FMT == MXFP4_FMT_MXFP8 ? 2 : 1;
           uint32_t scale = ks[t][0];
           if constexpr (Sh::kScales > 1) {
@@ -226,8 +231,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArg
 #pragma unroll
           for (int n = 0; n < NT; n++) sv[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, q[n][i], sv[n][t], 0, 0, 0);
         }
-      }
-      if (k + 1 < k1) load_k(k + 1, next);
+      if (kMore) load_k(k + 1, next);
 
       if (!whole) {
         // Positions whose values are not finite must not meet the zero weights of rows that do not see them: they count as
@@ -254,7 +258,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArg
               for (int j = 0; j < Sh::kPieceScales; j++) vs[i][j] = 0;
             }
         }
-        hide<NT, 2>(a, s, draft, base, there, bad, kg, sv);
+        hide<NT, 2>(arguments(), s, draft, base, there, bad, kg, sv);
       }
 
       bf16x8_t p[NT][1];
@@ -272,11 +276,18 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArg
           *reinterpret_cast<bf16x8_t*>(dst + 8 * j) = x;
         }
       }
-      if (k + 1 < k1) load_v(k + 1, next);
+      if (kMore) load_v(k + 1, next);
       __builtin_amdgcn_wave_barrier();
       rows.template add_values<1>(vt, Sh::kStride, p, 0, lane);
       __builtin_amdgcn_wave_barrier();
       found = next;
+      next = after;
+    };
+    if (end > 0) {
+      load_k(k0, found);
+      load_v(k0, found);
+      for (int32_t k = k0; k + 1 < k1; k++) step(k, std::true_type{});
+      step(k1 - 1, std::false_type{});
     }
 
     // the waves' sums, joined
@@ -299,10 +310,10 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArg
       rows.join((float*)lds, DV + 4, top, x == 0, lane);
     }
     __syncthreads();
-    write_item<FMT, DV, MT, kWaves, kUnit>(a, w, k0, k1, 0, MT, (const float*)lds, ms, ls, part, part_ml);
-    w.leave_open(open, k0, k1);
+    write_item<FMT, DV, MT, kWaves, kUnit>(arguments(), w, workers, 0, MT, (const float*)lds, ms, ls, part, part_ml);
+    w.leave_open(open, workers);
     __syncthreads();
-    if (!w.next(a, k1 - k0)) break;
+    if (!w.next(arguments())) break;
   }
 }
 

@@ -105,6 +105,7 @@ AttendPlan attend_plan(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows,
   p.part = take(4 * part_rows * (uint64_t)p.dv);
   p.ml = take(8 * part_rows);
   p.open = take(12 * all);
+  p.totals = take(8);
   p.total = at;
   return p;
 }
@@ -166,7 +167,7 @@ MX_API int mxfp4_cache_attend(const mxfp4_cache_dims* d, const void* k_q, const 
   c.start = start;
   c.table = page_table;
   c.n_seqs = n_seqs;
-  c.max_pages = max_pages;
+  c.max_pages = d->num_pages > 0 ? max_pages : 0;  // a table of no page at all has no positions
   c.page_size = d->page_size;
   c.heads = d->heads;
   a.mask = tree_mask;
@@ -174,7 +175,7 @@ MX_API int mxfp4_cache_attend(const mxfp4_cache_dims* d, const void* k_q, const 
   a.mask_cols = mask_cols;
   a.group = q_heads / d->heads;
   a.out_fp32 = out_is_fp32;
-  a.page_shift = d->page_size & (d->page_size - 1) ? -1 : __builtin_ctz((unsigned)d->page_size);
+  a.set_page_size(d->page_size);
   a.rows_of_tile = 16 * plan.nt / a.group;
   a.part_of_tile = 16 * plan.nt % a.group;
   a.scale = scale;

@@ -12,7 +12,24 @@ struct AttendArgs {
   const uint8_t* mask;
   int64_t ld_mask;
   int32_t mask_cols, group, out_fp32;  // group: query heads of a key head
-  int32_t page_shift;                  // of a page size that is a power of two, else -1
+  // the page that a position below 2^31 lies in: position >> page_shift for page sizes that are powers of two, else the upper
+  // half of its product with page_magic, shifted
+  uint32_t page_magic;
+  int32_t page_shift;
+#ifdef __HIPCC__
+  __host__ __device__
+#endif
+  uint32_t page_of(uint32_t position) const {
+    return (page_magic ? (uint32_t)(((uint64_t)position * page_magic) >> 32) : position) >> page_shift;
+  }
+  void set_page_size(int32_t size) {
+    int log = 0;
+    while ((int64_t(1) << log) < size) log++;
+    const bool power = (int64_t(1) << log) == size;
+    // 2^(31 + log) / size, rounded up: off by less than 2^log / size of itself, which no position below 2^31 sees
+    page_magic = power ? 0u : (uint32_t)(((uint64_t(1) << (31 + log)) + (uint64_t)size - 1) / (uint64_t)size);
+    page_shift = power ? log : log - 1;
+  }
   int32_t rows_of_tile, part_of_tile;  // tile rows / group, and the remainder
   float scale;
 };
@@ -20,7 +37,7 @@ struct AttendArgs {
 // head; the workspace's parts.
 struct AttendPlan {
   int32_t nt, unit, dk, dv, workers;
-  uint64_t part, ml, open, total;
+  uint64_t part, ml, open, totals, total;
 };
 // Workgroups of a compute unit: what their registers and LDS leave room for.
 constexpr int attend_waves(int dk, int nt) { return nt == 1 ? (dk <= 128 ? 3 : 2) : dk <= 192 ? 2 : 1; }

@@ -139,11 +139,23 @@ static void test_attend() {
           // the parts follow each other inside the workspace
           const uint64_t workers = (uint64_t)g_plan.workers * heads, part_rows = 2 * workers * 16 * g_plan.nt;
           CHECK(g_plan.part + 4 * part_rows * g_plan.dv <= g_plan.ml && g_plan.ml + 8 * part_rows <= g_plan.open &&
-                g_plan.open + 12 * workers <= g_plan.total);
+                g_plan.open + 12 * workers <= g_plan.totals && g_plan.totals + 8 <= g_plan.total);
         }
   d = kOk;
   CHECK(mxfp4_cache_attend_workspace_bytes(&d, 3, 5, 2) == 0 && mxfp4_cache_attend_workspace_bytes(nullptr, 4, 5, 2) == 0);
   CHECK(mxfp4_cache_attend_workspace_bytes(&d, 4, 0, 0) > 0);
+}
+
+// The division by the page size is exact for every position.
+static void test_page_of() {
+  AttendArgs a = {};
+  for (int64_t size : {1ll, 2ll, 3ll, 5ll, 7ll, 16ll, 24ll, 96ll, 100ll, 128ll, 129ll, 1000ll, 65535ll, 65537ll, 1ll << 30, (1ll << 30) + 1, (1ll << 31) - 1}) {
+    a.set_page_size((int32_t)size);
+    for (int64_t k = 0; k <= (int64_t(1) << 31) / size; k += 1 + k / 50)
+      for (int64_t p : {k * size - 1, k * size, k * size + 1, k * size + size / 2})
+        if (p >= 0 && p < int64_t(1) << 31) CHECK(a.page_of((uint32_t)p) == (uint32_t)(p / size));
+    for (int64_t p = (int64_t(1) << 31) - 1; p > (int64_t(1) << 31) - 3000; p--) CHECK(a.page_of((uint32_t)p) == (uint32_t)(p / size));
+  }
 }
 
 static void test_moves() {
@@ -265,6 +277,7 @@ static void test_rotary() {
 
 int main() {
   test_attend();
+  test_page_of();
   test_moves();
   test_pool();
   test_rotary();
