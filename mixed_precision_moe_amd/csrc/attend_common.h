@@ -44,9 +44,13 @@ constexpr int kBlock = FMT == MXFP4_FMT_NVFP4 ? 16 : 32;
 template <int FMT>
 constexpr int kPerByte = FMT == MXFP4_FMT_MXFP8 ? 1 : 2;
 
-// What a worker leaves for the join, next to its sums: the item that it begins and others go on with.
+// What a worker leaves for the join, next to its sums: an item that it begins and others go on with.  The entries are the
+// items', where there are fewer of those than workers, else the workers', of whose items only the last can go on.
 struct Open {
-  int32_t tile, seq, rest;  // rest: units of the item behind the worker's range, 0: none
+  int32_t tile, seq, worker, rest;  // rest: units of the item behind the worker's range, 0: none
+};
+struct Totals {
+  int64_t units, items;  // of a head; the heads' are alike
 };
 
 // The kernels' first argument, read again where it is needed: what the kernels use of it is more than the scalar registers
@@ -119,9 +123,9 @@ MX_DEV Seq sequence(const AttendArgs& a, int b) {
   return Seq{at, some ? end - at : 0, some ? there - at : 0, c.start ? c.start[b] : 0};
 }
 
-// Of a sequence, tile by tile of MT rows: the positions that some row of the tile sees are below `end`, UNIT of them are a
-// unit; a tile has one at least, since its rows are written where nothing is seen too.
-template <int MT, int UNIT>
+// Of a sequence, tile by tile of MT rows: the positions that some row of the tile sees are below `end`, 2^unit_log of them are
+// a unit; a tile has one at least, since its rows are written where nothing is seen too.
+template <int MT>
 struct Tiles {
   int32_t tile, tiles, end, units;
   int32_t row, part;  // without a mask: the draft of the row behind the tile, and that row's place in its group
@@ -130,7 +134,7 @@ struct Tiles {
     const int64_t n = a.mask ? s.drafts : min(s.rows, row + (part > 0));
     const int64_t e = min(s.start + n, (int64_t)a.cache.max_pages * a.cache.page_size);
     end = e < 0 ? 0 : (int32_t)e;
-    units = end <= UNIT ? 1 : (end + UNIT - 1) / UNIT;
+    units = end == 0 ? 1 : (end - 1 >> a.unit_log) + 1;
   }
   MX_DEV void begin(const AttendArgs& a, const Seq& s) {
     tile = 0;
@@ -151,9 +155,9 @@ struct Tiles {
   }
 };
 
-template <int MT, int UNIT>
+template <int MT>
 MX_DEV int64_t seq_units(const AttendArgs& a, const Seq& s) {
-  Tiles<MT, UNIT> t;
+  Tiles<MT> t;
   t.begin(a, s);
   if (a.mask) return (int64_t)t.tiles * t.units;
   int64_t n = 0;
@@ -178,17 +182,22 @@ MX_DEV int64_t shfl64_up(int64_t v, int by) {
   return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
 }
 
-// Units of the 64 sequences from b0 on, summed up to and including each lane's.
-template <int MT, int UNIT>
-MX_DEV int64_t scan_units(const AttendArgs& a, int b0, int lane) {
-  int64_t n = 0;
-  if (b0 + lane < a.cache.n_seqs) n = seq_units<MT, UNIT>(a, sequence(a, b0 + lane));
+// Units, and tiles, of the 64 sequences from b0 on, summed up to and including each lane's.
+MX_DEV int64_t scan_lanes(int64_t n, int lane) {
 #pragma unroll
   for (int h = 1; h < 64; h <<= 1) {
     const int64_t o = shfl64_up(n, h);
     if (lane >= h) n += o;
   }
   return n;
+}
+template <int MT>
+MX_DEV int64_t scan_units(const AttendArgs& a, int b0, int lane) {
+  return scan_lanes(b0 + lane < a.cache.n_seqs ? seq_units<MT>(a, sequence(a, b0 + lane)) : 0, lane);
+}
+template <int MT>
+MX_DEV int64_t scan_tiles(const AttendArgs& a, int b0, int lane) {
+  return scan_lanes(b0 + lane < a.cache.n_seqs ? (sequence(a, b0 + lane).rows * a.group + MT - 1) / MT : 0, lane);
 }
 
 // Eight elements of a row of the result from its sums x, y and the sum of its weights.
@@ -232,50 +241,61 @@ MX_DEV void worker_range(int64_t all, int workers, int worker, int64_t& first, i
 }
 
 // Where a worker is in its range of units; every wave has the same.
-template <int MT, int UNIT>
+template <int MT>
 struct Work {
-  int32_t g, worker, b, k0;  // k0: the first of the item's units that are the worker's
-  int64_t left;              // units from there on
+  int32_t group, worker, b, k0;  // group: of heads; k0: the first of the item's units that are the worker's
+  int64_t left;                   // units from there on
+  int32_t index;                  // the item's, among all
   Seq s;
-  Tiles<MT, UNIT> ti;
+  Tiles<MT> ti;
 
   // False: nothing to do.
-  MX_DEV bool begin(const AttendArgs& a, int workers, Open* open, int64_t* totals, int lane) {
+  MX_DEV bool begin(const AttendArgs& a, int workers, Open* open, Totals* totals, int lane) {
     const CacheArgs& c = a.cache;
+    const int groups = c.heads >> a.heads_log;
     // Workgroups go to the eight XCDs in turn: a worker's heads, which read pieces of the same tokens, share one.
     if (workers % 8 == 0) {
       const int i = blockIdx.x / 8;
-      g = i % c.heads;
-      worker = i / c.heads * 8 + blockIdx.x % 8;
+      group = i % groups;
+      worker = i / groups * 8 + blockIdx.x % 8;
     } else {
-      g = blockIdx.x % c.heads;
-      worker = blockIdx.x / c.heads;
+      group = blockIdx.x % groups;
+      worker = blockIdx.x / groups;
     }
-    int64_t all = 0, u, u1;
-    for (int b0 = 0; b0 < c.n_seqs; b0 += 64) all += lane64(scan_units<MT, UNIT>(a, b0, lane), 63);
+    int64_t all = 0, items = 0, u, u1;
+    for (int b0 = 0; b0 < c.n_seqs; b0 += 64) {
+      all += lane64(scan_units<MT>(a, b0, lane), 63);
+      items += lane64(scan_tiles<MT>(a, b0, lane), 63);
+    }
     if (threadIdx.x == 0) {
-      open[(int64_t)g * workers + worker] = Open{0, 0, 0};
-      if (worker == 0 && g == 0) *totals = all;  // the heads' units are alike
+      if (!a.open_items) open[(int64_t)group * workers + worker] = Open{0, 0, 0, 0};
+      if (worker == 0 && group == 0) *totals = Totals{all, items};
     }
     worker_range(all, workers, worker, u, u1);
     if (u == u1) return false;
     b = 0;
+    index = 0;
     int64_t item = 0;
     for (int b0 = 0; b0 < c.n_seqs; b0 += 64) {
-      const int64_t sums = item + scan_units<MT, UNIT>(a, b0, lane);
+      const int64_t sums = item + scan_units<MT>(a, b0, lane), tiles = index + scan_tiles<MT>(a, b0, lane);
       const uint64_t past = __ballot(sums > u);
       if (past) {
         const int l = __ffsll((unsigned long long)past) - 1;
         b = b0 + l;
-        if (l > 0) item = lane64(sums, l - 1);
+        if (l > 0) {
+          item = lane64(sums, l - 1);
+          index = (int32_t)lane64(tiles, l - 1);
+        }
         break;
       }
       item = lane64(sums, 63);
+      index = (int32_t)lane64(tiles, 63);
     }
     s = sequence(a, b);
     ti.begin(a, s);
     while (item + ti.units <= u) {
       item += ti.units;
+      index++;
       ti.next(a, s);
     }
     k0 = (int32_t)(u - item);
@@ -286,9 +306,10 @@ struct Work {
   MX_DEV int32_t k1() const { return (int32_t)min((int64_t)ti.units, k0 + left); }
   // The same, in scalar registers again after a loop's end that the compiler takes to differ between lanes.
   MX_DEV void settle() {
-    g = uniform(g);
+    group = uniform(group);
     worker = uniform(worker);
     b = uniform(b);
+    index = uniform(index);
     k0 = uniform(k0);
     left = lane64(left, 0);
     s = Seq{uniform(s.first), uniform(s.drafts), uniform(s.rows), uniform(s.start)};
@@ -304,6 +325,7 @@ struct Work {
     left -= k1() - k0;
     if (left <= 0) return false;
     k0 = 0;
+    index++;
     ti.next(a, s);
     if (ti.tile >= ti.tiles) {
       do s = sequence(a, ++b);
@@ -312,9 +334,14 @@ struct Work {
     }
     return true;
   }
-  // What the join needs to know, if the item begins here and goes on.
-  MX_DEV void leave_open(Open* open, int workers) const {
-    if (threadIdx.x == 0 && k0 == 0 && k1() < ti.units) open[(int64_t)g * workers + worker] = Open{ti.tile, b, ti.units - k1()};
+  // What the join needs to know of an item that begins here.
+  MX_DEV void leave_open(const AttendArgs& a, Open* open, int workers) const {
+    if (threadIdx.x != 0 || k0 != 0) return;
+    const Open o = {ti.tile, b, worker, ti.units - k1()};
+    if (a.open_items)
+      open[(int64_t)group * a.open_items + index] = o;
+    else if (o.rest > 0)
+      open[(int64_t)group * workers + worker] = o;
   }
 };
 
@@ -422,24 +449,21 @@ struct Rows {
     }
   }
 
-  // Adds the rows' sums, brought to the maxima `top`, to those in LDS (first: puts them there).
-  MX_DEV void join(float* sums, int stride, const float (&top)[NT], bool first, int lane) const {
+  // Adds the sums of the rows of column tile n, brought to the maximum `top`, to those in LDS (first: puts them there).
+  MX_DEV void join(int n, float* sums, int stride, float top, bool first, int lane) const {
+    const float f = top > -INFINITY ? __builtin_amdgcn_exp2f(m[n] - top) : 0.0f;
+    float* dst = sums + (lane & 15) * stride + 4 * (lane >> 4);
 #pragma unroll
-    for (int n = 0; n < NT; n++) {
-      const float f = top[n] > -INFINITY ? __builtin_amdgcn_exp2f(m[n] - top[n]) : 0.0f;
-      float* dst = sums + (16 * n + (lane & 15)) * stride + 4 * (lane >> 4);
+    for (int v = 0; v < VT; v++) {
+      f32x4_t x = o[n][v];
 #pragma unroll
-      for (int v = 0; v < VT; v++) {
-        f32x4_t x = o[n][v];
+      for (int i = 0; i < 4; i++) x[i] *= f;
+      if (!first) {
+        const f32x4_t y = *reinterpret_cast<const f32x4_t*>(dst + 16 * v);
 #pragma unroll
-        for (int i = 0; i < 4; i++) x[i] *= f;
-        if (!first) {
-          const f32x4_t y = *reinterpret_cast<const f32x4_t*>(dst + 16 * v);
-#pragma unroll
-          for (int i = 0; i < 4; i++) x[i] += y[i];
-        }
-        *reinterpret_cast<f32x4_t*>(dst + 16 * v) = x;
+        for (int i = 0; i < 4; i++) x[i] += y[i];
       }
+      *reinterpret_cast<f32x4_t*>(dst + 16 * v) = x;
     }
   }
 };
@@ -477,21 +501,19 @@ MX_DEV void hide(const AttendArgs& a, const Seq& s, const int32_t (&draft)[NT], 
   }
 }
 
-// The result of `n` of an item's rows from `r0` on, or its part for the join: their sums in LDS, and the maxima and sums of
-// weights of the PARTS waves that had them.
-template <int FMT, int DV, int MT, int PARTS, int UNIT>
-MX_DEV void write_item(const AttendArgs& a, const Work<MT, UNIT>& w, int workers, int r0, int n, const float* sums, const float (&ms)[PARTS][MT],
-                       const float (&ls)[PARTS][MT], float* part, float2* part_ml) {
+// The result of `n` of an item's rows from `r0` on for key head g, or their part for the join, by `threads` threads: their
+// sums in LDS, and the maxima and sums of weights of the `parts` waves that had them, MT of each a wave.
+template <int FMT, int DV, int MT>
+MX_DEV void write_item(const AttendArgs& a, const Work<MT>& w, int g, int workers, int r0, int n, const float* sums, const float* ms,
+                       const float* ls, int parts, int thread, int threads, float* part, float2* part_ml) {
   const int there = min(n, w.s.rows * a.group - w.ti.tile * MT - r0);
   const bool whole = w.k0 == 0 && w.k1() == w.ti.units;
-  const int64_t slot = 2 * ((int64_t)w.g * workers + w.worker) + (w.k0 == 0 ? 1 : 0);
-  for (int id = threadIdx.x; id < there * (DV / 8); id += kThreads) {
+  const int64_t slot = 2 * ((int64_t)g * workers + w.worker) + (w.k0 == 0 ? 1 : 0);
+  for (int id = thread; id < there * (DV / 8); id += threads) {
     const int r = r0 + id / (DV / 8), e = id % (DV / 8) * 8;
-    float top = ms[0][r], sum = 0.0f;
-#pragma unroll
-    for (int x = 1; x < PARTS; x++) top = fmaxf(top, ms[x][r]);
-#pragma unroll
-    for (int x = 0; x < PARTS; x++) sum += top > -INFINITY ? ls[x][r] * __builtin_amdgcn_exp2f(ms[x][r] - top) : 0.0f;
+    float top = ms[r], sum = 0.0f;
+    for (int x = 1; x < parts; x++) top = fmaxf(top, ms[x * MT + r]);
+    for (int x = 0; x < parts; x++) sum += top > -INFINITY ? ls[x * MT + r] * __builtin_amdgcn_exp2f(ms[x * MT + r] - top) : 0.0f;
     const f32x4_t* src = reinterpret_cast<const f32x4_t*>(sums + (r - r0) * (DV + 4) + e);
     const f32x4_t x = src[0], y = src[1];
     if (!whole) {
@@ -500,7 +522,7 @@ MX_DEV void write_item(const AttendArgs& a, const Work<MT, UNIT>& w, int workers
       dst[1] = y;
       if (e == 0) part_ml[slot * MT + r] = float2{top, sum};
     } else if (e < a.cache.plane[1].dim) {
-      write_row<FMT>(a, w.s, w.ti.tile * MT + r, w.g, e, x, y, sum);
+      write_row<FMT>(a, w.s, w.ti.tile * MT + r, g, e, x, y, sum);
     }
   }
 }

@@ -6,58 +6,88 @@
 
 namespace {
 
-// Joins the parts of the item that a worker begins and others go on with: a wave a row, blockIdx.y: rows of the tile.
+// Joins the parts of the items that a worker begins and others go on with.  blockIdx.x: entry of `open`, blockIdx.y: rows of
+// the tile, blockIdx.z: the head in the worker's group.  A row of a part is LANES lanes; the rest of the wave's have other
+// rows where the parts are few, else other parts of the same row.
 template <int FMT, int DV, int NT>
 __global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendArgs a, const float* __restrict__ part,
                                                                const float2* __restrict__ part_ml,
                                                                const Open* __restrict__ open,
-                                                               const int64_t* __restrict__ totals, int workers) {
-  constexpr int MT = 16 * NT, LANES = DV / 8, SIDES = 64 / LANES;  // lanes of a row of a part, parts side by side
+                                                               const Totals* __restrict__ totals, int workers) {
+  constexpr int MT = 16 * NT, LANES = DV / 8, SIDES = 64 / LANES, kFew = 8, kAhead = 4;
+  const int entries = a.open_items ? a.open_items : workers;
+  if (a.open_items && blockIdx.x % entries >= totals->items) return;
   const Open it = open[blockIdx.x];
   if (it.rest <= 0) return;
-  const int g = blockIdx.x / workers, worker = blockIdx.x % workers;
-  const int lane = threadIdx.x & 63, e = lane % LANES * 8, side = lane / LANES;
+  const int g = (blockIdx.x / entries << a.heads_log) + blockIdx.z;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = lane % LANES * 8, side = lane / LANES;
   const Seq s = sequence(a, it.seq);
   const int there = min(MT, s.rows * a.group - it.tile * MT);
   // the worker of the item's last unit
+  const int64_t all = totals->units, used = min((int64_t)workers, all);
   int64_t u0, u1;
-  worker_range(*totals, workers, worker, u0, u1);
-  const int64_t used = min((int64_t)workers, *totals);
-  const int last = (int)(((u1 + it.rest) * used - 1) / *totals), n = last - worker + 1;
-  // the first part is the second of its worker's two, the others are the first of theirs
-  const auto slot = [&](int i) { return 2 * ((int64_t)g * workers + worker + i) + (i == 0 ? 1 : 0); };
-  for (int r = blockIdx.y * (kThreads / 64) + (threadIdx.x >> 6); r < there; r += gridDim.y * (kThreads / 64)) {
-    float top = -INFINITY;
-    for (int i = lane; i < n; i += 64) top = fmaxf(top, part_ml[slot(i) * MT + r].x);
-#pragma unroll
-    for (int h = 1; h < 64; h <<= 1) top = fmaxf(top, __shfl_xor(top, h));
+  worker_range(all, workers, it.worker, u0, u1);
+  const int n = (int)(((u1 + it.rest) * used - 1) / all) - it.worker + 1;
+  const bool few = n <= kFew;
+  const int per_wave = few ? SIDES : 1, step = few ? 1 : SIDES;
+  for (int r0 = (blockIdx.y * (kThreads / 64) + wave) * per_wave; r0 < there; r0 += gridDim.y * (kThreads / 64) * per_wave) {
+    const int r = few ? min(r0 + side, there - 1) : r0;
+    // the first part is the second of its worker's two, the others are the first of theirs
+    const int64_t first = 2 * ((int64_t)g * workers + it.worker);
     f32x4_t x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
-    float sum = 0.0f;
-    if (top > -INFINITY) {
-#pragma unroll 4
-      for (int i = side; i < n; i += SIDES) {
-        const float2 ml = part_ml[slot(i) * MT + r];
-        const f32x4_t* src = reinterpret_cast<const f32x4_t*>(part + (slot(i) * MT + r) * DV + e);
-        const float f = __builtin_amdgcn_exp2f(ml.x - top);
-        const f32x4_t p = src[0], q = src[1];
-        sum += f * ml.y;
+    float sum = 0.0f, top = -INFINITY;
+    for (int i = few ? 0 : side; i < n; i += kAhead * step) {
+      float2 ml[kAhead];
+      f32x4_t p[kAhead], q[kAhead];
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-          x[j] += f * p[j];
-          y[j] += f * q[j];
+      for (int j = 0; j < kAhead; j++) {
+        const int k = min(i + j * step, n - 1);
+        const int64_t at = (k == 0 ? first + 1 : first + 2 * k) * MT + r;
+        ml[j] = part_ml[at];
+        const f32x4_t* src = reinterpret_cast<const f32x4_t*>(part + at * DV + e);
+        p[j] = src[0];
+        q[j] = src[1];
+        if (i + j * step >= n) ml[j] = float2{-INFINITY, 0.0f};
+      }
+      float now = top;
+#pragma unroll
+      for (int j = 0; j < kAhead; j++) now = fmaxf(now, ml[j].x);
+      const float by = now > -INFINITY ? now : 0.0f, keep = __builtin_amdgcn_exp2f(top - by);
+      top = now;
+      sum *= keep;
+#pragma unroll
+      for (int c = 0; c < 4; c++) {
+        x[c] *= keep;
+        y[c] *= keep;
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; j++) {
+        const float f = __builtin_amdgcn_exp2f(ml[j].x - by);
+        if (f == 0.0f) continue;  // what its sums are is of no account
+        sum += f * ml[j].y;
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+          x[c] += f * p[j][c];
+          y[c] += f * q[j][c];
         }
       }
     }
+    if (!few) {
 #pragma unroll
-    for (int h = LANES; h < 64; h <<= 1) {
-      sum += __shfl_xor(sum, h);
+      for (int h = LANES; h < 64; h <<= 1) {
+        const float other = __shfl_xor(top, h), now = fmaxf(top, other), by = now > -INFINITY ? now : 0.0f;
+        const float f = __builtin_amdgcn_exp2f(top - by), o = __builtin_amdgcn_exp2f(other - by);
+        top = now;
+        sum = sum * f + __shfl_xor(sum, h) * o;
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
-        x[j] += __shfl_xor(x[j], h);
-        y[j] += __shfl_xor(y[j], h);
+        for (int c = 0; c < 4; c++) {
+          x[c] = x[c] * f + __shfl_xor(x[c], h) * o;
+          y[c] = y[c] * f + __shfl_xor(y[c], h) * o;
+        }
       }
     }
-    if (side == 0 && e < a.cache.plane[1].dim) write_row<FMT>(a, s, it.tile * MT + r, g, e, x, y, sum);
+    if ((few ? r0 + side < there : side == 0) && e < a.cache.plane[1].dim)
+      write_row<FMT>(a, s, it.tile * MT + r, g, e, x, y, sum);
   }
 }
 
@@ -68,13 +98,18 @@ int launch_both(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream
   float* part = (float*)(ws + p.part);
   float2* ml = (float2*)(ws + p.ml);
   Open* open = (Open*)(ws + p.open);
-  int64_t* totals = (int64_t*)(ws + p.totals);
-  const unsigned n = (unsigned)p.workers * (unsigned)a.cache.heads;
+  Totals* totals = (Totals*)(ws + p.totals);
+  const unsigned n = (unsigned)p.workers * ((unsigned)a.cache.heads >> p.heads_log);
   hipLaunchKernelGGL(kernel, dim3(n), dim3(kThreads), 0, stream, a, part, ml, open, totals, p.workers);
   if (hipGetLastError() != hipSuccess) return MXFP4_ERR_DEVICE;
   // one unit holds the longest context that the table can: nothing to join
-  if ((int64_t)a.cache.max_pages * a.cache.page_size <= p.unit) return MXFP4_OK;
-  hipLaunchKernelGGL((attend_join_kernel<FMT, DV, NT>), dim3(n, 2 * NT), dim3(kThreads), 0, stream, a, part, ml, open, totals, p.workers);
+  if ((int64_t)a.cache.max_pages * a.cache.page_size <= 1 << p.unit_log) return MXFP4_OK;
+  // at most `workers` items are in parts; enough workgroups to have their rows side by side
+  const unsigned groups = (unsigned)a.cache.heads >> p.heads_log, heads = 1u << p.heads_log;
+  const unsigned entries = groups * (unsigned)(a.open_items ? a.open_items : p.workers);
+  const unsigned rows = min(4u * NT, max((unsigned)NT, 2048u / (entries * heads)));
+  hipLaunchKernelGGL((attend_join_kernel<FMT, DV, NT>), dim3(entries, rows, heads), dim3(kThreads), 0, stream, a, part, ml, open,
+                     totals, p.workers);
   return hipGetLastError() == hipSuccess ? MXFP4_OK : MXFP4_ERR_DEVICE;
 }
 

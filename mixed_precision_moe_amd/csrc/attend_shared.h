@@ -95,7 +95,7 @@ struct Pieces {
 template <int FMT, int DK, int DV, int WR, int KEYS, int WAVES>
 __global__ __launch_bounds__(kThreads, WAVES) void attend_shared_kernel(AttendArgs given, float* __restrict__ part,
                                                                         float2* __restrict__ part_ml,
-                                                                        Open* __restrict__ open, int64_t* __restrict__ totals, int workers) {
+                                                                        Open* __restrict__ open, Totals* __restrict__ totals, int workers) {
   using Sh = Shared<FMT, DK, DV, WR, KEYS>;
   constexpr int MT = Sh::kRows, NT = 2, KT = Sh::kKT;
   static_assert(KT % 2 == 0 && KEYS <= 64, "32 positions a matrix instruction, and 64 a lookup");
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_shared_kernel(AttendAr
   __shared__ float ms[Sh::kWK][MT], ls[Sh::kWK][MT];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, kg = lane >> 4;
   const int wr = wave % WR, wk = wave / WR;
-  Work<MT, KEYS> w;
+  Work<MT> w;
   if (!w.begin(given, workers, open, totals, lane)) return;
   const float sc = score_scale<FMT>(given);
 
@@ -127,7 +127,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_shared_kernel(AttendAr
       const int32_t r = w.ti.tile * MT + 32 * wr + 16 * n + col;
       const int32_t d = (uint32_t)r / (uint32_t)a.group;
       draft[n] = d < s.rows ? d : -1;
-      const uint16_t* src = (const uint16_t*)pk.rows + (int64_t)(s.first + d) * pk.ldt + (w.g * a.group + (r - d * a.group)) * pk.ldh;
+      const uint16_t* src = (const uint16_t*)pk.rows + (int64_t)(s.first + d) * pk.ldt + (w.group * a.group + (r - d * a.group)) * pk.ldh;
 #pragma unroll
       for (int i = 0; i < DK / 32; i++) {
         const int e = 32 * i + 8 * kg;
@@ -147,7 +147,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_shared_kernel(AttendAr
       const uint32_t p = a.page_of((uint32_t)pos);
       const int32_t page = c.table[(int64_t)w.b * c.ld_table + p];
       if (page < 0 || page >= c.num_pages) return -1;
-      return ((int64_t)page * c.page_size + ((uint32_t)pos - p * (uint32_t)c.page_size)) * c.heads + w.g;
+      return ((int64_t)page * c.page_size + ((uint32_t)pos - p * (uint32_t)c.page_size)) * c.heads + w.group;
     };
     const auto note = [&](int32_t k, int64_t vector) {
       if (lane < KEYS) vectors[k & 3][lane] = vector;
@@ -223,19 +223,20 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_shared_kernel(AttendAr
       for (int x = 0; x < Sh::kWK; x++) {
         __syncthreads();
         if (x != wk || wr < first || wr >= first + kGroups) continue;
-        float top[NT];
 #pragma unroll
         for (int n = 0; n < NT; n++) {
-          top[n] = ms[0][32 * wr + 16 * n + col];
+          const int r = 32 * wr + 16 * n;
+          float top = ms[0][r + col];
 #pragma unroll
-          for (int y = 1; y < Sh::kWK; y++) top[n] = fmaxf(top[n], ms[y][32 * wr + 16 * n + col]);
+          for (int y = 1; y < Sh::kWK; y++) top = fmaxf(top, ms[y][r + col]);
+          rows.join(n, (float*)lds + (r - 32 * first) * (DV + 4), DV + 4, top, x == 0, lane);
         }
-        rows.join((float*)lds + 32 * (wr - first) * (DV + 4), DV + 4, top, x == 0, lane);
       }
       __syncthreads();
-      write_item<FMT, DV, MT, Sh::kWK, KEYS>(arguments(), w, workers, 32 * first, 32 * kGroups, (const float*)lds, ms, ls, part, part_ml);
+      write_item<FMT, DV, MT>(arguments(), w, w.group, workers, 32 * first, 32 * kGroups, (const float*)lds, ms[0], ls[0], Sh::kWK, threadIdx.x,
+                              kThreads, part, part_ml);
     }
-    w.leave_open(open, workers);
+    w.leave_open(arguments(), open, workers);
     __syncthreads();
     if (!w.next(arguments())) break;
   }

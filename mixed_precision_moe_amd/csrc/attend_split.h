@@ -1,4 +1,6 @@
-// Attention for few rows a key head: the four waves of a worker take 32 positions of a unit each and meet once an item.
+// Attention for few rows a key head: the four waves of a worker take four heads, or two or one with positions of their own,
+// and meet once an item.  Heads side by side read whole stretches of tokens: 8 heads of 128 bytes were read at 5.4 TB/s by
+// waves with a head each, at 4.6 TB/s by waves with 32 positions each of one head.
 //
 // Codes of K go from memory to registers as they are needed there (a lane: a quarter of a key's elements); V's are
 // dequantized into the wave's own piece of LDS.  The next tile's codes are on their way while a tile is worked on: K's
@@ -9,8 +11,7 @@
 
 namespace {
 
-constexpr int kTile = 32;               // positions of a wave at a time
-constexpr int kUnit = kTile * kWaves;   // and of a worker
+constexpr int kTile = 32;  // positions of a wave at a time
 
 template <int FMT, int DK, int DV, int NT>
 struct Shape {
@@ -33,16 +34,16 @@ struct Shape {
 template <int FMT, int DK, int DV, int NT, int WAVES, bool PAGED>
 __global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArgs given, float* __restrict__ part,
                                                                  float2* __restrict__ part_ml, Open* __restrict__ open,
-                                                                 int64_t* __restrict__ totals, int workers) {
+                                                                 Totals* __restrict__ totals, int workers) {
   using Sh = Shape<FMT, DK, DV, NT>;
   using Found = std::conditional_t<PAGED, int32_t, int64_t>;
   constexpr int MT = Sh::kRows;
   constexpr int kBytes = kWaves * kTile * Sh::kStride * 2;
-  static_assert(MT * (DV + 4) * 4 <= kBytes, "the sums take the place of V");
+  static_assert(16 * (DV + 4) * 4 <= kBytes / kWaves, "sixteen rows' sums take the place of a wave's V");
   __shared__ __attribute__((aligned(16))) uint8_t lds[kBytes];
   __shared__ float ms[kWaves][MT], ls[kWaves][MT];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, kg = lane >> 4;
-  Work<MT, kUnit> w;
+  Work<MT> w;
   if (!w.begin(given, workers, open, totals, lane)) return;
   const CacheArgs& c = given.cache;
   const float sc = score_scale<FMT>(given);
@@ -57,10 +58,14 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArg
   const uint32_t vs_at = v_in_tile * (DV / kBlock<FMT>) + lane % Sh::kPerKey * Sh::kElems / kBlock<FMT>;
   uint16_t* const vt = (uint16_t*)lds + wave * kTile * Sh::kStride;
 
+  // 2^heads_log heads of a worker, for each of them `side` waves; a unit is a tile of each wave
+  const int side_log = 2 - given.heads_log, side = 1 << side_log, first_wave = wave & ~(side - 1);
+
   for (;;) {
     w.settle();
     const Seq& s = w.s;
-    const int32_t k0 = w.k0, k1 = w.k1(), end = w.ti.end;
+    const int32_t k0 = w.k0, k1 = w.k1(), end = w.ti.end, g = (w.group << given.heads_log) + (wave >> side_log);
+    const auto base_of = [&](int32_t k) { return ((k << side_log) + (wave & (side - 1))) * kTile; };
     const int32_t* const pages = c.table + (int64_t)w.b * c.ld_table;
 
     // Where a tile's codes are.  PAGED: its page, in every lane; else in the lanes 0 to 31 the cache's vector of each of its
@@ -68,21 +73,21 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArg
     // those behind it as well: places past the end, without a page or past a vector are replaced by some that are there, and
     // what comes from them is dropped.
     const auto find = [&](int32_t k) {
-      const int32_t pos = k * kUnit + wave * kTile + (PAGED ? 0 : lane & 31), there = min(pos, end - 1);
+      const int32_t pos = base_of(k) + (PAGED ? 0 : lane & 31), there = min(pos, end - 1);
       const uint32_t p = given.page_of((uint32_t)there);
       const int32_t page = pages[p];
       Found f = page;
       if (!PAGED)
         f = pos < end && page >= 0 && page < c.num_pages
-                ? ((int64_t)page * c.page_size + ((uint32_t)there - p * (uint32_t)c.page_size)) * heads + w.g
+                ? ((int64_t)page * c.page_size + ((uint32_t)there - p * (uint32_t)c.page_size)) * heads + g
                 : -1;
       return f;
     };
     // PAGED: the tile's first vector.  Its positions past the end lie in the page too.
     const auto first_vector = [&](int32_t k, Found f) -> int64_t {
       const int32_t page = uniform((int)f), there = page < 0 || page >= c.num_pages ? 0 : page;
-      const uint32_t pos = (uint32_t)k * kUnit + (uint32_t)wave * kTile;
-      return ((int64_t)there * c.page_size + (pos - given.page_of(pos) * (uint32_t)c.page_size)) * heads + w.g;
+      const uint32_t pos = base_of(k);
+      return ((int64_t)there * c.page_size + (pos - given.page_of(pos) * (uint32_t)c.page_size)) * heads + g;
     };
     uint32_t kc[2][Sh::kCodes], ks[2][Sh::kScales];
     // a lane's quarter of a key
@@ -183,7 +188,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArg
         const int32_t r = w.ti.tile * MT + 16 * n + col;
         const int32_t d = (uint32_t)r / (uint32_t)a.group;
         draft[n] = d < s.rows ? d : -1;
-        const uint16_t* src = (const uint16_t*)query.rows + (int64_t)(s.first + d) * query.ldt + (w.g * a.group + (r - d * a.group)) * query.ldh;
+        const uint16_t* src = (const uint16_t*)query.rows + (int64_t)(s.first + d) * query.ldt + (g * a.group + (r - d * a.group)) * query.ldh;
 #pragma unroll
         for (int i = 0; i < Sh::kSteps; i++) {
           const int e = kg * Sh::kQuarter + 8 * i;
@@ -197,7 +202,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArg
 
     const auto step = [&](int32_t k, auto more) {
       constexpr bool kMore = decltype(more)::value;  // another tile follows
-      const int32_t base = k * kUnit + wave * kTile;
+      const int32_t base = base_of(k);
       // which of the tile's positions have a vector, and whether all rows see them all
       uint32_t there;
       if (PAGED) {
@@ -290,28 +295,28 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArg
       step(k1 - 1, std::false_type{});
     }
 
-    // the waves' sums, joined
-    float top[NT];
+    // the sums of a head's waves, joined
 #pragma unroll
     for (int n = 0; n < NT; n++)
       if (kg == 0) {
         ms[wave][16 * n + col] = rows.m[n];
         ls[wave][16 * n + col] = rows.l[n][0];
       }
-    for (int x = 0; x < kWaves; x++) {
-      __syncthreads();
-      if (x != wave) continue;
+    float* const sums = (float*)(lds + first_wave * (kBytes / kWaves));
 #pragma unroll
-      for (int n = 0; n < NT; n++) {
-        top[n] = ms[0][16 * n + col];
-#pragma unroll
-        for (int y = 1; y < kWaves; y++) top[n] = fmaxf(top[n], ms[y][16 * n + col]);
+    for (int n = 0; n < NT; n++) {
+      for (int x = 0; x < side; x++) {
+        __syncthreads();
+        if (first_wave + x != wave) continue;
+        float top = ms[first_wave][16 * n + col];
+        for (int y = 1; y < side; y++) top = fmaxf(top, ms[first_wave + y][16 * n + col]);
+        rows.join(n, sums, DV + 4, top, x == 0, lane);
       }
-      rows.join((float*)lds, DV + 4, top, x == 0, lane);
+      __syncthreads();
+      write_item<FMT, DV, MT>(arguments(), w, g, workers, 16 * n, 16, sums, ms[first_wave], ls[first_wave], side,
+                              (wave - first_wave) * 64 + lane, side * 64, part, part_ml);
     }
-    __syncthreads();
-    write_item<FMT, DV, MT, kWaves, kUnit>(arguments(), w, workers, 0, MT, (const float*)lds, ms, ls, part, part_ml);
-    w.leave_open(open, workers);
+    w.leave_open(arguments(), open, workers);
     __syncthreads();
     if (!w.next(arguments())) break;
   }

@@ -89,25 +89,40 @@ int pool_args(PoolArgs& a, int64_t num_pages, int32_t page_size, int32_t* refs, 
 
 // The sizes of the attention kernels: dims up to 64, 128, 192 and 128, or 256; tiles of rows by what a sequence has on average:
 // up to 16 and 32 the kernel whose waves split the positions, up to 64 (where it exists) and from there on the shared one.
-AttendPlan attend_plan(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows, int32_t n_seqs) {
+AttendPlan attend_plan(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows, int32_t n_seqs, int64_t positions) {
   AttendPlan p = {};
   const int k = d->k_dim, v = d->v_dim;
   p.dk = k <= 64 && v <= 64 ? 64 : k <= 128 && v <= 128 ? 128 : k <= 192 && v <= 128 ? 192 : 256;
   p.dv = p.dk == 192 ? 128 : p.dk;
   const int64_t per_seq = (rows + n_seqs - 1) / (n_seqs > 0 ? n_seqs : 1) * (q_heads / d->heads);
   p.nt = per_seq <= 16 ? 1 : per_seq <= 32 ? 2 : per_seq <= 64 && attend_keys(p.dk) == 64 ? 4 : 8;
-  p.unit = p.nt <= 2 ? 128 : attend_keys(p.dk);
-  const int64_t fill = (int64_t)kCus * attend_waves(p.dk, p.nt) / d->heads;
+  if (p.nt <= 2) {
+    // heads side by side, unless the positions are few: one unit of all four waves then needs no join
+    p.heads_log = positions <= 128 ? 0 : d->heads % 4 == 0 ? 2 : d->heads % 2 == 0 ? 1 : 0;
+    p.unit_log = 7 - p.heads_log;
+  } else {
+    p.unit_log = attend_keys(p.dk) == 64 ? 6 : 5;
+  }
+  const int64_t groups = d->heads >> p.heads_log, fill = (int64_t)kCus * attend_waves(p.dk, p.nt) / groups;
   p.workers = (int32_t)(fill < 1 ? 1 : fill < 8 ? fill : fill & ~int64_t(7));  // as many on each XCD
   uint64_t at = 0;
   auto take = [&](uint64_t bytes) { uint64_t o = at; at = up256(at + bytes); return o; };
   const uint64_t all = (uint64_t)p.workers * (uint64_t)d->heads, part_rows = 2 * all * 16 * (uint64_t)p.nt;
   p.part = take(4 * part_rows * (uint64_t)p.dv);
   p.ml = take(8 * part_rows);
-  p.open = take(12 * all);
-  p.totals = take(8);
+  // tiles, each sequence's last one cut short
+  const int64_t items = rows * (q_heads / d->heads) / (16 * p.nt) + n_seqs;
+  p.items = items < p.workers ? (int32_t)items : 0;
+  p.open = take(16 * (uint64_t)(p.items ? p.items : p.workers) * (uint64_t)groups);
+  p.totals = take(16);
   p.total = at;
   return p;
+}
+
+// Enough for either plan of a call: it goes by its table too.
+uint64_t attend_bytes(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows, int32_t n_seqs) {
+  const uint64_t few = attend_plan(d, q_heads, rows, n_seqs, 0).total, many = attend_plan(d, q_heads, rows, n_seqs, INT64_MAX).total;
+  return few > many ? few : many;
 }
 
 int check_attend(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows, int32_t n_seqs) {
@@ -128,7 +143,7 @@ int check_attend(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows, int32
 MX_API size_t mxfp4_cache_attend_workspace_bytes(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows,
                                                  int32_t n_seqs) {
   if (check_attend(d, q_heads, rows, n_seqs) != MXFP4_OK) return 0;
-  return (size_t)attend_plan(d, q_heads, rows, n_seqs).total;
+  return (size_t)attend_bytes(d, q_heads, rows, n_seqs);
 }
 
 MX_API int mxfp4_cache_attend(const mxfp4_cache_dims* d, const void* k_q, const void* k_s, const void* v_q,
@@ -154,8 +169,8 @@ MX_API int mxfp4_cache_attend(const mxfp4_cache_dims* d, const void* k_q, const 
   if (!aligned(q_bf16, 16) || !aligned(out, 16) || !aligned(k_q, 8) || !aligned(v_q, 8) || !aligned(cu_rows, 4) ||
       !aligned(start, 4) || !aligned(page_table, 4) || !aligned(workspace, 256))
     return MXFP4_ERR_ALIGN;
-  const AttendPlan plan = attend_plan(d, q_heads, rows, n_seqs);
-  if (workspace_bytes < plan.total) return MXFP4_ERR_WORKSPACE;
+  const AttendPlan plan = attend_plan(d, q_heads, rows, n_seqs, (int64_t)max_pages * d->page_size);
+  if (workspace_bytes < attend_bytes(d, q_heads, rows, n_seqs)) return MXFP4_ERR_WORKSPACE;
   AttendArgs a = {};
   CacheArgs& c = a.cache;
   c.plane[0] = CachePlane{(void*)q_bf16, q_ldt, q_ldh, (uint8_t*)k_q, (uint8_t*)k_s, d->k_dim, d->k_global_scale};
@@ -178,6 +193,9 @@ MX_API int mxfp4_cache_attend(const mxfp4_cache_dims* d, const void* k_q, const 
   a.set_page_size(d->page_size);
   a.rows_of_tile = 16 * plan.nt / a.group;
   a.part_of_tile = 16 * plan.nt % a.group;
+  a.unit_log = plan.unit_log;
+  a.heads_log = plan.heads_log;
+  a.open_items = plan.items;
   a.scale = scale;
   uint8_t* ws = (uint8_t*)workspace;
   if (d->fmt == MXFP4_FMT_MXFP4) return launch_attend_mxfp4(a, plan, ws, S(stream));

@@ -31,12 +31,14 @@ struct AttendArgs {
     page_shift = power ? log : log - 1;
   }
   int32_t rows_of_tile, part_of_tile;  // tile rows / group, and the remainder
+  int32_t unit_log, heads_log;         // positions of a unit and key heads of a worker: powers of two
+  int32_t open_items;                  // most items of a head, where they are fewer than its workers, else 0
   float scale;
 };
-// How a call is cut up: tiles of 16 nt rows, units of positions, elements of a key and a value in the kernel, workers of each
-// head; the workspace's parts.
+// How a call is cut up: tiles of 16 nt rows, units of 2^unit_log positions, elements of a key and a value in the kernel, workers
+// of each 2^heads_log key heads, open_items; the workspace's parts.
 struct AttendPlan {
-  int32_t nt, unit, dk, dv, workers;
+  int32_t nt, unit_log, heads_log, dk, dv, workers, items;
   uint64_t part, ml, open, totals, total;
 };
 // Workgroups of a compute unit: what their registers and LDS leave room for.

@@ -139,7 +139,8 @@ static void test_attend() {
           // the parts follow each other inside the workspace
           const uint64_t workers = (uint64_t)g_plan.workers * heads, part_rows = 2 * workers * 16 * g_plan.nt;
           CHECK(g_plan.part + 4 * part_rows * g_plan.dv <= g_plan.ml && g_plan.ml + 8 * part_rows <= g_plan.open &&
-                g_plan.open + 12 * workers <= g_plan.totals && g_plan.totals + 8 <= g_plan.total);
+                g_plan.open + 16 * ((g_plan.items ? (uint64_t)g_plan.items * heads : workers) >> g_plan.heads_log) <= g_plan.totals &&
+                g_plan.totals + 16 <= g_plan.total);
         }
   d = kOk;
   CHECK(mxfp4_cache_attend_workspace_bytes(&d, 3, 5, 2) == 0 && mxfp4_cache_attend_workspace_bytes(nullptr, 4, 5, 2) == 0);
