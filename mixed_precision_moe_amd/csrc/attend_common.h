@@ -35,6 +35,7 @@ typedef unsigned u32x2_t __attribute__((ext_vector_type(2)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef u32x4_t u32x4_a8 __attribute__((aligned(8)));  // vectors of codes start on 8 bytes
 typedef u32x2_t u32x2_a8 __attribute__((aligned(8)));
+typedef uint16_t u16_a1 __attribute__((aligned(1)));
 
 constexpr int kThreads = 256;
 constexpr int kWaves = 4;
@@ -433,19 +434,35 @@ struct Rows {
   }
 
   // O^T += V^T P^T for 32 positions: their values are rows of LDS, `stride` elements apart.
-  template <int KT>
+  template <int AHEAD, int KT>
   MX_DEV void add_values(const uint16_t* v0, int stride, const bf16x8_t (&p)[NT][KT], int h, int lane) {
     // two blocks of four positions by sixteen elements a group of sixteen lanes, transposed
     typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
     const int col = lane & 15, kg = lane >> 4;
     const uint16_t* src = v0 + (4 * kg + (col >> 2)) * stride + 4 * (col & 3);
+    // AHEAD columns of tiles are read ahead of the products of the AHEAD before
+    static_assert(VT % AHEAD == 0, "whole steps");
+    s16x4_t x[2][AHEAD][2];
+    const auto read = [&](int v0) {
 #pragma unroll
-    for (int v = 0; v < VT; v++) {
-      const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src + 16 * v));
-      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src + 16 * stride + 16 * v));
-      const bf16x8_t x = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+      for (int v = 0; v < AHEAD; v++)
 #pragma unroll
-      for (int n = 0; n < NT; n++) o[n][v] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, p[n][h], o[n][v], 0, 0, 0);
+        for (int y = 0; y < 2; y++)
+          x[v0 / AHEAD & 1][v][y] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src + 16 * y * stride + 16 * (v0 + v)));
+    };
+    read(0);
+#pragma unroll
+    for (int v0 = 0; v0 < VT; v0 += AHEAD) {
+      if (v0 + AHEAD < VT) read(v0 + AHEAD);
+      if (AHEAD > 1) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int v = 0; v < AHEAD; v++) {
+        const auto& t = x[v0 / AHEAD & 1][v];
+        const bf16x8_t both = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(t[0], t[1], 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+        for (int n = 0; n < NT; n++) o[n][v0 + v] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(both, p[n][h], o[n][v0 + v], 0, 0, 0);
+      }
+      if (AHEAD > 1) __builtin_amdgcn_sched_barrier(0);
     }
   }
 
@@ -491,12 +508,14 @@ MX_DEV void hide(const AttendArgs& a, const Seq& s, const int32_t (&draft)[NT], 
       seen |= four << (4 * t);
       nan |= ((uint32_t)(bad >> (16 * t + 4 * kg)) & four) << (4 * t);
     }
+    // with masks of bits, which stay in vector registers
 #pragma unroll
     for (int t = 0; t < KT; t++)
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        if (nan >> (4 * t + i) & 1) sv[n][t][i] = NAN;
-        if (!(seen >> (4 * t + i) & 1)) sv[n][t][i] = -INFINITY;
+        const uint32_t keep = (uint32_t)__builtin_amdgcn_sbfe((int)seen, 4 * t + i, 1), none = __builtin_amdgcn_sbfe((int)nan, 4 * t + i, 1);
+        const uint32_t x = __float_as_uint(sv[n][t][i]) | (none & 0x7FFFFFFFu);
+        sv[n][t][i] = __uint_as_float((x & keep) | (~keep & 0xFF800000u));
       }
   }
 }

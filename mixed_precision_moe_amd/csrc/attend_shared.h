@@ -29,7 +29,7 @@ struct Pieces {
   static constexpr int kN = (kAll + kThreads - 1) / kThreads;
   static constexpr int kScales = kElems / kBlock<FMT> ? kElems / kBlock<FMT> : 1;
   u32x4_t codes[kN];
-  uint32_t scales[kN][kScales];
+  uint32_t scales[kN];  // a byte a block
 
   // vectors: the cache's vector of each position, -1: none
   MX_DEV void load(const CachePlane& p, const int64_t* vectors) {
@@ -39,23 +39,23 @@ struct Pieces {
     for (int i = 0; i < kN; i++) {
       const int id = i * kThreads + threadIdx.x, key = id / kPerKey, piece = id % kPerKey, e = piece * kElems;
       codes[i] = u32x4_t{0, 0, 0, 0};
-#pragma unroll
-      for (int j = 0; j < kScales; j++) scales[i][j] = 0;
-      if (kAll % kThreads && id >= kAll) continue;
-      const int64_t at = vectors[key];
+      scales[i] = 0;
+      const int64_t at = kAll % kThreads && id >= kAll ? -1 : vectors[key];
       if (at < 0 || e >= p.dim) continue;
       const uint8_t* src = p.q + at * bytes + 16 * piece;
       const uint8_t* s = p.s + at * blocks + e / kBlock<FMT>;
-      if (e + kElems <= p.dim) {
+      if (kScales == 1) {
         codes[i] = *reinterpret_cast<const u32x4_a8*>(src);
-      } else {
+        scales[i] = s[0];
+      } else if (e + kElems <= p.dim) {
+        codes[i] = *reinterpret_cast<const u32x4_a8*>(src);
+        scales[i] = *reinterpret_cast<const u16_a1*>(s);
+      } else {  // the last block of an odd number
         const u32x2_t x = *reinterpret_cast<const u32x2_a8*>(src);
         codes[i][0] = x[0];
         codes[i][1] = x[1];
+        scales[i] = s[0];
       }
-#pragma unroll
-      for (int j = 0; j < kScales; j++)
-        if (e + j * kBlock<FMT> < p.dim) scales[i][j] = s[j];
     }
   }
 
@@ -68,8 +68,8 @@ struct Pieces {
       uint16_t* to = dst + key * stride + piece * kElems;
 #pragma unroll
       for (int j = 0; j < kElems / 8; j++)
-        *reinterpret_cast<bf16x8_t*>(to + 8 * j) = FMT == MXFP4_FMT_MXFP8 ? values8<FMT>(codes[i][2 * j], codes[i][2 * j + 1], scales[i][0])
-                                                                          : values8<FMT>(codes[i][j], 0, scales[i][8 * j / kBlock<FMT>]);
+        *reinterpret_cast<bf16x8_t*>(to + 8 * j) = FMT == MXFP4_FMT_MXFP8 ? values8<FMT>(codes[i][2 * j], codes[i][2 * j + 1], scales[i])
+                                                                          : values8<FMT>(codes[i][j], 0, scales[i] >> 8 * (8 * j / kBlock<FMT>) & 0xFFu);
     }
   }
 
@@ -80,13 +80,12 @@ struct Pieces {
       const int id = i * kThreads + threadIdx.x, key = id / kPerKey;
       bool x = false;
 #pragma unroll
-      for (int j = 0; j < kScales; j++) x = x || not_finite<FMT>(scales[i][j]);
+      for (int j = 0; j < kScales; j++) x = x || not_finite<FMT>(scales[i] >> 8 * j & 0xFFu);
       if (FMT == MXFP4_FMT_MXFP8)
         x = x || has_nan_code(codes[i][0]) || has_nan_code(codes[i][1]) || has_nan_code(codes[i][2]) || has_nan_code(codes[i][3]);
       if (!x) continue;
       codes[i] = u32x4_t{0, 0, 0, 0};
-#pragma unroll
-      for (int j = 0; j < kScales; j++) scales[i][j] = 0;
+      scales[i] = 0;
       atomicOr(&bad[key >> 5], 1u << (key & 31));
     }
   }
@@ -135,19 +134,22 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_shared_kernel(AttendAr
         if (draft[n] >= 0 && e < pk.dim) q[n][i] = query8(a, src + e);
       }
     }
+    // the positions before this one are seen by all of the wave's rows: with a mask the context, else the first row's drafts too
+    const int32_t seen = (int32_t)min((int64_t)s.start + (a.mask ? 0 : (uint32_t)(w.ti.tile * MT + 32 * wr) / (uint32_t)a.group + 1), (int64_t)INT32_MAX);
     Rows<NT, DV / 16> rows;
     rows.clear();
 
-    // the vector of this lane's position of tile k
-    const auto find = [&](int32_t k) -> int64_t {
-      const AttendArgs a = arguments();
+    // the page of this lane's position of tile k, and that position's vector
+    const int32_t* table = a.cache.table + (int64_t)w.b * a.cache.ld_table;
+    const auto look_up = [&](int32_t k) -> int32_t {
+      return end > 0 ? table[a.page_of(min((uint32_t)k * KEYS + lane, (uint32_t)end - 1))] : -1;
+    };
+    const auto find = [&](int32_t k, int32_t page) -> int64_t {
       const CacheArgs& c = a.cache;
-      const int32_t pos = k * KEYS + lane;
-      if (lane >= KEYS || pos >= end) return -1;
-      const uint32_t p = a.page_of((uint32_t)pos);
-      const int32_t page = c.table[(int64_t)w.b * c.ld_table + p];
-      if (page < 0 || page >= c.num_pages) return -1;
-      return ((int64_t)page * c.page_size + ((uint32_t)pos - p * (uint32_t)c.page_size)) * c.heads + w.group;
+      const uint32_t pos = (uint32_t)k * KEYS + lane;
+      if (lane >= KEYS || pos >= (uint32_t)end || page < 0 || page >= c.num_pages) return -1;
+      const uint32_t at = pos - a.page_of(pos) * (uint32_t)c.page_size;
+      return ((int64_t)page * c.page_size + at) * c.heads + w.group;
     };
     const auto note = [&](int32_t k, int64_t vector) {
       if (lane < KEYS) vectors[k & 3][lane] = vector;
@@ -159,7 +161,6 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_shared_kernel(AttendAr
     const auto tile_k = [&](int32_t k) { return (uint16_t*)(lds + (k & 1) * Sh::kTileBytes); };
     const auto tile_v = [&](int32_t k) { return (uint16_t*)(lds + (k & 1) * Sh::kTileBytes) + KEYS * Sh::kStrideK; };
     const auto load = [&](int32_t k) {
-      const AttendArgs a = arguments();
       kp.load(a.cache.plane[0], vectors[k & 3]);
       vp.load(a.cache.plane[1], vectors[k & 3]);
     };
@@ -171,7 +172,8 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_shared_kernel(AttendAr
     };
 
     if (threadIdx.x < 8) (&bad[0][0])[threadIdx.x] = 0;
-    if (wave < 3) note(k0 + wave, find(k0 + wave));
+    if (wave < 3) note(k0 + wave, find(k0 + wave, look_up(k0 + wave)));
+    int32_t page = look_up(k0 + 3);
     __syncthreads();
     load(k0);
     store(k0);
@@ -179,36 +181,44 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_shared_kernel(AttendAr
     __syncthreads();
     for (int32_t k = k0; k < k1; k++) {
       const int32_t base = k * KEYS + 16 * KT * wk;
-      int64_t ahead = -1;
-      if (wave == 0 && k + 3 < k1) ahead = find(k + 3);
+      const int32_t ahead = look_up(k + 4);
       f32x4_t sv[NT][KT];
       const uint16_t* keys = tile_k(k) + (16 * KT * wk + col) * Sh::kStrideK + 8 * kg;
 #pragma unroll
-      for (int t = 0; t < KT; t++) {
+      for (int t = 0; t < KT; t++)
 #pragma unroll
         for (int n = 0; n < NT; n++) sv[n][t] = f32x4_t{0, 0, 0, 0};
+      bf16x8_t x[2][KT];
 #pragma unroll
-        for (int i = 0; i < DK / 32; i++) {
-          const bf16x8_t x = *reinterpret_cast<const bf16x8_t*>(keys + 16 * t * Sh::kStrideK + 32 * i);
+      for (int t = 0; t < KT; t++) x[0][t] = *reinterpret_cast<const bf16x8_t*>(keys + 16 * t * Sh::kStrideK);
 #pragma unroll
-          for (int n = 0; n < NT; n++) sv[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, q[n][i], sv[n][t], 0, 0, 0);
+      for (int i = 0; i < DK / 32; i++) {
+        if (i + 1 < DK / 32) {
+#pragma unroll
+          for (int t = 0; t < KT; t++) x[(i + 1) & 1][t] = *reinterpret_cast<const bf16x8_t*>(keys + 16 * t * Sh::kStrideK + 32 * (i + 1));
         }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int t = 0; t < KT; t++)
+#pragma unroll
+          for (int n = 0; n < NT; n++) sv[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i & 1][t], q[n][i], sv[n][t], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
       }
       constexpr uint64_t kFull = KT == 4 ? ~0ull : ~0u;
       const uint64_t there = valid[k & 3] >> (16 * KT * wk) & kFull;
-      if (there != kFull || (int64_t)base + 16 * KT > s.start) {
-        const uint64_t b = (uint64_t)bad[k & 3][1] << 32 | bad[k & 3][0];
-        hide<NT, KT>(arguments(), s, draft, base, there, b >> (16 * KT * wk), kg, sv);
-      }
+      const uint64_t b = ((uint64_t)bad[k & 3][1] << 32 | bad[k & 3][0]) >> (16 * KT * wk) & kFull;
+      if (__builtin_expect(there != kFull || b != 0 || base + 16 * KT > seen, 0)) hide<NT, KT>(arguments(), s, draft, base, there, b, kg, sv);
       bf16x8_t p[NT][KT / 2];
       rows.template weights<KT>(sv, sc, p);
 #pragma unroll
       for (int h = 0; h < KT / 2; h++)
-        rows.template add_values<KT / 2>(tile_v(k) + (16 * KT * wk + 32 * h) * Sh::kStrideV, Sh::kStrideV, p, h, lane);
+        rows.template add_values<4, KT / 2>(tile_v(k) + (16 * KT * wk + 32 * h) * Sh::kStrideV, Sh::kStrideV, p, h, lane);
       // the other tiles' turn
       if (k + 1 < k1) store(k + 1);
+      if (wave == 0) note(k + 3, find(k + 3, page));
+      page = ahead;
+      asm volatile("" : "+v"(page));  // here, and not behind the loads that follow
       if (k + 2 < k1) load(k + 2);
-      if (wave == 0 && k + 3 < k1) note(k + 3, ahead);
       if (threadIdx.x < 2) bad[(k + 2) & 3][threadIdx.x] = 0;
       __syncthreads();
     }

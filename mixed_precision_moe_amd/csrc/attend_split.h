@@ -283,7 +283,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArg
       }
       if (kMore) load_v(k + 1, next);
       __builtin_amdgcn_wave_barrier();
-      rows.template add_values<1>(vt, Sh::kStride, p, 0, lane);
+      rows.template add_values<1, 1>(vt, Sh::kStride, p, 0, lane);
       __builtin_amdgcn_wave_barrier();
       found = next;
       next = after;
