@@ -94,13 +94,13 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendArgs a, con
 // ---------------------------------------------------------------------------------------------
 
 template <int FMT, int DV, int NT, typename F>
-int launch_both(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream, F kernel) {
+int launch_both(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream, F kernel, int threads = kThreads) {
   float* part = (float*)(ws + p.part);
   float2* ml = (float2*)(ws + p.ml);
   Open* open = (Open*)(ws + p.open);
   Totals* totals = (Totals*)(ws + p.totals);
   const unsigned n = (unsigned)p.workers * ((unsigned)a.cache.heads >> p.heads_log);
-  hipLaunchKernelGGL(kernel, dim3(n), dim3(kThreads), 0, stream, a, part, ml, open, totals, p.workers);
+  hipLaunchKernelGGL(kernel, dim3(n), dim3(threads), 0, stream, a, part, ml, open, totals, p.workers);
   if (hipGetLastError() != hipSuccess) return MXFP4_ERR_DEVICE;
   // one unit holds the longest context that the table can: nothing to join
   if ((int64_t)a.cache.max_pages * a.cache.page_size <= 1 << p.unit_log) return MXFP4_OK;
@@ -124,8 +124,10 @@ int launch_dims(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream
     return launch_both<FMT, DV, 2>(a, p, ws, stream, paged ? attend_split_kernel<FMT, DK, DV, 2, attend_waves(DK, 2), true>
                                                            : attend_split_kernel<FMT, DK, DV, 2, attend_waves(DK, 2), false>);
   constexpr int KEYS = attend_keys(DK);
-  if constexpr (KEYS == 64)
+  if constexpr (KEYS == 64) {
     if (p.nt == 4) return launch_both<FMT, DV, 4>(a, p, ws, stream, attend_shared_kernel<FMT, DK, DV, 2, KEYS, attend_waves(DK, 4)>);
+    if (p.nt == 16) return launch_both<FMT, DV, 16>(a, p, ws, stream, attend_shared_kernel<FMT, DK, DV, 8, KEYS, 2>, 512);
+  }
   return launch_both<FMT, DV, 8>(a, p, ws, stream, attend_shared_kernel<FMT, DK, DV, 4, KEYS, attend_waves(DK, 8)>);
 }
 

@@ -13,7 +13,9 @@ namespace {
 
 template <int FMT, int DK, int DV, int WR, int KEYS>
 struct Shared {
-  static constexpr int kWK = kWaves / WR;       // groups of waves that share the positions
+  static constexpr int kW = WR > kWaves ? WR : kWaves;
+  static constexpr int kThreads = 64 * kW;
+  static constexpr int kWK = kW / WR;           // groups of waves that share the positions
   static constexpr int kRows = 32 * WR;
   static constexpr int kKT = KEYS / kWK / 16;   // tiles of 16 positions of a wave
   static constexpr int kElems = 16 * kPerByte<FMT>;
@@ -23,7 +25,7 @@ struct Shared {
 };
 
 // A thread's pieces of a plane's tile.
-template <int FMT, int KEYS, int D>
+template <int FMT, int KEYS, int D, int kThreads>
 struct Pieces {
   static constexpr int kElems = 16 * kPerByte<FMT>, kPerKey = D / kElems, kAll = KEYS * kPerKey;
   static constexpr int kN = (kAll + kThreads - 1) / kThreads;
@@ -92,16 +94,16 @@ struct Pieces {
 };
 
 template <int FMT, int DK, int DV, int WR, int KEYS, int WAVES>
-__global__ __launch_bounds__(kThreads, WAVES) void attend_shared_kernel(AttendArgs given, float* __restrict__ part,
+__global__ __launch_bounds__(64 * (WR > kWaves ? WR : kWaves), WAVES) void attend_shared_kernel(AttendArgs given, float* __restrict__ part,
                                                                         float2* __restrict__ part_ml,
                                                                         Open* __restrict__ open, Totals* __restrict__ totals, int workers) {
   using Sh = Shared<FMT, DK, DV, WR, KEYS>;
   constexpr int MT = Sh::kRows, NT = 2, KT = Sh::kKT;
   static_assert(KT % 2 == 0 && KEYS <= 64, "32 positions a matrix instruction, and 64 a lookup");
   constexpr int kBytes = 2 * Sh::kTileBytes;
-  // the sums take the place of the tiles, as many groups of 32 rows at a time as fit
-  constexpr int kFit = kBytes / (32 * (DV + 4) * 4), kGroups = kFit < WR ? kFit : WR;
-  static_assert(kGroups > 0 && WR % kGroups == 0, "whole passes");
+  // the sums take the place of the tiles, as many waves' rows at a time as fit
+  constexpr int kFit = kBytes / (32 * (DV + 4) * 4), kGroups = kFit >= WR ? WR : kFit >= 4 ? 4 : kFit >= 2 ? 2 : 1;
+  static_assert(kFit > 0, "a wave's rows at least");
   __shared__ __attribute__((aligned(16))) uint8_t lds[kBytes];
   __shared__ int64_t vectors[4][KEYS];
   __shared__ uint64_t valid[4];
@@ -156,8 +158,8 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_shared_kernel(AttendAr
       const uint64_t there = __ballot(vector >= 0);
       if (lane == 0) valid[k & 3] = there;
     };
-    Pieces<FMT, KEYS, DK> kp;
-    Pieces<FMT, KEYS, DV> vp;
+    Pieces<FMT, KEYS, DK, Sh::kThreads> kp;
+    Pieces<FMT, KEYS, DV, Sh::kThreads> vp;
     const auto tile_k = [&](int32_t k) { return (uint16_t*)(lds + (k & 1) * Sh::kTileBytes); };
     const auto tile_v = [&](int32_t k) { return (uint16_t*)(lds + (k & 1) * Sh::kTileBytes) + KEYS * Sh::kStrideK; };
     const auto load = [&](int32_t k) {
@@ -188,6 +190,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_shared_kernel(AttendAr
       for (int t = 0; t < KT; t++)
 #pragma unroll
         for (int n = 0; n < NT; n++) sv[n][t] = f32x4_t{0, 0, 0, 0};
+      __builtin_amdgcn_s_setprio(1);  // the matrix cores' turn, while other waves do the rest
       bf16x8_t x[2][KT];
 #pragma unroll
       for (int t = 0; t < KT; t++) x[0][t] = *reinterpret_cast<const bf16x8_t*>(keys + 16 * t * Sh::kStrideK);
@@ -204,15 +207,18 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_shared_kernel(AttendAr
           for (int n = 0; n < NT; n++) sv[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i & 1][t], q[n][i], sv[n][t], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
       }
+      __builtin_amdgcn_s_setprio(0);
       constexpr uint64_t kFull = KT == 4 ? ~0ull : ~0u;
       const uint64_t there = valid[k & 3] >> (16 * KT * wk) & kFull;
       const uint64_t b = ((uint64_t)bad[k & 3][1] << 32 | bad[k & 3][0]) >> (16 * KT * wk) & kFull;
       if (__builtin_expect(there != kFull || b != 0 || base + 16 * KT > seen, 0)) hide<NT, KT>(arguments(), s, draft, base, there, b, kg, sv);
       bf16x8_t p[NT][KT / 2];
       rows.template weights<KT>(sv, sc, p);
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int h = 0; h < KT / 2; h++)
         rows.template add_values<4, KT / 2>(tile_v(k) + (16 * KT * wk + 32 * h) * Sh::kStrideV, Sh::kStrideV, p, h, lane);
+      __builtin_amdgcn_s_setprio(0);
       // the other tiles' turn
       if (k + 1 < k1) store(k + 1);
       if (wave == 0) note(k + 3, find(k + 3, page));
@@ -244,7 +250,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_shared_kernel(AttendAr
       }
       __syncthreads();
       write_item<FMT, DV, MT>(arguments(), w, w.group, workers, 32 * first, 32 * kGroups, (const float*)lds, ms[0], ls[0], Sh::kWK, threadIdx.x,
-                              kThreads, part, part_ml);
+                              Sh::kThreads, part, part_ml);
     }
     w.leave_open(arguments(), open, workers);
     __syncthreads();

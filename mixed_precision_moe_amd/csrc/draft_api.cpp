@@ -95,7 +95,12 @@ AttendPlan attend_plan(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows,
   p.dk = k <= 64 && v <= 64 ? 64 : k <= 128 && v <= 128 ? 128 : k <= 192 && v <= 128 ? 192 : 256;
   p.dv = p.dk == 192 ? 128 : p.dk;
   const int64_t per_seq = (rows + n_seqs - 1) / (n_seqs > 0 ? n_seqs : 1) * (q_heads / d->heads);
-  p.nt = per_seq <= 16 ? 1 : per_seq <= 32 ? 2 : per_seq <= 64 && attend_keys(p.dk) == 64 ? 4 : 8;
+  p.nt = per_seq <= 16 ? 1 : per_seq <= 32 ? 2 : 8;
+  if (p.nt == 8 && attend_keys(p.dk) == 64) {
+    // tiles of 256 rows take seven eighths of the time that tiles of 128 take for the same rows, padding included
+    const int64_t wide = (per_seq + 255) / 256 * 256, narrow = (per_seq + 127) / 128 * 128;
+    p.nt = per_seq <= 64 ? 4 : wide * 7 <= narrow * 8 ? 16 : 8;
+  }
   if (p.nt <= 2) {
     // heads side by side, unless the positions are few: one unit of all four waves then needs no join
     p.heads_log = positions <= 128 ? 0 : d->heads % 4 == 0 ? 2 : d->heads % 2 == 0 ? 1 : 0;

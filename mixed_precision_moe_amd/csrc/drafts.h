@@ -42,7 +42,7 @@ struct AttendPlan {
   uint64_t part, ml, open, totals, total;
 };
 // Workgroups of a compute unit: what their registers and LDS leave room for.
-constexpr int attend_waves(int dk, int nt) { return nt == 1 ? (dk <= 128 ? 3 : 2) : dk <= 192 ? 2 : 1; }
+constexpr int attend_waves(int dk, int nt) { return nt == 1 ? (dk <= 128 ? 3 : 2) : nt == 16 ? 1 : dk <= 192 ? 2 : 1; }
 // Positions of a tile of the shared kernel.
 constexpr int attend_keys(int dk) { return dk <= 128 ? 64 : 32; }
 int launch_attend_mxfp4(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream);

@@ -134,7 +134,7 @@ static void test_attend() {
                                             nullptr, fake<int32_t>(), 4, 1, 4, nullptr, 0, 0, 1.0f, fake(), 1 << 20, v, 0, fake(),
                                             mxfp4_cache_attend_workspace_bytes(&d, heads, rows, 1), nullptr);
           CHECK(rc == MXFP4_OK);
-          CHECK(g_plan.dk >= dim && g_plan.dv >= v && g_plan.nt >= 1 && g_plan.nt <= 8 && g_plan.workers >= 1);
+          CHECK(g_plan.dk >= dim && g_plan.dv >= v && g_plan.nt >= 1 && g_plan.nt <= 16 && g_plan.workers >= 1);
           CHECK(g_plan.total <= mxfp4_cache_attend_workspace_bytes(&d, heads, rows, 1));
           // the parts follow each other inside the workspace
           const uint64_t workers = (uint64_t)g_plan.workers * heads, part_rows = 2 * workers * 16 * g_plan.nt;
