@@ -178,28 +178,36 @@ MX_DEV int64_t lane64(int64_t v, int lane) {  // the same for the whole wave, an
   const int lo = __builtin_amdgcn_readlane((int)v, lane), hi = __builtin_amdgcn_readlane((int)(v >> 32), lane);
   return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
 }
-MX_DEV int64_t shfl64_up(int64_t v, int by) {
-  const int lo = __shfl_up((int)v, by), hi = __shfl_up((int)(v >> 32), by);
-  return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
+
+// n, and that of the lane that DPP control CTRL names, in the rows of 16 lanes of ROWS.
+template <int CTRL, int ROWS>
+MX_DEV int64_t add_lane(int64_t n) {
+  const int lo = __builtin_amdgcn_update_dpp(0, (int)n, CTRL, ROWS, 0xF, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, (int)(n >> 32), CTRL, ROWS, 0xF, false);
+  return n + (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
+}
+// Sums over the lanes up to and including each.
+MX_DEV int64_t scan_lanes(int64_t n) {
+  n = add_lane<0x111, 0xF>(n);  // from 1, 2, 4 and 8 lanes below in a row
+  n = add_lane<0x112, 0xF>(n);
+  n = add_lane<0x114, 0xF>(n);
+  n = add_lane<0x118, 0xF>(n);
+  n = add_lane<0x142, 0xA>(n);         // from the last lane of the row below
+  return add_lane<0x143, 0xC>(n);      // from lane 31
 }
 
-// Units, and tiles, of the 64 sequences from b0 on, summed up to and including each lane's.
-MX_DEV int64_t scan_lanes(int64_t n, int lane) {
-#pragma unroll
-  for (int h = 1; h < 64; h <<= 1) {
-    const int64_t o = shfl64_up(n, h);
-    if (lane >= h) n += o;
+// Of 64 sequences from b0 on: each lane's, and its units and tiles with those of the lanes before.
+template <int MT>
+struct Scan {
+  Seq s;
+  int64_t units, tiles;
+
+  MX_DEV Scan(const AttendArgs& a, int b0, int lane) : s{0, 0, 0, 0} {
+    if (b0 + lane < a.cache.n_seqs) s = sequence(a, b0 + lane);
+    tiles = scan_lanes((s.rows * a.group + MT - 1) / MT);
+    units = scan_lanes(s.rows > 0 ? seq_units<MT>(a, s) : 0);
   }
-  return n;
-}
-template <int MT>
-MX_DEV int64_t scan_units(const AttendArgs& a, int b0, int lane) {
-  return scan_lanes(b0 + lane < a.cache.n_seqs ? seq_units<MT>(a, sequence(a, b0 + lane)) : 0, lane);
-}
-template <int MT>
-MX_DEV int64_t scan_tiles(const AttendArgs& a, int b0, int lane) {
-  return scan_lanes(b0 + lane < a.cache.n_seqs ? (sequence(a, b0 + lane).rows * a.group + MT - 1) / MT : 0, lane);
-}
+};
 
 // Eight elements of a row of the result from its sums x, y and the sum of its weights.
 template <int FMT>
@@ -263,10 +271,12 @@ struct Work {
       group = blockIdx.x % groups;
       worker = blockIdx.x / groups;
     }
-    int64_t all = 0, items = 0, u, u1;
-    for (int b0 = 0; b0 < c.n_seqs; b0 += 64) {
-      all += lane64(scan_units<MT>(a, b0, lane), 63);
-      items += lane64(scan_tiles<MT>(a, b0, lane), 63);
+    Scan<MT> first(a, 0, lane);
+    int64_t all = lane64(first.units, 63), items = lane64(first.tiles, 63), u, u1;
+    for (int b0 = 64; b0 < c.n_seqs; b0 += 64) {
+      const Scan<MT> more(a, b0, lane);
+      all += lane64(more.units, 63);
+      items += lane64(more.tiles, 63);
     }
     if (threadIdx.x == 0) {
       if (!a.open_items) open[(int64_t)group * workers + worker] = Open{0, 0, 0, 0};
@@ -277,22 +287,22 @@ struct Work {
     b = 0;
     index = 0;
     int64_t item = 0;
-    for (int b0 = 0; b0 < c.n_seqs; b0 += 64) {
-      const int64_t sums = item + scan_units<MT>(a, b0, lane), tiles = index + scan_tiles<MT>(a, b0, lane);
-      const uint64_t past = __ballot(sums > u);
-      if (past) {
-        const int l = __ffsll((unsigned long long)past) - 1;
-        b = b0 + l;
-        if (l > 0) {
-          item = lane64(sums, l - 1);
-          index = (int32_t)lane64(tiles, l - 1);
-        }
-        break;
-      }
-      item = lane64(sums, 63);
-      index = (int32_t)lane64(tiles, 63);
+    uint64_t past;
+    while (!(past = __ballot(item + first.units > u))) {
+      if (b + 64 >= c.n_seqs) return false;  // not with cu_rows and start that stay
+      item += lane64(first.units, 63);
+      index += (int32_t)lane64(first.tiles, 63);
+      b += 64;
+      first = Scan<MT>(a, b, lane);
     }
-    s = sequence(a, b);
+    const int l = __ffsll((unsigned long long)past) - 1;
+    b += l;
+    if (l > 0) {
+      item += lane64(first.units, l - 1);
+      index += (int32_t)lane64(first.tiles, l - 1);
+    }
+    const auto of = [&](int32_t v) { return __builtin_amdgcn_readlane(v, l); };
+    s = Seq{of(first.s.first), of(first.s.drafts), of(first.s.rows), of(first.s.start)};
     ti.begin(a, s);
     while (item + ti.units <= u) {
       item += ti.units;
