@@ -349,9 +349,9 @@ struct Work {
   MX_DEV void leave_open(const AttendArgs& a, Open* open, int workers) const {
     if (threadIdx.x != 0 || k0 != 0) return;
     const Open o = {ti.tile, b, worker, ti.units - k1()};
-    if (a.open_items)
-      open[(int64_t)group * a.open_items + index] = o;
-    else if (o.rest > 0)
+    if (a.open_items) {
+      if (index < a.open_items) open[(int64_t)group * a.open_items + index] = o;  // there are no more with cu_rows in order
+    } else if (o.rest > 0)
       open[(int64_t)group * workers + worker] = o;
   }
 };
@@ -366,14 +366,42 @@ MX_DEV float score_scale(const AttendArgs& a) {
   return fmaxf(s * 1.44269504f / (FMT == MXFP4_FMT_NVFP4 ? a.cache.plane[0].gs : 1.0f), 1e-38f);
 }
 
-// Eight elements of a row of q: the scale's sign goes to them, and with a scale of 0 they are 0.
-MX_DEV bf16x8_t query8(const AttendArgs& a, const uint16_t* src) {
-  u32x4_t x = *reinterpret_cast<const u32x4_t*>(src);
-  const uint32_t keep = a.scale == 0.0f ? 0u : ~0u, sign = a.scale < 0.0f ? 0x80008000u : 0u;
+// A wave's 16 NT rows of q, a lane's elements first(i) to first(i) + 7 of them.  `load` asks for places that are there
+// throughout, so that no wait for what was asked for before waits for q too; `finish` waits.
+template <int NT, int STEPS>
+struct Query {
+  bf16x8_t q[NT][STEPS];
+  int32_t draft[NT];  // of this lane's columns; -1: no such row
+
+  template <typename F>
+  MX_DEV void load(const AttendArgs& a, const Seq& s, int32_t row0, int g, F first) {
+    const CachePlane& query = a.cache.plane[0];
 #pragma unroll
-  for (int j = 0; j < 4; j++) x[j] = (x[j] & keep) ^ sign;
-  return __builtin_bit_cast(bf16x8_t, x);
-}
+    for (int n = 0; n < NT; n++) {
+      const int32_t r = row0 + 16 * n + (threadIdx.x & 15), d = (uint32_t)r / (uint32_t)a.group;
+      draft[n] = d < s.rows ? d : -1;
+      const uint16_t* src = (const uint16_t*)query.rows + (int64_t)(s.first + min(d, s.rows - 1)) * query.ldt +
+                            (g * a.group + (r - d * a.group)) * query.ldh;
+#pragma unroll
+      for (int i = 0; i < STEPS; i++) q[n][i] = *reinterpret_cast<const bf16x8_t*>(src + (first(i) < query.dim ? first(i) : 0));
+    }
+  }
+  // The scale's sign goes to q, and with a scale of 0 it is 0.
+  template <typename F>
+  MX_DEV void finish(const AttendArgs& a, F first) {
+    const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+      for (int i = 0; i < STEPS; i++) {
+        const uint32_t keep = draft[n] >= 0 && first(i) < a.cache.plane[0].dim && a.scale != 0.0f ? ~0u : 0u;
+        u32x4_t x = __builtin_bit_cast(u32x4_t, q[n][i]);
+#pragma unroll
+        for (int j = 0; j < 4; j++) x[j] = (x[j] & keep) ^ (sign & keep);
+        q[n][i] = __builtin_bit_cast(bf16x8_t, x);
+      }
+  }
+};
 
 // The sums of a wave's 16 NT rows, of their weights too; the exponents' subtrahend m, and the score from which on it is
 // raised.

@@ -119,30 +119,14 @@ __global__ __launch_bounds__(64 * (WR > kWaves ? WR : kWaves), WAVES) void atten
     w.settle();
     const Seq& s = w.s;
     const int32_t k0 = w.k0, k1 = w.k1(), end = w.ti.end;
-    bf16x8_t q[NT][DK / 32];
-    int32_t draft[NT];  // -1: no such row
     const AttendArgs a = arguments();
-    const CachePlane& pk = a.cache.plane[0];
-#pragma unroll
-    for (int n = 0; n < NT; n++) {
-      const int32_t r = w.ti.tile * MT + 32 * wr + 16 * n + col;
-      const int32_t d = (uint32_t)r / (uint32_t)a.group;
-      draft[n] = d < s.rows ? d : -1;
-      const uint16_t* src = (const uint16_t*)pk.rows + (int64_t)(s.first + d) * pk.ldt + (w.group * a.group + (r - d * a.group)) * pk.ldh;
-#pragma unroll
-      for (int i = 0; i < DK / 32; i++) {
-        const int e = 32 * i + 8 * kg;
-        q[n][i] = __builtin_bit_cast(bf16x8_t, u32x4_t{0, 0, 0, 0});
-        if (draft[n] >= 0 && e < pk.dim) q[n][i] = query8(a, src + e);
-      }
-    }
     // the positions before this one are seen by all of the wave's rows: with a mask the context, else the first row's drafts too
     const int32_t seen = (int32_t)min((int64_t)s.start + (a.mask ? 0 : (uint32_t)(w.ti.tile * MT + 32 * wr) / (uint32_t)a.group + 1), (int64_t)INT32_MAX);
     Rows<NT, DV / 16> rows;
     rows.clear();
 
     // the page of this lane's position of tile k, and that position's vector
-    const int32_t* table = a.cache.table + (int64_t)w.b * a.cache.ld_table;
+    const int32_t* const table = a.cache.table + (int64_t)w.b * a.cache.ld_table;
     const auto look_up = [&](int32_t k) -> int32_t {
       return end > 0 ? table[a.page_of(min((uint32_t)k * KEYS + lane, (uint32_t)end - 1))] : -1;
     };
@@ -174,10 +158,17 @@ __global__ __launch_bounds__(64 * (WR > kWaves ? WR : kWaves), WAVES) void atten
     };
 
     if (threadIdx.x < 8) (&bad[0][0])[threadIdx.x] = 0;
-    if (wave < 3) note(k0 + wave, find(k0 + wave, look_up(k0 + wave)));
+    const int32_t first_page = look_up(k0 + min(wave, 2));
     int32_t page = look_up(k0 + 3);
+    const auto element = [&](int i) { return 32 * i + 8 * kg; };
+    Query<NT, DK / 32> query;
+    query.load(a, s, w.ti.tile * MT + 32 * wr, w.group, element);
+    if (wave < 3) note(k0 + wave, find(k0 + wave, first_page));
     __syncthreads();
     load(k0);
+    query.finish(a, element);
+    const auto& q = query.q;
+    const auto& draft = query.draft;
     store(k0);
     if (k0 + 1 < k1) load(k0 + 1);
     __syncthreads();

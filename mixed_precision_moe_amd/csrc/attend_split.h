@@ -177,26 +177,16 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArg
       found = find(k0);
       next = find(k0 + 1);
     }
-    // the rows of this lane's columns
-    bf16x8_t q[NT][Sh::kSteps];
-    int32_t draft[NT];  // -1: no such row
-    {
-      const AttendArgs a = arguments();
-      const CachePlane& query = a.cache.plane[0];
-#pragma unroll
-      for (int n = 0; n < NT; n++) {
-        const int32_t r = w.ti.tile * MT + 16 * n + col;
-        const int32_t d = (uint32_t)r / (uint32_t)a.group;
-        draft[n] = d < s.rows ? d : -1;
-        const uint16_t* src = (const uint16_t*)query.rows + (int64_t)(s.first + d) * query.ldt + (g * a.group + (r - d * a.group)) * query.ldh;
-#pragma unroll
-        for (int i = 0; i < Sh::kSteps; i++) {
-          const int e = kg * Sh::kQuarter + 8 * i;
-          q[n][i] = __builtin_bit_cast(bf16x8_t, u32x4_t{0, 0, 0, 0});
-          if (draft[n] >= 0 && e < k_dim) q[n][i] = query8(a, src + e);
-        }
-      }
+    const auto element = [&](int i) { return kg * Sh::kQuarter + 8 * i; };
+    Query<NT, Sh::kSteps> query;
+    query.load(arguments(), s, w.ti.tile * MT, g, element);
+    if (end > 0) {
+      load_k(k0, found);
+      load_v(k0, found);
     }
+    query.finish(arguments(), element);
+    const auto& q = query.q;
+    const auto& draft = query.draft;
     Rows<NT, Sh::kVT> rows;
     rows.clear();
 
@@ -289,8 +279,6 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArg
       next = after;
     };
     if (end > 0) {
-      load_k(k0, found);
-      load_v(k0, found);
       for (int32_t k = k0; k + 1 < k1; k++) step(k, std::true_type{});
       step(k1 - 1, std::false_type{});
     }
