@@ -11,11 +11,10 @@
 
 namespace {
 
-template <int FMT, int DK, int DV, int WR, int KEYS>
+template <int FMT, int DK, int DV, int W, int WR, int KEYS>
 struct Shared {
-  static constexpr int kW = WR > kWaves ? WR : kWaves;
-  static constexpr int kThreads = 64 * kW;
-  static constexpr int kWK = kW / WR;           // groups of waves that share the positions
+  static constexpr int kThreads = 64 * W;
+  static constexpr int kWK = W / WR;           // groups of waves that share the positions
   static constexpr int kRows = 32 * WR;
   static constexpr int kKT = KEYS / kWK / 16;   // tiles of 16 positions of a wave
   static constexpr int kElems = 16 * kPerByte<FMT>;
@@ -93,11 +92,11 @@ struct Pieces {
   }
 };
 
-template <int FMT, int DK, int DV, int WR, int KEYS, int WAVES>
-__global__ __launch_bounds__(64 * (WR > kWaves ? WR : kWaves), WAVES) void attend_shared_kernel(AttendArgs given, float* __restrict__ part,
+template <int FMT, int DK, int DV, int W, int WR, int KEYS, int WAVES>
+__global__ __launch_bounds__(64 * W, WAVES) void attend_shared_kernel(AttendArgs given, float* __restrict__ part,
                                                                         float2* __restrict__ part_ml,
                                                                         Open* __restrict__ open, Totals* __restrict__ totals, int workers) {
-  using Sh = Shared<FMT, DK, DV, WR, KEYS>;
+  using Sh = Shared<FMT, DK, DV, W, WR, KEYS>;
   constexpr int MT = Sh::kRows, NT = 2, KT = Sh::kKT;
   static_assert(KT % 2 == 0 && KEYS <= 64, "32 positions a matrix instruction, and 64 a lookup");
   constexpr int kBytes = 2 * Sh::kTileBytes;

@@ -96,10 +96,12 @@ AttendPlan attend_plan(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows,
   p.dv = p.dk == 192 ? 128 : p.dk;
   const int64_t per_seq = (rows + n_seqs - 1) / (n_seqs > 0 ? n_seqs : 1) * (q_heads / d->heads);
   p.nt = per_seq <= 16 ? 1 : per_seq <= 32 ? 2 : 8;
-  if (p.nt == 8 && attend_keys(p.dk) == 64) {
-    // tiles of 256 rows take seven eighths of the time that tiles of 128 take for the same rows, padding included
+  if (p.nt == 8 && p.dk <= 192) {
+    // Tiles of 256 rows read and dequantize for twice the rows, and leave twice as much to join.  4 sequences of 4096
+    // positions, MXFP4, us with tiles of 128 and 256 rows, by rows a key head; keys of 128: 256: 33, 42; 512: 44, 44;
+    // 8192: 337, 333; of 192: 35, 44; 49, 51; 499, 379; of 64: 29, 34; 36, 34; 287, 245.
     const int64_t wide = (per_seq + 255) / 256 * 256, narrow = (per_seq + 127) / 128 * 128;
-    p.nt = per_seq <= 64 ? 4 : wide * 7 <= narrow * 8 ? 16 : 8;
+    p.nt = per_seq <= 64 && p.dk <= 128 ? 4 : per_seq > 512 && wide * 8 <= narrow * 9 ? 16 : 8;
   }
   if (p.nt <= 2) {
     // heads side by side, unless the positions are few: one unit of all four waves then needs no join
@@ -108,7 +110,7 @@ AttendPlan attend_plan(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows,
   } else {
     p.unit_log = attend_keys(p.dk) == 64 ? 6 : 5;
   }
-  const int64_t groups = d->heads >> p.heads_log, fill = (int64_t)kCus * attend_waves(p.dk, p.nt) / groups;
+  const int64_t groups = d->heads >> p.heads_log, fill = (int64_t)kCus * attend_fit(p.dk, p.nt) / groups;
   p.workers = (int32_t)(fill < 1 ? 1 : fill < 8 ? fill : fill & ~int64_t(7));  // as many on each XCD
   uint64_t at = 0;
   auto take = [&](uint64_t bytes) { uint64_t o = at; at = up256(at + bytes); return o; };
