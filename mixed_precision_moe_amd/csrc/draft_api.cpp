@@ -33,7 +33,14 @@ int move_planes(MoveArgs& a, const mxfp4_cache_dims* d, void* k_q, void* k_s, vo
   void* base[4] = {k_q, k_s, v_q, v_s};
   const int64_t row[4] = {h * (d->k_dim / per), h * (d->k_dim / g), h * (d->v_dim / per), h * (d->v_dim / g)};
   a.planes = two ? 4 : 2;
-  for (int i = 0; i < a.planes; i++) a.plane[i] = BytePlane{(uint8_t*)base[i], row[i], unit_of(base[i], row[i])};
+  int64_t units = 0;
+  for (int i = 0; i < 4; i++) {
+    if (i < a.planes) {
+      a.plane[i] = BytePlane{(uint8_t*)base[i], row[i], unit_of(base[i], row[i])};
+      units += row[i] / a.plane[i].unit;
+    }
+    a.ends[i] = units;
+  }
   a.num_pages = d->num_pages;
   a.page_size = d->page_size;
   return MXFP4_OK;

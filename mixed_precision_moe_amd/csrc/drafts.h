@@ -62,6 +62,7 @@ struct BytePlane {
 };
 struct MoveArgs {
   BytePlane plane[4];
+  int64_t ends[4];  // units of a token up to and with each plane
   int64_t num_pages, ld_table, ld_path;
   const int32_t *start, *path, *table;
   int32_t* lengths;

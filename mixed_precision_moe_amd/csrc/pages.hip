@@ -18,28 +18,46 @@ constexpr int kBatch = 8;        // units on their way in each thread
 
 typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
 
-// A unit of 1 to 16 bytes.
-template <typename F>
-MX_DEV void with_unit(int unit, F f) {
-  if (unit == 16) f(u32x4_t{});
-  else if (unit == 8) f((uint64_t)0);
-  else if (unit == 4) f((uint32_t)0);
-  else if (unit == 2) f((uint16_t)0);
-  else f((uint8_t)0);
-}
+// Units of a token in the planes before plane p.
+MX_DEV int64_t units_before(const MoveArgs& a, int p) { return p == 0 ? 0 : p == 1 ? a.ends[0] : p == 2 ? a.ends[1] : p == 3 ? a.ends[2] : a.ends[3]; }
 
 MX_DEV int64_t slot_at(const MoveArgs& a, const int32_t* row, int64_t pos) {
   if (pos < 0) return -1;
-  const int64_t p = pos / a.page_size;
-  if (p >= a.max_pages) return -1;
+  const uint32_t p = (uint32_t)pos / (uint32_t)a.page_size;  // start and place in the path: below 2^32
+  if (p >= (uint32_t)a.max_pages) return -1;
   const int64_t page = row[p];
   if (page < 0 || page >= a.num_pages) return -1;
-  return page * a.page_size + (pos - p * a.page_size);
+  return page * a.page_size + ((uint32_t)pos - p * (uint32_t)a.page_size);
 }
 
-// blockIdx.x: sequence, blockIdx.y: a stripe of each token's units.  A thread owns its units of all moved tokens and goes
-// through them in path order: the path increases, so a token's source never lies where an earlier token went, and
-// each batch is read before it is written.
+// A unit of `unit` bytes at the head of 16; WIDE: all planes' are 16 bytes.
+template <bool WIDE>
+MX_DEV u32x4_t get_unit(const uint8_t* p, int unit) {
+  u32x4_t v = {0, 0, 0, 0};
+  if (WIDE || unit == 16) return *(const u32x4_t*)p;
+  if (unit == 8) {
+    const uint64_t x = *(const uint64_t*)p;
+    v[0] = (uint32_t)x;
+    v[1] = (uint32_t)(x >> 32);
+  } else {
+    v[0] = unit == 4 ? *(const uint32_t*)p : unit == 2 ? *(const uint16_t*)p : *p;
+  }
+  return v;
+}
+template <bool WIDE>
+MX_DEV void put_unit(uint8_t* p, int unit, u32x4_t v) {
+  if (WIDE || unit == 16) *(u32x4_t*)p = v;
+  else if (unit == 8) *(uint64_t*)p = (uint64_t)v[1] << 32 | v[0];
+  else if (unit == 4) *(uint32_t*)p = v[0];
+  else if (unit == 2) *(uint16_t*)p = (uint16_t)v[0];
+  else *p = (uint8_t)v[0];
+}
+
+// blockIdx.x: sequence, blockIdx.y: a stripe of each token's units, those of all planes in a row.  The moved tokens' units
+// are dealt to the threads in path order, kBatch each a round, and all of a round are read before any is written.  Where an
+// earlier token goes, no later one comes from (the path increases, and is never behind its place), so nothing is read
+// that another round has written.
+template <bool WIDE>
 __global__ __launch_bounds__(kThreads) void compact_kernel(MoveArgs a) {
   __shared__ int64_t from[kThreads], to[kThreads];
   __shared__ int32_t in_wave[kThreads / 64], stop;
@@ -82,23 +100,41 @@ __global__ __launch_bounds__(kThreads) void compact_kernel(MoveArgs a) {
         to[at] = dst;
       }
       __syncthreads();
-      for (int p = 0; p < a.planes; p++) {
-        with_unit(a.plane[p].unit, [&](auto zero) {
-          using U = decltype(zero);
-          const int64_t units = a.plane[p].row / (int)sizeof(U);
-          for (int64_t u = (int64_t)blockIdx.y * kThreads + t; u < units; u += (int64_t)gridDim.y * kThreads) {
-            U* base = (U*)a.plane[p].base + u;
-            for (int j = 0; j < total; j += kBatch) {
-              U v[kBatch];
+      const int64_t u0 = units_before(a, 4) * blockIdx.y / gridDim.y;
+      const uint32_t units = (uint32_t)(units_before(a, 4) * (blockIdx.y + 1) / gridDim.y - u0), count = units * (uint32_t)total;
+      // a thread's unit of a token, and what a step of all threads adds to them
+      uint32_t token = t / units, u = t - token * units;
+      const uint32_t step_token = kThreads / units, step_u = kThreads - step_token * units;
+      const auto step = [&](uint32_t& token, uint32_t& u) {
+        token += step_token;
+        u += step_u;
+        if (u >= units) u -= units, token++;
+      };
+      const auto place = [&](const int64_t* slots, uint32_t token, uint32_t u, int& unit) {
+        int64_t at = u0 + u;
+        const int p = (at >= units_before(a, 1)) + (at >= units_before(a, 2)) + (at >= units_before(a, 3));
+        at -= units_before(a, p);
+        unit = a.plane[p].unit;
+        return a.plane[p].base + slots[token] * a.plane[p].row + at * unit;
+      };
+      for (uint32_t first = 0; first < count; first += kBatch * kThreads) {
+        u32x4_t v[kBatch];
+        uint32_t to_token = token, to_u = u;
+        int unit;
 #pragma unroll
-              for (int k = 0; k < kBatch; k++)
-                if (j + k < total) v[k] = base[from[j + k] * units];
+        for (int k = 0; k < kBatch; k++) {
+          if (first + k * kThreads + t < count) v[k] = get_unit<WIDE>(place(from, token, u, unit), unit);
+          step(token, u);
+        }
+        __syncthreads();
 #pragma unroll
-              for (int k = 0; k < kBatch; k++)
-                if (j + k < total) base[to[j + k] * units] = v[k];
-            }
+        for (int k = 0; k < kBatch; k++) {
+          if (first + k * kThreads + t < count) {
+            uint8_t* const at = place(to, to_token, to_u, unit);
+            put_unit<WIDE>(at, unit, v[k]);
           }
-        });
+          step(to_token, to_u);
+        }
       }
       accepted += n;
       __syncthreads();
@@ -108,29 +144,32 @@ __global__ __launch_bounds__(kThreads) void compact_kernel(MoveArgs a) {
   }
 }
 
-// blockIdx.x: pair, blockIdx.y: a stripe of the pages' units.
-__global__ __launch_bounds__(kThreads) void copy_pages_kernel(MoveArgs a) {
-  for (int i = blockIdx.x; i < a.n; i += gridDim.x) {
-    const int64_t src = a.src[i], dst = a.dst[i];
-    if (src < 0 || src >= a.num_pages || dst < 0 || dst >= a.num_pages || src == dst) continue;
-    const int64_t rows = a.rows ? min(a.rows[i], a.page_size) : a.page_size;
-    for (int p = 0; p < a.planes; p++) {
-      with_unit(a.plane[p].unit, [&](auto zero) {
-        using U = decltype(zero);
-        const int64_t per = a.plane[p].row / (int)sizeof(U), units = rows * per, page = a.page_size * per;
-        const U* from = (const U*)a.plane[p].base + src * page;
-        U* to = (U*)a.plane[p].base + dst * page;
-        const int64_t step = (int64_t)gridDim.y * kThreads;
-        for (int64_t u = (int64_t)blockIdx.y * kThreads + threadIdx.x; u < units; u += kBatch * step) {
-          U v[kBatch];
+struct Stripes {
+  int64_t ends[4];  // up to and with each plane
+};
+
+// blockIdx.x: pair, blockIdx.y: a stripe of a page's units, kBatch a thread; those of all planes in a row.
+template <bool WIDE>
+__global__ __launch_bounds__(kThreads) void copy_pages_kernel(MoveArgs a, Stripes stripes) {
+  const int64_t* const e = stripes.ends;
+  for (int64_t y = blockIdx.y; y < e[3]; y += gridDim.y) {
+    const int p = (y >= e[0]) + (y >= e[1]) + (y >= e[2]);
+    const BytePlane plane = a.plane[p];
+    const int64_t first = p == 0 ? 0 : p == 1 ? e[0] : p == 2 ? e[1] : e[2];
+    const int64_t per = plane.row / plane.unit, u = (y - first) * kThreads * kBatch + threadIdx.x;
+    for (int i = blockIdx.x; i < a.n; i += gridDim.x) {
+      const int64_t src = a.src[i], dst = a.dst[i];
+      if (src < 0 || src >= a.num_pages || dst < 0 || dst >= a.num_pages || src == dst) continue;
+      const int64_t units = (a.rows ? min(a.rows[i], a.page_size) : a.page_size) * per;
+      const uint8_t* from = plane.base + src * a.page_size * plane.row + u * plane.unit;
+      uint8_t* to = plane.base + dst * a.page_size * plane.row + u * plane.unit;
+      u32x4_t v[kBatch];
 #pragma unroll
-          for (int k = 0; k < kBatch; k++)
-            if (u + k * step < units) v[k] = from[u + k * step];
+      for (int k = 0; k < kBatch; k++)
+        if (u + k * kThreads < units) v[k] = get_unit<WIDE>(from + (int64_t)k * kThreads * plane.unit, plane.unit);
 #pragma unroll
-          for (int k = 0; k < kBatch; k++)
-            if (u + k * step < units) to[u + k * step] = v[k];
-        }
-      });
+      for (int k = 0; k < kBatch; k++)
+        if (u + k * kThreads < units) put_unit<WIDE>(to + (int64_t)k * kThreads * plane.unit, plane.unit, v[k]);
     }
   }
 }
@@ -346,25 +385,38 @@ __global__ __launch_bounds__(kPool) void pool_take_kernel(PoolArgs a, Items it) 
 
 int status() { return hipGetLastError() == hipSuccess ? MXFP4_OK : MXFP4_ERR_DEVICE; }
 
-// Workgroups along each token or page: enough of them for the plane with the most units, at most `most`.
-unsigned stripes(const MoveArgs& a, int64_t tokens, int64_t most) {
-  int64_t units = 1;
-  for (int p = 0; p < a.planes; p++) units = max(units, tokens * (a.plane[p].row / a.plane[p].unit));
-  const int64_t n = (units + kThreads - 1) / kThreads;
-  return (unsigned)(n < most ? n : most);
+bool wide(const MoveArgs& a) {
+  for (int p = 0; p < a.planes; p++)
+    if (a.plane[p].unit != 16) return false;
+  return true;
 }
 
 }  // namespace
 
 int launch_compact(const MoveArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)min(a.n_seqs, 65536), stripes(a, 1, 64));
-  hipLaunchKernelGGL(compact_kernel, grid, dim3(kThreads), 0, stream, a);
+  // stripes that take one round if the whole path moves, as long as the sequences leave room for more workgroups
+  const int64_t units = a.ends[3], round = kThreads * kBatch, moves = min(a.path_cols, kThreads);
+  const int64_t n = max(min(min((units * moves + round - 1) / round, units), int64_t(4096 / a.n_seqs)), int64_t(1));
+  const dim3 grid((unsigned)min(a.n_seqs, 65536), (unsigned)n);
+  if (wide(a))
+    hipLaunchKernelGGL(compact_kernel<true>, grid, dim3(kThreads), 0, stream, a);
+  else
+    hipLaunchKernelGGL(compact_kernel<false>, grid, dim3(kThreads), 0, stream, a);
   return status();
 }
 
 int launch_copy_pages(const MoveArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)min(a.n, 65536), stripes(a, a.page_size, 16));
-  hipLaunchKernelGGL(copy_pages_kernel, grid, dim3(kThreads), 0, stream, a);
+  Stripes stripes;
+  int64_t n = 0;
+  for (int p = 0; p < 4; p++) {
+    if (p < a.planes) n += ((int64_t)a.page_size * (a.plane[p].row / a.plane[p].unit) + kThreads * kBatch - 1) / (kThreads * kBatch);
+    stripes.ends[p] = n;
+  }
+  const dim3 grid((unsigned)min(a.n, 65536), (unsigned)min(n, int64_t(65535)));
+  if (wide(a))
+    hipLaunchKernelGGL(copy_pages_kernel<true>, grid, dim3(kThreads), 0, stream, a, stripes);
+  else
+    hipLaunchKernelGGL(copy_pages_kernel<false>, grid, dim3(kThreads), 0, stream, a, stripes);
   return status();
 }
 
