@@ -508,15 +508,15 @@ class PagePool:
         nws = _pool_workspace(self._pages, n, P)
         if nws == 0:
             raise ValueError("invalid page pool arguments")
-        ws = torch.empty(nws, dtype=torch.uint8, device=self._device)
-        # copies [3, n] and missing
-        made = torch.empty(3 * n + 1, dtype=torch.int32, device=self._device)
-        copies = made.data_ptr()
+        # the workspace and copies [3, n] behind it (a whole number of 256 bytes)
+        ws = torch.empty(nws + 12 * n, dtype=torch.uint8, device=self._device)
+        missing = torch.empty((), dtype=torch.int32, device=self._device)
+        copies = ws.data_ptr() + nws
         _call(self._gpu, fn, self._pages, self._page_size, self._refs.data_ptr(), page_table.data_ptr(), ld, B, P, *lists,
-              copies, copies + 12 * n, ws.data_ptr(), nws)
+              copies, missing.data_ptr(), copies - nws, nws)
         for c in self._caches:
             _call(self._gpu, "mxfp4_cache_copy_pages", c._dref, copies, copies + 4 * n, copies + 8 * n, n, *c._memory())
-        return made[3 * n]
+        return missing
 
     def resize(self, page_table, lengths):
         """Row b of page_table (int32 [B, pages]) then holds the pages of lengths[b] tokens (int32 [B]; negative: the row

@@ -103,25 +103,28 @@ class Rotary:
         _need(self._offset + self._dim <= dim, "the turned part must lie inside head_dim")
         _need(positions.dtype == torch.int32 and positions.shape == (rows,) and positions.is_contiguous(),
               "positions: contiguous int32 [rows]")
-        q_out = torch.empty((rows, heads, dim), dtype=dtype, device=q.device) if out is None else out[0]
-        args = [*_vectors(q, "q", heads, dim), heads, *_vectors(q_out, "q", heads, dim)]
-        if k is None:
-            args += [None, 0, 0, 0, None, 0, 0]
-            made = (q_out,)
-        else:
+        q_args, k_args, k_heads = _vectors(q, "q", heads, dim), (None, 0, 0), 0
+        if k is not None:
             k_heads = k.shape[1]
             _need_int32(k_heads)
             _need(k.dtype == dtype and k.shape[0] == rows, "q and k must have the same rows and dtype")
             _need(k_heads > 0, "k must have a head")
-            k_out = torch.empty((rows, k_heads, dim), dtype=dtype, device=q.device) if out is None else out[1]
-            args += [*_vectors(k, "k", k_heads, dim), k_heads, *_vectors(k_out, "k", k_heads, dim)]
-            made = (q_out, k_out)
+            k_args = _vectors(k, "k", k_heads, dim)
+        if out is None:
+            q_out = torch.empty((rows, heads, dim), dtype=dtype, device=q.device)
+            made, q_to, k_to = (q_out,), (q_out.data_ptr(), heads * dim, dim), (None, 0, 0)
+            if k is not None:
+                k_out = torch.empty((rows, k_heads, dim), dtype=dtype, device=q.device)
+                made, k_to = (q_out, k_out), (k_out.data_ptr(), k_heads * dim, dim)
+        else:
+            made, q_to, k_to = out, q_args, k_args
         _call(gpu, "mxfp4_rotary", self._turns.data_ptr(), positions.data_ptr(), rows, dim, self._dim, self._offset,
-              self._interleaved, self._magnitude, 1 if inverse else 0, 1 if dtype == torch.float32 else 0, *args)
+              self._interleaved, self._magnitude, 1 if inverse else 0, 1 if dtype == torch.float32 else 0, *q_args, heads,
+              *q_to, *k_args, k_heads, *k_to)
         return made
 
     def _turn(self, tensors, positions, inverse):
-        if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
+        if torch.is_grad_enabled() and (tensors[0].requires_grad or tensors[-1].requires_grad):
             return _Rotary.apply(self, inverse, positions, *tensors)
         return self._apply(tensors, positions, inverse)
 

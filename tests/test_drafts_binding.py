@@ -86,7 +86,7 @@ def test_a_pool_copies_in_all_its_caches(calls):
     assert (f0, f1, f2) == ("mxfp4_pool_resize", "mxfp4_cache_copy_pages", "mxfp4_cache_copy_pages")
     assert r[:2] == (4, 8) and r[2] == pool.refs.data_ptr() and r[3:7] == (table.data_ptr(), 5, 3, 5)
     copies = r[8]
-    assert r[9] == copies + 36 == missing.data_ptr() and missing.shape == ()
+    assert r[9] == missing.data_ptr() and missing.shape == () and copies == r[10] + r[11]
     assert x[1:5] == y[1:5] == (copies, copies + 12, copies + 24, 3)
     assert x[5] == a.k_q.data_ptr() and y[5] == b.k_q.data_ptr() and y[7] is None
     with pytest.raises(AttributeError):
