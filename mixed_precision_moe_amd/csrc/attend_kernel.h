@@ -125,12 +125,13 @@ int launch_dims(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream
                                                            : attend_split_kernel<FMT, DK, DV, 2, attend_waves(DK, 2), false>);
   constexpr int KEYS = attend_keys(DK);
   if constexpr (DK <= 128)
-    if (p.nt == 4) return launch_both<FMT, DV, 4>(a, p, ws, stream, attend_shared_kernel<FMT, DK, DV, 4, 2, KEYS, attend_waves(DK, 4)>);
+    if (p.nt == 4) return launch_both<FMT, DV, 4>(a, p, ws, stream, attend_shared_kernel<FMT, DK, DV, 2, 4, 2, KEYS, attend_waves(DK, 4)>);
   constexpr int W8 = attend_size(DK, 8), W16 = attend_size(DK, 16);
   if constexpr (DK <= 192)
     if (p.nt == 16)
-      return launch_both<FMT, DV, 16>(a, p, ws, stream, attend_shared_kernel<FMT, DK, DV, W16, 8, KEYS, attend_waves(DK, 16)>, 64 * W16);
-  return launch_both<FMT, DV, 8>(a, p, ws, stream, attend_shared_kernel<FMT, DK, DV, W8, 4, KEYS, attend_waves(DK, 8)>, 64 * W8);
+      return launch_both<FMT, DV, 16>(a, p, ws, stream, attend_shared_kernel<FMT, DK, DV, 2, W16, 8, KEYS, attend_waves(DK, 16)>, 64 * W16);
+  constexpr int NT = attend_columns(DK);
+  return launch_both<FMT, DV, 8>(a, p, ws, stream, attend_shared_kernel<FMT, DK, DV, NT, W8, 8 / NT, KEYS, attend_waves(DK, 8)>, 64 * W8);
 }
 
 template <int FMT>

@@ -11,11 +11,11 @@
 
 namespace {
 
-template <int FMT, int DK, int DV, int W, int WR, int KEYS>
+template <int FMT, int DK, int DV, int NT, int W, int WR, int KEYS>
 struct Shared {
   static constexpr int kThreads = 64 * W;
   static constexpr int kWK = W / WR;           // groups of waves that share the positions
-  static constexpr int kRows = 32 * WR;
+  static constexpr int kRows = 16 * NT * WR;
   static constexpr int kKT = KEYS / kWK / 16;   // tiles of 16 positions of a wave
   static constexpr int kElems = 16 * kPerByte<FMT>;
   static constexpr int kScales = kElems / kBlock<FMT> ? kElems / kBlock<FMT> : 1;
@@ -92,16 +92,16 @@ struct Pieces {
   }
 };
 
-template <int FMT, int DK, int DV, int W, int WR, int KEYS, int WAVES>
+template <int FMT, int DK, int DV, int NT, int W, int WR, int KEYS, int WAVES>
 __global__ __launch_bounds__(64 * W, WAVES) void attend_shared_kernel(AttendArgs given, float* __restrict__ part,
                                                                         float2* __restrict__ part_ml,
                                                                         Open* __restrict__ open, Totals* __restrict__ totals, int workers) {
-  using Sh = Shared<FMT, DK, DV, W, WR, KEYS>;
-  constexpr int MT = Sh::kRows, NT = 2, KT = Sh::kKT;
+  using Sh = Shared<FMT, DK, DV, NT, W, WR, KEYS>;
+  constexpr int MT = Sh::kRows, R = 16 * NT, KT = Sh::kKT;
   static_assert(KT % 2 == 0 && KEYS <= 64, "32 positions a matrix instruction, and 64 a lookup");
   constexpr int kBytes = 2 * Sh::kTileBytes;
   // the sums take the place of the tiles, as many waves' rows at a time as fit
-  constexpr int kFit = kBytes / (32 * (DV + 4) * 4), kGroups = kFit >= WR ? WR : kFit >= 4 ? 4 : kFit >= 2 ? 2 : 1;
+  constexpr int kFit = kBytes / (R * (DV + 4) * 4), kGroups = kFit >= WR ? WR : kFit >= 4 ? 4 : kFit >= 2 ? 2 : 1;
   static_assert(kFit > 0, "a wave's rows at least");
   __shared__ __attribute__((aligned(16))) uint8_t lds[kBytes];
   __shared__ int64_t vectors[4][KEYS];
@@ -120,7 +120,7 @@ __global__ __launch_bounds__(64 * W, WAVES) void attend_shared_kernel(AttendArgs
     const int32_t k0 = w.k0, k1 = w.k1(), end = w.ti.end;
     const AttendArgs a = arguments();
     // the positions before this one are seen by all of the wave's rows: with a mask the context, else the first row's drafts too
-    const int32_t seen = (int32_t)min((int64_t)s.start + (a.mask ? 0 : (uint32_t)(w.ti.tile * MT + 32 * wr) / (uint32_t)a.group + 1), (int64_t)INT32_MAX);
+    const int32_t seen = (int32_t)min((int64_t)s.start + (a.mask ? 0 : (uint32_t)(w.ti.tile * MT + R * wr) / (uint32_t)a.group + 1), (int64_t)INT32_MAX);
     Rows<NT, DV / 16> rows;
     rows.clear();
 
@@ -161,7 +161,7 @@ __global__ __launch_bounds__(64 * W, WAVES) void attend_shared_kernel(AttendArgs
     int32_t page = look_up(k0 + 3);
     const auto element = [&](int i) { return 32 * i + 8 * kg; };
     Query<NT, DK / 32> query;
-    query.load(a, s, w.ti.tile * MT + 32 * wr, w.group, element);
+    query.load(a, s, w.ti.tile * MT + R * wr, w.group, element);
     if (wave < 3) note(k0 + wave, find(k0 + wave, first_page));
     __syncthreads();
     load(k0);
@@ -222,8 +222,8 @@ __global__ __launch_bounds__(64 * W, WAVES) void attend_shared_kernel(AttendArgs
 #pragma unroll
     for (int n = 0; n < NT; n++)
       if (kg == 0) {
-        ms[wk][32 * wr + 16 * n + col] = rows.m[n];
-        ls[wk][32 * wr + 16 * n + col] = rows.l[n][0];
+        ms[wk][R * wr + 16 * n + col] = rows.m[n];
+        ls[wk][R * wr + 16 * n + col] = rows.l[n][0];
       }
     for (int first = 0; first < WR; first += kGroups) {
       for (int x = 0; x < Sh::kWK; x++) {
@@ -231,15 +231,15 @@ __global__ __launch_bounds__(64 * W, WAVES) void attend_shared_kernel(AttendArgs
         if (x != wk || wr < first || wr >= first + kGroups) continue;
 #pragma unroll
         for (int n = 0; n < NT; n++) {
-          const int r = 32 * wr + 16 * n;
+          const int r = R * wr + 16 * n;
           float top = ms[0][r + col];
 #pragma unroll
           for (int y = 1; y < Sh::kWK; y++) top = fmaxf(top, ms[y][r + col]);
-          rows.join(n, (float*)lds + (r - 32 * first) * (DV + 4), DV + 4, top, x == 0, lane);
+          rows.join(n, (float*)lds + (r - R * first) * (DV + 4), DV + 4, top, x == 0, lane);
         }
       }
       __syncthreads();
-      write_item<FMT, DV, MT>(arguments(), w, w.group, workers, 32 * first, 32 * kGroups, (const float*)lds, ms[0], ls[0], Sh::kWK, threadIdx.x,
+      write_item<FMT, DV, MT>(arguments(), w, w.group, workers, R * first, R * kGroups, (const float*)lds, ms[0], ls[0], Sh::kWK, threadIdx.x,
                               Sh::kThreads, part, part_ml);
     }
     w.leave_open(arguments(), open, workers);

@@ -45,11 +45,13 @@ struct AttendPlan {
 // With keys of 192 elements eight waves share a tile of 64 positions: 12 sequences with 264 rows a key head and 5000
 // positions, NVFP4, took 84 us with four waves, 32 positions and two workgroups, 75 us so; with keys of 128 the same change
 // took 2 x 1024 rows from 192 to 221 us.
-constexpr int attend_size(int dk, int nt) { return nt == 16 || (nt == 8 && dk == 192) ? 8 : 4; }
+constexpr int attend_size(int dk, int nt) { return nt == 16 || (nt == 8 && dk >= 192) ? 8 : 4; }
 constexpr int attend_fit(int dk, int nt) { return nt == 1 ? (dk <= 128 ? 3 : 2) : attend_size(dk, nt) == 8 || dk > 192 ? 1 : 2; }
 constexpr int attend_waves(int dk, int nt) { return attend_fit(dk, nt) * attend_size(dk, nt) / 4; }
 // Positions of a tile of the shared kernel.
-constexpr int attend_keys(int dk) { return dk <= 192 ? 64 : 32; }
+constexpr int attend_keys(int dk) { return dk <= 256 ? 64 : 32; }
+// Column tiles of 16 rows of a wave of tiles of 128 rows.
+constexpr int attend_columns(int dk) { return dk <= 192 ? 2 : 1; }
 int launch_attend_mxfp4(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream);
 int launch_attend_nvfp4(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream);
 int launch_attend_mxfp8(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream);
