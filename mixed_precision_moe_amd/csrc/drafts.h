@@ -51,7 +51,7 @@ constexpr int attend_waves(int dk, int nt) { return attend_fit(dk, nt) * attend_
 // Positions of a tile of the shared kernel.
 constexpr int attend_keys(int dk) { return dk <= 256 ? 64 : 32; }
 // Column tiles of 16 rows of a wave of tiles of 128 rows.
-constexpr int attend_columns(int dk) { return dk <= 192 ? 2 : 1; }
+constexpr int attend_columns(int dk) { return dk <= 128 ? 2 : 1; }
 int launch_attend_mxfp4(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream);
 int launch_attend_nvfp4(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream);
 int launch_attend_mxfp8(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream);
