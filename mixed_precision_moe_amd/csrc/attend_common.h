@@ -12,7 +12,8 @@
 // Both kernels form S^T = K Q^T and O^T = V^T P^T: a row of q is a column of both, so its maximum, sum and rescaling stay in
 // one lane (and three others, which hold other positions), and S^T leaves the matrix instruction as P^T enters the next one.
 // Values are exact in bf16 (at most six significant bits), so both products are of what the cache holds; V is read back from
-// LDS transposed.
+// LDS transposed.  The weights are rounded to bf16, as the second product needs them, and their sum is of the rounded ones.
+// Few rows a key head (up to 32): attend_split.h; more: attend_shared.h.
 #pragma once
 
 #include <hip/hip_runtime.h>

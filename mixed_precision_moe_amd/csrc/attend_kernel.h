@@ -8,7 +8,9 @@ namespace {
 
 // Joins the parts of the items that a worker begins and others go on with.  blockIdx.x: entry of `open`, blockIdx.y: rows of
 // the tile, blockIdx.z: the head in the worker's group.  A row of a part is LANES lanes; the rest of the wave's have other
-// rows where the parts are few, else other parts of the same row.
+// rows where the parts are few, else other parts of the same row; kAhead parts are asked for at a time.  Bound by the parts'
+// trip: 67 MB of 2 x 1024 rows of 8 x 4 heads join in 14 us, 64 parts of one context's 35 rows a head in 7.7 (22 with a
+// workgroup for each of a tile's rows that takes a part after the other).
 template <int FMT, int DV, int NT>
 __global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendArgs a, const float* __restrict__ part,
                                                                const float2* __restrict__ part_ml,
@@ -123,15 +125,14 @@ int launch_dims(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream
   if (p.nt == 2)
     return launch_both<FMT, DV, 2>(a, p, ws, stream, paged ? attend_split_kernel<FMT, DK, DV, 2, attend_waves(DK, 2), true>
                                                            : attend_split_kernel<FMT, DK, DV, 2, attend_waves(DK, 2), false>);
-  constexpr int KEYS = attend_keys(DK);
   if constexpr (DK <= 128)
-    if (p.nt == 4) return launch_both<FMT, DV, 4>(a, p, ws, stream, attend_shared_kernel<FMT, DK, DV, 2, 4, 2, KEYS, attend_waves(DK, 4)>);
+    if (p.nt == 4) return launch_both<FMT, DV, 4>(a, p, ws, stream, attend_shared_kernel<FMT, DK, DV, 2, 4, 2, attend_waves(DK, 4)>);
   constexpr int W8 = attend_size(DK, 8), W16 = attend_size(DK, 16);
   if constexpr (DK <= 192)
     if (p.nt == 16)
-      return launch_both<FMT, DV, 16>(a, p, ws, stream, attend_shared_kernel<FMT, DK, DV, 2, W16, 8, KEYS, attend_waves(DK, 16)>, 64 * W16);
+      return launch_both<FMT, DV, 16>(a, p, ws, stream, attend_shared_kernel<FMT, DK, DV, 2, W16, 8, attend_waves(DK, 16)>, 64 * W16);
   constexpr int NT = attend_columns(DK);
-  return launch_both<FMT, DV, 8>(a, p, ws, stream, attend_shared_kernel<FMT, DK, DV, NT, W8, 8 / NT, KEYS, attend_waves(DK, 8)>, 64 * W8);
+  return launch_both<FMT, DV, 8>(a, p, ws, stream, attend_shared_kernel<FMT, DK, DV, NT, W8, 8 / NT, attend_waves(DK, 8)>, 64 * W8);
 }
 
 template <int FMT>

@@ -1,17 +1,27 @@
 // Attention for many rows a key head: a worker's waves share tiles of K and V, dequantized into LDS.
 //
-// A worker takes 32 WR rows, WR waves of 32 rows each; with WR = 2 the waves come in two groups that have half of each
+// A worker takes 16 NT WR rows, W waves: WR of them with 16 NT rows each, in W / WR groups that have each their part of a
 // tile's positions.  Per tile every thread dequantizes its pieces of 16 bytes of codes, so that is paid once for all rows, and
 // codes leave the caches once for all of them.  Two tiles of K and V are in LDS: while one is worked on, the codes of the next
 // are on their way to registers, and they are dequantized into the other behind it, with one barrier a tile.  Pages are
-// looked up three tiles ahead.
+// looked up four tiles ahead, and made addresses three tiles ahead.
+//
+// Bound, where rows are many, by the matrix cores beside the exponentials and conversions: two waves a matrix core overlap them
+// in part.  By LDS too (what a wave reads it uses for 16 NT rows: 32 took 66 us where 16, with twice the waves, took 92),
+// so NT is 2 where the registers of two waves hold it, and 1 for more than 128 elements (256: 726 us against 1427 with two
+// column tiles and one wave).  1024 rows a sequence of 8 query heads a key head, 4 sequences, 4096 positions before them,
+// MXFP8: 942 TFLOP/s (128 elements), 852 (256), MXFP4 1010 (192 and 128).  Few rows and long contexts by what a worker does
+// once: 12 sequences of 264 rows a key head and 5000 positions took 65 us, 23 of them for finding and loading what comes first.
 #pragma once
 
 #include "attend_common.h"
 
 namespace {
 
-template <int FMT, int DK, int DV, int NT, int W, int WR, int KEYS>
+constexpr int KEYS = kAttendKeys;  // a lane each where they are looked up
+static_assert(KEYS == 64, "the lanes of a wave");
+
+template <int FMT, int DK, int DV, int NT, int W, int WR>
 struct Shared {
   static constexpr int kThreads = 64 * W;
   static constexpr int kWK = W / WR;           // groups of waves that share the positions
@@ -24,7 +34,7 @@ struct Shared {
 };
 
 // A thread's pieces of a plane's tile.
-template <int FMT, int KEYS, int D, int kThreads>
+template <int FMT, int D, int kThreads>
 struct Pieces {
   static constexpr int kElems = 16 * kPerByte<FMT>, kPerKey = D / kElems, kAll = KEYS * kPerKey;
   static constexpr int kN = (kAll + kThreads - 1) / kThreads;
@@ -92,13 +102,13 @@ struct Pieces {
   }
 };
 
-template <int FMT, int DK, int DV, int NT, int W, int WR, int KEYS, int WAVES>
+template <int FMT, int DK, int DV, int NT, int W, int WR, int WAVES>
 __global__ __launch_bounds__(64 * W, WAVES) void attend_shared_kernel(AttendArgs given, float* __restrict__ part,
                                                                         float2* __restrict__ part_ml,
                                                                         Open* __restrict__ open, Totals* __restrict__ totals, int workers) {
-  using Sh = Shared<FMT, DK, DV, NT, W, WR, KEYS>;
+  using Sh = Shared<FMT, DK, DV, NT, W, WR>;
   constexpr int MT = Sh::kRows, R = 16 * NT, KT = Sh::kKT;
-  static_assert(KT % 2 == 0 && KEYS <= 64, "32 positions a matrix instruction, and 64 a lookup");
+  static_assert(KT % 2 == 0, "32 positions a matrix instruction");
   constexpr int kBytes = 2 * Sh::kTileBytes;
   // the sums take the place of the tiles, as many waves' rows at a time as fit
   constexpr int kFit = kBytes / (R * (DV + 4) * 4), kGroups = kFit >= WR ? WR : kFit >= 4 ? 4 : kFit >= 2 ? 2 : 1;
@@ -132,17 +142,17 @@ __global__ __launch_bounds__(64 * W, WAVES) void attend_shared_kernel(AttendArgs
     const auto find = [&](int32_t k, int32_t page) -> int64_t {
       const CacheArgs& c = a.cache;
       const uint32_t pos = (uint32_t)k * KEYS + lane;
-      if (lane >= KEYS || pos >= (uint32_t)end || page < 0 || page >= c.num_pages) return -1;
+      if (pos >= (uint32_t)end || page < 0 || page >= c.num_pages) return -1;
       const uint32_t at = pos - a.page_of(pos) * (uint32_t)c.page_size;
       return ((int64_t)page * c.page_size + at) * c.heads + w.group;
     };
     const auto note = [&](int32_t k, int64_t vector) {
-      if (lane < KEYS) vectors[k & 3][lane] = vector;
+      vectors[k & 3][lane] = vector;
       const uint64_t there = __ballot(vector >= 0);
       if (lane == 0) valid[k & 3] = there;
     };
-    Pieces<FMT, KEYS, DK, Sh::kThreads> kp;
-    Pieces<FMT, KEYS, DV, Sh::kThreads> vp;
+    Pieces<FMT, DK, Sh::kThreads> kp;
+    Pieces<FMT, DV, Sh::kThreads> vp;
     const auto tile_k = [&](int32_t k) { return (uint16_t*)(lds + (k & 1) * Sh::kTileBytes); };
     const auto tile_v = [&](int32_t k) { return (uint16_t*)(lds + (k & 1) * Sh::kTileBytes) + KEYS * Sh::kStrideK; };
     const auto load = [&](int32_t k) {

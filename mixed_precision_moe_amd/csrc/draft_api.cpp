@@ -115,7 +115,7 @@ AttendPlan attend_plan(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows,
     p.heads_log = positions <= 128 ? 0 : d->heads % 4 == 0 ? 2 : d->heads % 2 == 0 ? 1 : 0;
     p.unit_log = 7 - p.heads_log;
   } else {
-    p.unit_log = attend_keys(p.dk) == 64 ? 6 : 5;
+    p.unit_log = 6;  // kAttendKeys
   }
   const int64_t groups = d->heads >> p.heads_log, fill = (int64_t)kCus * attend_fit(p.dk, p.nt) / groups;
   p.workers = (int32_t)(fill < 1 ? 1 : fill < 8 ? fill : fill & ~int64_t(7));  // as many on each XCD

@@ -1,4 +1,4 @@
-// What the C entry points of draft_api.cpp hand to their kernels: attention over the paged cache (attend.hip), moving
+// What the C entry points of draft_api.cpp hand to their kernels: attention over the paged cache (attend_*.hip), moving
 // and counting its rows and pages (pages.hip), rotary positions (rotary.hip).
 #pragma once
 
@@ -48,8 +48,7 @@ struct AttendPlan {
 constexpr int attend_size(int dk, int nt) { return nt == 16 || (nt == 8 && dk >= 192) ? 8 : 4; }
 constexpr int attend_fit(int dk, int nt) { return nt == 1 ? (dk <= 128 ? 3 : 2) : attend_size(dk, nt) == 8 || dk > 192 ? 1 : 2; }
 constexpr int attend_waves(int dk, int nt) { return attend_fit(dk, nt) * attend_size(dk, nt) / 4; }
-// Positions of a tile of the shared kernel.
-constexpr int attend_keys(int dk) { return dk <= 256 ? 64 : 32; }
+constexpr int kAttendKeys = 64;  // positions of a tile that waves share
 // Column tiles of 16 rows of a wave of tiles of 128 rows.
 constexpr int attend_columns(int dk) { return dk <= 128 ? 2 : 1; }
 int launch_attend_mxfp4(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream);
