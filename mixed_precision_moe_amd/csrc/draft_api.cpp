@@ -147,8 +147,8 @@ int check_attend(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows, int32
   if (st) return st;
   if (d->v_dim < 1 || d->k_dim > kMaxDim || d->v_dim > kMaxDim) return MXFP4_ERR_SHAPE;
   if (q_heads < 1 || q_heads > kMaxHeads || q_heads % d->heads) return MXFP4_ERR_SHAPE;
-  // rows of a key head, and positions, are counted in 32 bits
-  if (rows < 0 || rows >= kMaxRows || n_seqs < 0 || rows * (q_heads / d->heads) >= kMaxRows - 64) return MXFP4_ERR_SHAPE;
+  // rows of a key head, those past the last in a tile too, and positions are counted in 32 bits
+  if (rows < 0 || rows >= kMaxRows || n_seqs < 0 || rows * (q_heads / d->heads) >= kMaxRows - 256) return MXFP4_ERR_SHAPE;
   return MXFP4_OK;
 }
 

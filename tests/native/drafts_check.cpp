@@ -145,6 +145,11 @@ static void test_attend() {
   d = kOk;
   CHECK(mxfp4_cache_attend_workspace_bytes(&d, 3, 5, 2) == 0 && mxfp4_cache_attend_workspace_bytes(nullptr, 4, 5, 2) == 0);
   CHECK(mxfp4_cache_attend_workspace_bytes(&d, 4, 0, 0) > 0);
+  // rows of a key head up to the end of the largest tile are counted in 32 bits
+  d.heads = 1;
+  CHECK(mxfp4_cache_attend_workspace_bytes(&d, 1, (int64_t(1) << 31) - 257, 1) > 0);
+  CHECK(mxfp4_cache_attend_workspace_bytes(&d, 1, (int64_t(1) << 31) - 256, 1) == 0);
+  CHECK(mxfp4_cache_attend_workspace_bytes(&d, 4, (int64_t(1) << 29) - 64, 1) == 0);
 }
 
 // The division by the page size is exact for every position.
