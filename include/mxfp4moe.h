@@ -405,7 +405,7 @@ int mxfp4_cache_read(const mxfp4_cache_dims* d, const void* k_q, const void* k_s
  *   q_heads a multiple of heads, q_heads <= 2^16.  k_dim and v_dim at most 256, v_dim > 0.  scale finite.
  *   max_pages * page_size <= 2^31 - 256, rows * q_heads / heads < 2^31 - 256.
  * out device bf16 or fp32 (out_is_fp32), element (row, head, i) at row * out_ldt + head * out_ldh + i, strides multiples
- *   of 8, 16-byte aligned; its vectors must not overlap.
+ *   of 8, 16-byte aligned; its vectors must not overlap each other or q.
  * tree_mask device uint8, row t of mask_cols entries at t * ld_mask, or NULL.
  * Arithmetic: values are exact in bf16 (code * scale), products accumulate in fp32, the maximum and the sum of the
  * softmax are fp32, the weights p are rounded to bf16 before the second product; parts of a long context are joined in

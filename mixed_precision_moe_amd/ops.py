@@ -397,7 +397,7 @@ class PagedCache:
         tree_mask[row, j] set: j counts from the sequence's first row.  Positions without a page are not seen.  scale
         (None: k_dim ** -0.5) multiplies the scores.  Returns [rows, q_heads, v_dim] in out_dtype (bfloat16 or float32);
         a row that sees nothing gets zeros.  Rows outside every sequence are undefined, or in `out` (strided like q)
-        left as they were.  Forward only: a q that asks for a gradient is refused."""
+        left as they were; `out` and q must not overlap.  Forward only: a q that asks for a gradient is refused."""
         _gpu_of("the cache", self._storage[0], q, page_table, cu_rows, start, tree_mask, out)
         if torch.is_grad_enabled() and q.requires_grad:
             raise ValueError("attend has no backward pass: detach q, or call it under torch.no_grad()")
