@@ -136,7 +136,7 @@ struct Tiles {
     const int64_t n = a.mask ? s.drafts : min(s.rows, row + (part > 0));
     const int64_t e = min(s.start + n, (int64_t)a.cache.max_pages * a.cache.page_size);
     end = e < 0 ? 0 : (int32_t)e;
-    units = end == 0 ? 1 : (end - 1 >> a.unit_log) + 1;
+    units = end == 0 ? 1 : ((end - 1) >> a.unit_log) + 1;
   }
   MX_DEV void begin(const AttendArgs& a, const Seq& s) {
     tile = 0;
