@@ -456,8 +456,10 @@ int mxfp4_cache_copy_pages(const mxfp4_cache_dims* d, const int32_t* src, const 
  *
  * copies device int32 [3, n_rows] (fork: [3, n]): the source page, new page and tokens of each row (pair) whose page has
  * to be copied, as mxfp4_cache_copy_pages takes them; -1, -1, 0 where there is none.
- * missing device int32 [1]: pages that were wanted when no page was free any more; their entries are -1 (a shared page
- * that was to be replaced stays).
+ * missing device int32 [1]: pages that were wanted when no page was free any more; their entries are -1.  So is that of a
+ * shared page that was to be replaced: the row lets go of it, and of its tokens in it, and the other rows keep them.  Where
+ * every row that held such a page let go of it or got a copy, the last of those that could not be given one keeps it as its
+ * own, and none is missing there.
  * workspace device, 256-byte aligned, >= mxfp4_pool_workspace_bytes(num_pages, n_rows or n, max_pages).
  * num_pages < 2^31, page_size >= 1, n_rows <= 2^24, n <= 2^16, n_rows * max_pages and n * max_pages < 2^31. */
 size_t mxfp4_pool_workspace_bytes(int64_t num_pages, int32_t n, int32_t max_pages);

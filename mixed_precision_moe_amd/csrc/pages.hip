@@ -319,7 +319,7 @@ MX_DEV int32_t scan(int32_t v, int32_t* part, int32_t& total) {
 
 template <bool FORK>
 __global__ __launch_bounds__(kPool) void pool_take_kernel(PoolArgs a, Items it) {
-  __shared__ int32_t part[kPool / 64];
+  __shared__ int32_t part[kPool / 64], kept;
   const int t = threadIdx.x;
   int32_t wanted = 0, all;
   for (int c = 0; c < a.n; c += kPool) {
@@ -358,15 +358,19 @@ __global__ __launch_bounds__(kPool) void pool_take_kernel(PoolArgs a, Items it) 
     found += all;
   }
   if (found > wanted) found = wanted;
-  if (t == 0) *a.missing = wanted - found;
+  if (t == 0) kept = 0;
   __syncthreads();
   // hand them out: page r of the list goes to the last item whose offset is at most r
-  for (int32_t r = t; r < wanted; r += kPool) {
+  const auto item_of = [&](int32_t r) {
     int lo = 0, hi = a.n - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (it.offset[mid] <= r) lo = mid; else hi = mid - 1;
     }
+    return lo;
+  };
+  for (int32_t r = t; r < wanted; r += kPool) {
+    const int lo = item_of(r);
     const int32_t page = r < found ? it.list[r] : -1, from = it.from[lo];
     const int32_t row = FORK ? a.dst[lo] : lo;
     int32_t* entry = a.table + (int64_t)row * a.ld_table + it.first[lo] + (r - it.offset[lo]);
@@ -379,11 +383,39 @@ __global__ __launch_bounds__(kPool) void pool_take_kernel(PoolArgs a, Items it) 
         a.copies[a.n + lo] = page;
       }
     } else if (from >= 0) {
-      a.copies[2 * (int64_t)a.n + lo] = 0;  // resize: the shared page stays; fork: its entry is -1 already
+      a.copies[2 * (int64_t)a.n + lo] = 0;
+      if (!FORK) atomicSub(&a.refs[from], 1);  // (fork: its entry is -1 already)
     } else {
       *entry = -1;
     }
   }
+  // Rows whose shared page could not be replaced have let go of it, so that none writes where another reads.  A page that
+  // nobody holds any more stays with the last of its rows: the highest, whatever the order of the atomics.
+  if (!FORK && found < wanted) {
+    const auto refs_of = [&](int32_t page) { return __hip_atomic_load(&a.refs[page], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
+    __threadfence();
+    __syncthreads();
+    for (int32_t r = found + t; r < wanted; r += kPool) {
+      const int lo = item_of(r);
+      const int32_t from = it.from[lo];
+      if (from >= 0 && refs_of(from) <= 0) atomicMin(&a.refs[from], -1 - lo);
+    }
+    __threadfence();
+    __syncthreads();
+    for (int32_t r = found + t; r < wanted; r += kPool) {
+      const int lo = item_of(r);
+      const int32_t from = it.from[lo];
+      if (from < 0) continue;
+      if (refs_of(from) == -1 - lo) {
+        atomicExch(&a.refs[from], 1);
+        atomicAdd(&kept, 1);
+      } else {
+        a.table[(int64_t)lo * a.ld_table + it.first[lo]] = -1;
+      }
+    }
+    __syncthreads();
+  }
+  if (t == 0) *a.missing = wanted - found - kept;
 }
 
 int status() { return hipGetLastError() == hipSuccess ? MXFP4_OK : MXFP4_ERR_DEVICE; }

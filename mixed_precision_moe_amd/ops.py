@@ -522,7 +522,9 @@ class PagePool:
         """Row b of page_table (int32 [B, pages]) then holds the pages of lengths[b] tokens (int32 [B]; negative: the row
         is left alone; as many pages as the table has columns at most): pages are taken, or given back (0: all).  Where
         the length ends inside a page that the row shares, it gets a copy of its own.  Returns int32, 0-dim: the pages that
-        were wanted when none was free; their entries are -1, where `write` and `attend` pass over them."""
+        were wanted when none was free; their entries are -1, where `write` and `attend` pass over them.  That holds for a
+        shared page that was to be replaced too: the row gives up its tokens there, unless no other row holds the page
+        any more, whose last row then keeps it.  (Make room first where a row must not lose them.)"""
         _gpu_of("the cache", self._refs, page_table, lengths)
         n = page_table.shape[0] if page_table.dim() == 2 else 0
         _check_list(lengths, "lengths", n)

@@ -81,9 +81,12 @@ def resize_ref(refs, table, lengths, page_size, planes=()):
     copies, missing = [], 0
     for (b, i, old), page in zip(wants, pages):
         if page < 0:
+            if old is not None:
+                if refs[old] == 1:  # the others have let go of it: it is the row's own
+                    continue
+                refs[old] -= 1
             missing += 1
-            if old is None:
-                table[b, i] = -1
+            table[b, i] = -1
             continue
         table[b, i] = page
         refs[page] = 1
