@@ -50,6 +50,9 @@ def _gpu_of(name, first, *others):
 
 _current_gpu = torch.cuda.current_device
 
+# For tensors of the caller's that a kernel has written: a backward pass that saved one must not go on with what it holds now.
+_changed = torch.autograd.graph.increment_version
+
 
 def _call(index, fn, *args):
     """fn(*args, stream) on the current stream of GPU `index`, which need not be the current device."""
@@ -238,7 +241,8 @@ def fp4_expert_matvec(x, w_q, w_s, expert_offsets, sorted_pairs, bias=None, *, f
     _need(not swiglu or N % 2 == 0, "swiglu needs an even number of rows")
     is_fp32 = _check_bias(bias, (E, N))
     width = N // 2 if swiglu else N
-    if y is None:
+    given = y is not None
+    if not given:
         out_fp32 = _check_out(out_dtype)
         y = torch.empty((P, width), dtype=out_dtype, device=x.device)
     else:
@@ -247,6 +251,8 @@ def fp4_expert_matvec(x, w_q, w_s, expert_offsets, sorted_pairs, bias=None, *, f
     _call(gpu, "fp4_expert_matvec", fmt, w_q.data_ptr(), w_s.data_ptr(), _ptr(global_scales), E, N, K, _ptr(bias),
           is_fp32, x.data_ptr(), ldx, top_k, expert_offsets.data_ptr(), sorted_pairs.data_ptr(), P, 1 if swiglu else 0,
           y.data_ptr(), out_fp32)
+    if given:
+        _changed(y)
     return y
 
 
@@ -376,7 +382,8 @@ class PagedCache:
         rows outside every sequence are left as they were and whose vectors must not overlap.
         Positions without a page read as zeros."""
         index = self._index(page_table, cu_rows, start)
-        if k_out is None:
+        given = k_out is not None
+        if not given:
             _need(rows is not None and rows >= 0 and v_out is None, "give rows, or the outputs")
             k_out = torch.empty((rows, self._heads, self._k_dim), dtype=torch.bfloat16, device=self._device)
             if self._v_dim:
@@ -385,6 +392,8 @@ class PagedCache:
         planes = self._planes(k_out, v_out)
         _need(rows is None or rows == k_out.shape[0], "rows must be the outputs' rows")
         _call(self._gpu, "mxfp4_cache_read", self._dref, *self._memory(), k_out.shape[0], *index, *planes)
+        if given:
+            _changed((k_out,) if v_out is None else (k_out, v_out))
         return k_out, v_out
 
     def attend(self, q, page_table, cu_rows, start=None, tree_mask=None, scale=None, out=None, out_dtype=torch.bfloat16):
@@ -408,7 +417,8 @@ class PagedCache:
         _need_int32(q_heads)
         _need(q_heads > 0 and q_heads % self._heads == 0, "q_heads must be a multiple of the cache's heads")
         q_args = _vectors(q, "q", q_heads, self._k_dim)
-        if out is None:
+        given = out is not None
+        if not given:
             out_fp32 = _check_out(out_dtype)
             out = torch.empty((rows, q_heads, self._v_dim), dtype=out_dtype, device=self._device)
         else:
@@ -432,6 +442,8 @@ class PagedCache:
         ws = torch.empty(nws, dtype=torch.uint8, device=self._device)
         _call(self._gpu, "mxfp4_cache_attend", self._dref, *self._memory(), *q_args, q_heads, rows, *index, mask, ld_mask, W,
               scale, *_vectors(out, "out", q_heads, self._v_dim), out_fp32, ws.data_ptr(), nws)
+        if given:
+            _changed(out)
         return out
 
     def compact(self, page_table, start, path):

@@ -4,7 +4,7 @@ import math
 
 import torch
 
-from .ops import _call, _gpu_of, _need, _need_int32, _vectors
+from .ops import _call, _changed, _gpu_of, _need, _need_int32, _vectors
 
 
 def rotary_frequencies(dim, base=10000.0, scaling=None):
@@ -131,14 +131,15 @@ class Rotary:
     def __call__(self, q, k, positions, inplace=False):
         """q [rows, q_heads, head_dim] and k [rows, k_heads, head_dim] (or None), bf16 or fp32, rows and heads strided as
         they like; positions int32 [rows].  Returns both turned (contiguous), differentiable in q and k any number of
-        times; with inplace, in their own memory (not where a gradient is asked for; the elements outside the turned part
-        are then not touched).  To capture the backward pass into a graph, drop every eager autograd graph of the same
+        times; with inplace, in their own memory (not where a gradient is asked for, and a backward pass that saved them is
+        then refused by autograd; the elements outside the turned part are not touched).  To capture the backward pass into a graph, drop every eager autograd graph of the same
         leaves first, as torch asks for any backward pass."""
         tensors = (q,) if k is None else (q, k)
         if inplace:
             _need(not (torch.is_grad_enabled() and any(t.requires_grad for t in tensors)),
-                  "inplace has no backward pass: detach q and k, or call it under torch.no_grad()")
+                  "inplace has no backward pass: a gradient needs the form that is not in place")
             out = self._apply(tensors, positions, False, out=tensors)
+            _changed(tensors)
         else:
             out = self._turn(tensors, positions, False)
         return out[0], None if k is None else out[1]
