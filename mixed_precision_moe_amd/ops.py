@@ -54,6 +54,16 @@ _current_gpu = torch.cuda.current_device
 _changed = torch.autograd.graph.increment_version
 
 
+def _no_tangent(what, *tensors):
+    """Refuses forward-mode derivatives, which a kernel behind raw pointers would drop without a word."""
+    # outside every dual level, where unpacking would cost a small call more than a microsecond, there are none
+    if _forward_ad._current_level >= 0 and any(_forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise ValueError(f"{what} has no forward-mode derivative")
+
+
+_forward_ad = torch.autograd.forward_ad
+
+
 def _call(index, fn, *args):
     """fn(*args, stream) on the current stream of GPU `index`, which need not be the current device."""
     if index == _current_gpu():
@@ -410,6 +420,7 @@ class PagedCache:
         _gpu_of("the cache", self._storage[0], q, page_table, cu_rows, start, tree_mask, out)
         if torch.is_grad_enabled() and q.requires_grad:
             raise ValueError("attend has no backward pass: detach q, or call it under torch.no_grad()")
+        _no_tangent("attend", q)
         index = self._index(page_table, cu_rows, start)
         _need(self._v_dim > 0, "attend needs a cache with keys and values (v_dim > 0)")
         _need(q.dtype == torch.bfloat16 and q.dim() == 3, f"q: bf16 [rows, q_heads, {self._k_dim}]")

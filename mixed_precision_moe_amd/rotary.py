@@ -4,7 +4,7 @@ import math
 
 import torch
 
-from .ops import _call, _changed, _gpu_of, _need, _need_int32, _vectors
+from .ops import _call, _changed, _gpu_of, _need, _need_int32, _no_tangent, _vectors
 
 
 def rotary_frequencies(dim, base=10000.0, scaling=None):
@@ -124,6 +124,7 @@ class Rotary:
         return made
 
     def _turn(self, tensors, positions, inverse):
+        _no_tangent("Rotary", *tensors)
         if torch.is_grad_enabled() and (tensors[0].requires_grad or tensors[-1].requires_grad):
             return _Rotary.apply(self, inverse, positions, *tensors)
         return self._apply(tensors, positions, inverse)
@@ -131,11 +132,13 @@ class Rotary:
     def __call__(self, q, k, positions, inplace=False):
         """q [rows, q_heads, head_dim] and k [rows, k_heads, head_dim] (or None), bf16 or fp32, rows and heads strided as
         they like; positions int32 [rows].  Returns both turned (contiguous), differentiable in q and k any number of
-        times; with inplace, in their own memory (not where a gradient is asked for, and a backward pass that saved them is
-        then refused by autograd; the elements outside the turned part are not touched).  To capture the backward pass into a graph, drop every eager autograd graph of the same
-        leaves first, as torch asks for any backward pass."""
+        times (backward; forward-mode tangents are refused); with inplace, in their own memory (not where a gradient is
+        asked for, and a backward pass that saved them is then refused by autograd; the elements outside the turned part
+        are not touched).  To capture the backward pass into a graph, drop every eager autograd graph of the same leaves
+        first, as torch asks for any backward pass."""
         tensors = (q,) if k is None else (q, k)
         if inplace:
+            _no_tangent("Rotary", *tensors)
             _need(not (torch.is_grad_enabled() and any(t.requires_grad for t in tensors)),
                   "inplace has no backward pass: a gradient needs the form that is not in place")
             out = self._apply(tensors, positions, False, out=tensors)

@@ -52,3 +52,49 @@ def test_given_results_are_seen_by_autograd(calls):  # noqa: F811
                          i32(0, 1, 2, 3), y=y)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         loss.backward()
+
+
+@pytest.mark.parametrize("which", ["q", "k", "both"])
+@pytest.mark.parametrize("how", ["plain", "inplace", "requires_grad"])
+def test_tangents_of_forward_mode_are_refused(calls, which, how):  # noqa: F811
+    import torch.autograd.forward_ad as fw
+    rot, p = mx.Rotary(32, device="cpu"), i32(0, 1, 2)
+    q, k = torch.zeros(3, 2, 32), torch.zeros(3, 1, 32)
+    with fw.dual_level():
+        if which != "k":
+            q = fw.make_dual(q, torch.ones_like(q))
+        if which != "q":
+            k = fw.make_dual(k, torch.ones_like(k))
+        if how == "requires_grad":
+            q.requires_grad_()
+        with pytest.raises(ValueError, match="forward-mode"):
+            rot(q, k, p, inplace=how == "inplace")
+        rot(torch.zeros(3, 2, 32), torch.zeros(3, 1, 32), p)  # nothing to lose
+    assert len(calls) == 1
+
+
+def test_tangents_of_the_attention_and_of_a_backward_pass_are_refused(calls):  # noqa: F811
+    import torch.autograd.forward_ad as fw
+    c = cache()
+    q, table, cu = torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.zeros(1, 2, dtype=torch.int32), i32(0, 3)
+    with fw.dual_level(), torch.no_grad():
+        for out in (None, torch.zeros(3, 4, 32, dtype=torch.bfloat16)):
+            with pytest.raises(ValueError, match="forward-mode"):
+                c.attend(fw.make_dual(q, torch.ones_like(q)), table, cu, out=out)
+    assert not calls
+    c.attend(q, table, cu)
+    rot, x = mx.Rotary(32, device="cpu"), torch.zeros(3, 2, 32, requires_grad=True)
+    y, _ = rot(x, None, i32(0, 1, 2))
+    with fw.dual_level():
+        with pytest.raises(ValueError, match="forward-mode"):
+            torch.autograd.grad(y, x, fw.make_dual(torch.ones_like(y), torch.ones_like(y)))
+
+
+def test_function_transforms_are_not_passed_by(calls):  # noqa: F811
+    """torch.func's wrapped tensors have no memory of their own: every transform ends in an error, none in a lost derivative."""
+    rot, p = mx.Rotary(32, device="cpu"), i32(0, 1, 2)
+    x = torch.zeros(3, 2, 32)
+    for transform in (lambda f: torch.func.jvp(f, (x,), (x,)), lambda f: torch.func.grad(lambda y: f(y).sum())(x),
+                      lambda f: torch.func.vmap(f)(x[None])):
+        with pytest.raises((ValueError, RuntimeError)):
+            transform(lambda y: rot(y, None, p)[0])
