@@ -56,7 +56,9 @@ class _Rotary(torch.autograd.Function):
         ctx.handle, ctx.inverse = handle, inverse
         ctx.save_for_backward(positions)
         ctx.set_materialize_grads(False)
-        return handle._apply(tensors, positions, inverse)
+        made = handle._apply(tensors, positions, inverse)
+        ctx.mark_non_differentiable(*(x for x, asks in zip(made, ctx.needs_input_grad[3:]) if not asks))
+        return made
 
     @staticmethod
     def backward(ctx, *grads):

@@ -98,3 +98,19 @@ def test_function_transforms_are_not_passed_by(calls):  # noqa: F811
                       lambda f: torch.func.vmap(f)(x[None])):
         with pytest.raises((ValueError, RuntimeError)):
             transform(lambda y: rot(y, None, p)[0])
+
+
+def test_only_what_asks_for_a_gradient_gets_one(calls):  # noqa: F811
+    rot, p = mx.Rotary(32, device="cpu"), i32(0, 1, 2)
+    q, k = torch.zeros(3, 2, 32, requires_grad=True), torch.zeros(3, 1, 32)
+    for a, b in ((q, k), (k, q)):
+        calls.clear()
+        x, y = rot(a, b, p)
+        assert x.requires_grad is a.requires_grad and y.requires_grad is b.requires_grad
+        grad = x if a is q else y
+        assert torch.autograd.grad(grad.sum(), q)[0].shape == q.shape
+        assert calls[-1][1][13] == 2 and calls[-1][1][17] is None  # q's gradient alone is turned back
+    # of a second derivative too
+    x, y = rot(q, k, p)
+    g, = torch.autograd.grad(x, q, torch.ones_like(x, requires_grad=True), create_graph=True)
+    assert g.requires_grad and g.grad_fn is not None
