@@ -135,14 +135,15 @@ class Rotary:
         """q [rows, q_heads, head_dim] and k [rows, k_heads, head_dim] (or None), bf16 or fp32, rows and heads strided as
         they like; positions int32 [rows].  Returns both turned (contiguous), differentiable in q and k any number of
         times (backward; forward-mode tangents are refused); with inplace, in their own memory (not where a gradient is
-        asked for, and a backward pass that saved them is then refused by autograd; the elements outside the turned part
-        are not touched).  To capture the backward pass into a graph, drop every eager autograd graph of the same leaves
-        first, as torch asks for any backward pass."""
+        asked for, and a backward pass that saved them is then refused by autograd; they must not overlap; the elements
+        outside the turned part are not touched).  To capture the backward pass into a graph, drop every eager autograd
+        graph of the same leaves first, as torch asks for any backward pass."""
         tensors = (q,) if k is None else (q, k)
         if inplace:
             _no_tangent("Rotary", *tensors)
             _need(not (torch.is_grad_enabled() and any(t.requires_grad for t in tensors)),
                   "inplace has no backward pass: a gradient needs the form that is not in place")
+            _need(k is None or q.shape[0] == 0 or q.data_ptr() != k.data_ptr(), "in place, q and k must not overlap")
             out = self._apply(tensors, positions, False, out=tensors)
             _changed(tensors)
         else:

@@ -114,3 +114,15 @@ def test_only_what_asks_for_a_gradient_gets_one(calls):  # noqa: F811
     x, y = rot(q, k, p)
     g, = torch.autograd.grad(x, q, torch.ones_like(x, requires_grad=True), create_graph=True)
     assert g.requires_grad and g.grad_fn is not None
+
+
+def test_one_memory_is_not_turned_twice_at_once(calls):  # noqa: F811
+    rot, p, x = mx.Rotary(32, device="cpu"), i32(0, 1, 2), torch.zeros(3, 2, 32)
+    for k in (x, x[:, :1], x.detach()):
+        with pytest.raises(ValueError, match="overlap"):
+            rot(x, k, p, inplace=True)
+    assert not calls and x._version == 0
+    rot(x, x, p)
+    rot(x[:, :1], x[:, 1:], p, inplace=True)
+    rot(x[:0], x[:0], p[:0], inplace=True)
+    assert len(calls) == 3
