@@ -32,6 +32,7 @@ def rotary_frequencies(dim, base=10000.0, scaling=None):
     if kind == "linear":
         f = f / factor
     elif kind == "ramp":
+        _need("length" in s, "kind='ramp' needs length")
         length, fast, slow = s.pop("length"), s.pop("fast", 32.0), s.pop("slow", 1.0)
         magnitude = s.pop("magnitude", 1.0 + 0.1 * math.log(factor))
         # the index of a pair that turns n times over the length
@@ -40,6 +41,7 @@ def rotary_frequencies(dim, base=10000.0, scaling=None):
         ramp = ((torch.arange(dim // 2, dtype=torch.float64) - low) / max(high - low, 0.001)).clamp(0, 1)
         f = f * (1 - ramp) + f / factor * ramp
     elif kind == "bands":
+        _need("length" in s, "kind='bands' needs length")
         length, low, high = s.pop("length"), s.pop("low", 1.0), s.pop("high", 4.0)
         _need(high > low, "high must be above low")
         kept = ((length * f / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
