@@ -14,7 +14,7 @@ def rotary_frequencies(dim, base=10000.0, scaling=None):
       None                      as they are
       kind="linear", factor     divided by factor
       kind="base", factor       base * factor ** (dim / (dim - 2)): the slowest is divided by factor, the fastest kept
-      kind="ramp", factor, length, fast=32, slow=1, magnitude=1 + 0.1 ln(factor)
+      kind="ramp", factor, length, fast=32, slow=1, magnitude=1 + 0.1 ln(factor) (1 for factors below 1)
           pairs that turn more than `fast` times over `length` positions are kept, those that turn fewer than `slow`
           times divided by factor, with a ramp over the pairs between; queries and keys are multiplied by magnitude
       kind="bands", factor, length, low=1, high=4
@@ -33,8 +33,9 @@ def rotary_frequencies(dim, base=10000.0, scaling=None):
         f = f / factor
     elif kind == "ramp":
         _need("length" in s, "kind='ramp' needs length")
+        _need(base != 1, "kind='ramp' needs a base other than 1")
         length, fast, slow = s.pop("length"), s.pop("fast", 32.0), s.pop("slow", 1.0)
-        magnitude = s.pop("magnitude", 1.0 + 0.1 * math.log(factor))
+        magnitude = s.pop("magnitude", 1.0 + 0.1 * math.log(max(factor, 1.0)))
         # the index of a pair that turns n times over the length
         pair = lambda n: dim * math.log(length / (2 * math.pi * n)) / (2 * math.log(base))  # noqa: E731
         low, high = max(0, math.floor(pair(fast))), min(dim - 1, math.ceil(pair(slow)))
