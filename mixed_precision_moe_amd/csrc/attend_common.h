@@ -571,7 +571,8 @@ MX_DEV void write_item(const AttendArgs& a, const Work<MT>& w, int g, int worker
     const int r = r0 + id / (DV / 8), e = id % (DV / 8) * 8;
     float top = ms[r], sum = 0.0f;
     for (int x = 1; x < parts; x++) top = fmaxf(top, ms[x * MT + r]);
-    for (int x = 0; x < parts; x++) sum += top > -INFINITY ? ls[x * MT + r] * __builtin_amdgcn_exp2f(ms[x * MT + r] - top) : 0.0f;
+    // a row without a maximum has sums of 0, or of NaN where all its scores are
+    for (int x = 0; x < parts; x++) sum += ls[x * MT + r] * (top > -INFINITY ? __builtin_amdgcn_exp2f(ms[x * MT + r] - top) : 1.0f);
     const f32x4_t* src = reinterpret_cast<const f32x4_t*>(sums + (r - r0) * (DV + 4) + e);
     const f32x4_t x = src[0], y = src[1];
     if (!whole) {

@@ -64,8 +64,7 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendArgs a, con
       }
 #pragma unroll
       for (int j = 0; j < kAhead; j++) {
-        const float f = __builtin_amdgcn_exp2f(ml[j].x - by);
-        if (f == 0.0f) continue;  // what its sums are is of no account
+        const float f = __builtin_amdgcn_exp2f(ml[j].x - by);  // 0 too: a part's NaN stays one
         sum += f * ml[j].y;
 #pragma unroll
         for (int c = 0; c < 4; c++) {
