@@ -402,7 +402,8 @@ int mxfp4_cache_read(const mxfp4_cache_dims* d, const void* k_q, const void* k_s
  * A position without a page (mxfp4_cache_write) is not seen; what lies there or in places that the mask hides is not
  * looked at.  A row that sees nothing gets zeros.  Rows outside every sequence are not read and keep their output.
  * q device bf16, element (row, head, i) at row * q_ldt + head * q_ldh + i, strides multiples of 8, 16-byte aligned,
- *   q_heads a multiple of heads, q_heads <= 2^16.  k_dim and v_dim at most 256, v_dim > 0.  scale finite.
+ *   q_heads a multiple of heads, q_heads <= 2^16.  k_dim and v_dim at most 256, v_dim > 0.  scale finite, log2(e) times
+ *   it too (NVFP4: divided by the keys' global scale).
  *   max_pages * page_size <= 2^31 - 256, rows * q_heads / heads < 2^31 - 256.
  * out device bf16 or fp32 (out_is_fp32), element (row, head, i) at row * out_ldt + head * out_ldh + i, strides multiples
  *   of 8, 16-byte aligned; its vectors must not overlap each other or q.

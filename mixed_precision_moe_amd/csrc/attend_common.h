@@ -360,11 +360,12 @@ struct Work {
 // ---------------------------------------------------------------------------------------------
 // Softmax.
 
-// What the scores are multiplied by before exp2.  Not 0, so that its product with a hidden position's -inf is one.
+// What the scores are multiplied by before exp2.  Not 0, so that its product with a hidden position's -inf is one: the smallest
+// number that binary32 has, with which no score reaches 2^-20.  Finite: the host has seen to that.
 template <int FMT>
 MX_DEV float score_scale(const AttendArgs& a) {
   const float s = a.scale == 0.0f ? 1.0f : fabsf(a.scale);
-  return fmaxf(s * 1.44269504f / (FMT == MXFP4_FMT_NVFP4 ? a.cache.plane[0].gs : 1.0f), 1e-38f);
+  return fmaxf(s * 1.44269504f / (FMT == MXFP4_FMT_NVFP4 ? a.cache.plane[0].gs : 1.0f), 0x1p-149f);
 }
 
 // A wave's 16 NT rows of q, a lane's elements first(i) to first(i) + 7 of them.  `load` asks for places that are there

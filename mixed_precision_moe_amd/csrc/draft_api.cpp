@@ -3,6 +3,8 @@
 // include/mxfp4moe.h.
 #include <hip/hip_runtime_api.h>
 
+#include <cmath>
+
 #include "api_checks.h"
 #include "drafts.h"
 
@@ -173,7 +175,8 @@ MX_API int mxfp4_cache_attend(const mxfp4_cache_dims* d, const void* k_q, const 
   int st = check_attend(d, q_heads, rows, n_seqs);
   if (st || (st = check_flags(out_is_fp32, 0, 0))) return st;
   if (!table_fits(ld_table, n_seqs, max_pages) || (int64_t)max_pages * d->page_size > kMaxRows - 256) return MXFP4_ERR_SHAPE;
-  if (!(scale >= -3.40282347e38f && scale <= 3.40282347e38f)) return MXFP4_ERR_SHAPE;
+  // what the kernels multiply the scores by: finite too (the comparison also rejects NaN)
+  if (!(std::fabs(scale) * 1.44269504f / (d->fmt == MXFP4_FMT_NVFP4 ? d->k_global_scale : 1.0f) <= 3.40282347e38f)) return MXFP4_ERR_SHAPE;
   auto bad_ld = [&](int64_t ldt, int64_t ldh, int32_t dim) {
     return ldt < 0 || ldt % 8 || ldt > kMaxLd || ldh < 0 || ldh % 8 || ldh > kMaxLd || (q_heads > 1 && ldh < dim) ||
            (rows > 1 && ldt < dim);
