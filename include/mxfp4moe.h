@@ -409,9 +409,9 @@ int mxfp4_cache_read(const mxfp4_cache_dims* d, const void* k_q, const void* k_s
  *   of 8, 16-byte aligned; its vectors must not overlap each other or q.
  * tree_mask device uint8, row t of mask_cols entries at t * ld_mask, or NULL.
  * Arithmetic: values are exact in bf16 (code * scale), products accumulate in fp32, the maximum and the sum of the
- * softmax are fp32, the weights p are rounded to bf16 before the second product; parts of a long context are joined in
- * fp32 in a fixed order, and the result is rounded once: repeated calls give the same bits.  Exponentials are the
- * hardware's.  A NaN in a query or in a key that it sees makes the result NaN, one in a value that it sees at least the
+ * softmax are fp32, the weights p are rounded to bf16 before the second product (2^-8 of each; for results in fp32 to two
+ * terms in bf16, 2^-16 of each); parts of a long context are joined in fp32 in a fixed order, and the result is rounded
+ * once: repeated calls give the same bits.  Exponentials are the hardware's.  A NaN in a query or in a key that it sees makes the result NaN, one in a value that it sees at least the
  * element it is in.  A value of 2^128 and more and scores past fp32's range are outside the contract.
  * workspace device, 256-byte aligned, >= mxfp4_cache_attend_workspace_bytes (0: invalid sizes); nothing in it is kept
  * between calls. */

@@ -11,7 +11,8 @@ ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libmxfp4moe.so")
 BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["quantize.hip", "repack.hip", "route.hip", "gemm.hip", "gemm_mx.hip", "linear.hip", "api.cpp", "noalloc.hip",
-           "balance.hip", "matvec.hip", "cache.hip", "ops_api.cpp", "attend_mxfp4.hip", "attend_nvfp4.hip", "attend_mxfp8.hip", "pages.hip", "rotary.hip", "draft_api.cpp"]
+           "balance.hip", "matvec.hip", "cache.hip", "ops_api.cpp", "attend_mxfp4.hip", "attend_nvfp4.hip", "attend_mxfp8.hip",
+           "attend_mxfp4_fp32.hip", "attend_nvfp4_fp32.hip", "attend_mxfp8_fp32.hip", "pages.hip", "rotary.hip", "draft_api.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # -packed-fp32-ops keeps the compiler from emitting packed fp32 VALU forms on gfx950.

@@ -12,7 +12,12 @@
 // Both kernels form S^T = K Q^T and O^T = V^T P^T: a row of q is a column of both, so its maximum, sum and rescaling stay in
 // one lane (and three others, which hold other positions), and S^T leaves the matrix instruction as P^T enters the next one.
 // Values are exact in bf16 (at most six significant bits), so both products are of what the cache holds; V is read back from
-// LDS transposed.  The weights are rounded to bf16, as the second product needs them, and their sum is of the rounded ones.
+// LDS transposed.  The weights are rounded to bf16, as the second product needs them, and their sum is of the rounded ones:
+// 2^-8 of each weight, as much as rounding the result to bf16 then costs.  FINE, for results in fp32: what that rounding
+// leaves is a second bf16 term, for another product with the values that are in registers then, and 2^-16 are lost.  A bf16
+// result would gain a third of a bit by it, for up to a tenth of the time with few rows and a quarter with many; with one term and
+// two, 32 sequences of up to 3900 positions, MXFP8: 53.5 and 53.3 us (4 rows a key head), 78.5 and 80.9 (24, pages of 16);
+// MXFP4, 24 rows: 46 and 50; 2 x 1024 rows: 164 and 206; 12 trees, NVFP4: 67 and 75; 130000 positions, MXFP4: 67 and 76.
 // Few rows a key head (up to 32): attend_split.h; more: attend_shared.h.
 #pragma once
 
@@ -405,9 +410,15 @@ struct Query {
   }
 };
 
+// Weights of 16 KT positions, in one or (FINE) two terms.
+template <int NT, int KT, bool FINE>
+struct Weights {
+  bf16x8_t p[NT][KT / 2], rest[FINE ? NT : 1][FINE ? KT / 2 : 1];
+};
+
 // The sums of a wave's 16 NT rows, of their weights too; the exponents' subtrahend m, and the score from which on it is
 // raised.
-template <int NT, int VT>
+template <int NT, int VT, bool FINE>
 struct Rows {
   f32x4_t o[NT][VT], l[NT];
   float m[NT], limit[NT];
@@ -425,7 +436,7 @@ struct Rows {
   // Scores of 16 KT positions to weights in bf16.  m is raised, and all sums with it, where a score is over it by more than
   // 8: weights stay below 2^8, and most tiles need no maximum over the row's four lanes and no rescaling.
   template <int KT>
-  MX_DEV void weights(const f32x4_t (&s)[NT][KT], float sc, bf16x8_t (&p)[NT][KT / 2]) {
+  MX_DEV void weights(const f32x4_t (&s)[NT][KT], float sc, Weights<NT, KT, FINE>& to) {
     bool over = false;
     float top[NT];
 #pragma unroll
@@ -465,17 +476,23 @@ struct Rows {
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
           const bf16x2_t two = __builtin_convertvector(f32x2_t{w[i], w[i + 1]}, bf16x2_t);
-          p[n][h][i] = two[0];
-          p[n][h][i + 1] = two[1];
+          to.p[n][h][i] = two[0];
+          to.p[n][h][i + 1] = two[1];
+          if constexpr (FINE) {
+            const bf16x2_t rest = __builtin_convertvector(f32x2_t{w[i] - (float)two[0], w[i + 1] - (float)two[1]}, bf16x2_t);
+            to.rest[n][h][i] = rest[0];
+            to.rest[n][h][i + 1] = rest[1];
+          }
         }
-        l[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, p[n][h], l[n], 0, 0, 0);
+        l[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, to.p[n][h], l[n], 0, 0, 0);
+        if constexpr (FINE) l[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, to.rest[n][h], l[n], 0, 0, 0);
       }
     }
   }
 
   // O^T += V^T P^T for 32 positions: their values are rows of LDS, `stride` elements apart.
   template <int AHEAD, int KT>
-  MX_DEV void add_values(const uint16_t* v0, int stride, const bf16x8_t (&p)[NT][KT], int h, int lane) {
+  MX_DEV void add_values(const uint16_t* v0, int stride, const Weights<NT, KT, FINE>& w, int h, int lane) {
     // two blocks of four positions by sixteen elements a group of sixteen lanes, transposed
     typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
     const int col = lane & 15, kg = lane >> 4;
@@ -500,7 +517,10 @@ struct Rows {
         const auto& t = x[v0 / AHEAD & 1][v];
         const bf16x8_t both = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(t[0], t[1], 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
-        for (int n = 0; n < NT; n++) o[n][v0 + v] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(both, p[n][h], o[n][v0 + v], 0, 0, 0);
+        for (int n = 0; n < NT; n++) {
+          o[n][v0 + v] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(both, w.p[n][h], o[n][v0 + v], 0, 0, 0);
+          if constexpr (FINE) o[n][v0 + v] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(both, w.rest[n][h], o[n][v0 + v], 0, 0, 0);
+        }
       }
       if (AHEAD > 1) __builtin_amdgcn_sched_barrier(0);
     }

@@ -114,32 +114,33 @@ int launch_both(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream
   return hipGetLastError() == hipSuccess ? MXFP4_OK : MXFP4_ERR_DEVICE;
 }
 
-template <int FMT, int DK, int DV>
+template <int FMT, bool FINE, int DK, int DV>
 int launch_dims(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream) {
   const CacheArgs& c = a.cache;
   const bool paged = c.page_size % kTile == 0 && c.plane[0].dim == DK && c.plane[1].dim == DV;
   if (p.nt == 1)
-    return launch_both<FMT, DV, 1>(a, p, ws, stream, paged ? attend_split_kernel<FMT, DK, DV, 1, attend_waves(DK, 1), true>
-                                                           : attend_split_kernel<FMT, DK, DV, 1, attend_waves(DK, 1), false>);
+    return launch_both<FMT, DV, 1>(a, p, ws, stream, paged ? attend_split_kernel<FMT, DK, DV, 1, attend_waves(DK, 1), true, FINE>
+                                                           : attend_split_kernel<FMT, DK, DV, 1, attend_waves(DK, 1), false, FINE>);
   if (p.nt == 2)
-    return launch_both<FMT, DV, 2>(a, p, ws, stream, paged ? attend_split_kernel<FMT, DK, DV, 2, attend_waves(DK, 2), true>
-                                                           : attend_split_kernel<FMT, DK, DV, 2, attend_waves(DK, 2), false>);
+    return launch_both<FMT, DV, 2>(a, p, ws, stream, paged ? attend_split_kernel<FMT, DK, DV, 2, attend_waves(DK, 2), true, FINE>
+                                                           : attend_split_kernel<FMT, DK, DV, 2, attend_waves(DK, 2), false, FINE>);
   if constexpr (DK <= 128)
-    if (p.nt == 4) return launch_both<FMT, DV, 4>(a, p, ws, stream, attend_shared_kernel<FMT, DK, DV, 2, 4, 2, attend_waves(DK, 4)>);
+    if (p.nt == 4) return launch_both<FMT, DV, 4>(a, p, ws, stream, attend_shared_kernel<FMT, DK, DV, 2, 4, 2, attend_waves(DK, 4), FINE>);
   constexpr int W8 = attend_size(DK, 8), W16 = attend_size(DK, 16);
   if constexpr (DK <= 192)
     if (p.nt == 16)
-      return launch_both<FMT, DV, 16>(a, p, ws, stream, attend_shared_kernel<FMT, DK, DV, 2, W16, 8, attend_waves(DK, 16)>, 64 * W16);
+      return launch_both<FMT, DV, 16>(a, p, ws, stream, attend_shared_kernel<FMT, DK, DV, 2, W16, 8, attend_waves(DK, 16), FINE>, 64 * W16);
   constexpr int NT = attend_columns(DK);
-  return launch_both<FMT, DV, 8>(a, p, ws, stream, attend_shared_kernel<FMT, DK, DV, NT, W8, 8 / NT, attend_waves(DK, 8)>, 64 * W8);
+  return launch_both<FMT, DV, 8>(a, p, ws, stream, attend_shared_kernel<FMT, DK, DV, NT, W8, 8 / NT, attend_waves(DK, 8), FINE>, 64 * W8);
 }
 
-template <int FMT>
+// FINE: for results in fp32.
+template <int FMT, bool FINE>
 int launch_format(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream) {
-  if (p.dk == 64) return launch_dims<FMT, 64, 64>(a, p, ws, stream);
-  if (p.dk == 128) return launch_dims<FMT, 128, 128>(a, p, ws, stream);
-  if (p.dk == 192) return launch_dims<FMT, 192, 128>(a, p, ws, stream);
-  return launch_dims<FMT, 256, 256>(a, p, ws, stream);
+  if (p.dk == 64) return launch_dims<FMT, FINE, 64, 64>(a, p, ws, stream);
+  if (p.dk == 128) return launch_dims<FMT, FINE, 128, 128>(a, p, ws, stream);
+  if (p.dk == 192) return launch_dims<FMT, FINE, 192, 128>(a, p, ws, stream);
+  return launch_dims<FMT, FINE, 256, 256>(a, p, ws, stream);
 }
 
 }  // namespace

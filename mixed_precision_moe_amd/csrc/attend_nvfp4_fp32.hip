@@ -1,0 +1,6 @@
+// Attention over the paged cache: the kernels for NVFP4, results in fp32.
+#include "attend_kernel.h"
+
+int launch_attend_nvfp4_fp32(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream) {
+  return launch_format<MXFP4_FMT_NVFP4, true>(a, p, ws, stream);
+}

@@ -102,7 +102,7 @@ struct Pieces {
   }
 };
 
-template <int FMT, int DK, int DV, int NT, int W, int WR, int WAVES>
+template <int FMT, int DK, int DV, int NT, int W, int WR, int WAVES, bool FINE>
 __global__ __launch_bounds__(64 * W, WAVES) void attend_shared_kernel(AttendArgs given, float* __restrict__ part,
                                                                         float2* __restrict__ part_ml,
                                                                         Open* __restrict__ open, Totals* __restrict__ totals, int workers) {
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(64 * W, WAVES) void attend_shared_kernel(AttendArgs
     const AttendArgs a = arguments();
     // the positions before this one are seen by all of the wave's rows: with a mask the context, else the first row's drafts too
     const int32_t seen = (int32_t)min((int64_t)s.start + (a.mask ? 0 : (uint32_t)(w.ti.tile * MT + R * wr) / (uint32_t)a.group + 1), (int64_t)INT32_MAX);
-    Rows<NT, DV / 16> rows;
+    Rows<NT, DV / 16, FINE> rows;
     rows.clear();
 
     // the page of this lane's position of tile k, and that position's vector
@@ -212,12 +212,12 @@ __global__ __launch_bounds__(64 * W, WAVES) void attend_shared_kernel(AttendArgs
       const uint64_t there = valid[k & 3] >> (16 * KT * wk) & kFull;
       const uint64_t b = ((uint64_t)bad[k & 3][1] << 32 | bad[k & 3][0]) >> (16 * KT * wk) & kFull;
       if (__builtin_expect(there != kFull || b != 0 || base + 16 * KT > seen, 0)) hide<NT, KT>(arguments(), s, draft, base, there, b, kg, sv);
-      bf16x8_t p[NT][KT / 2];
+      Weights<NT, KT, FINE> p;
       rows.template weights<KT>(sv, sc, p);
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int h = 0; h < KT / 2; h++)
-        rows.template add_values<4, KT / 2>(tile_v(k) + (16 * KT * wk + 32 * h) * Sh::kStrideV, Sh::kStrideV, p, h, lane);
+        rows.template add_values<4, KT>(tile_v(k) + (16 * KT * wk + 32 * h) * Sh::kStrideV, Sh::kStrideV, p, h, lane);
       __builtin_amdgcn_s_setprio(0);
       // the other tiles' turn
       if (k + 1 < k1) store(k + 1);

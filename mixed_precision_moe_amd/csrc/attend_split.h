@@ -35,7 +35,7 @@ struct Shape {
 
 // PAGED: pages of whole tiles, and dimensions that are DK and DV.  A tile's page is then looked up once, and a lane's part
 // of the addresses does not change from tile to tile: 49 us where the other form took 66 (32 sequences, MXFP8).
-template <int FMT, int DK, int DV, int NT, int WAVES, bool PAGED>
+template <int FMT, int DK, int DV, int NT, int WAVES, bool PAGED, bool FINE>
 __global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArgs given, float* __restrict__ part,
                                                                  float2* __restrict__ part_ml, Open* __restrict__ open,
                                                                  Totals* __restrict__ totals, int workers) {
@@ -191,7 +191,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArg
     query.finish(arguments(), element);
     const auto& q = query.q;
     const auto& draft = query.draft;
-    Rows<NT, Sh::kVT> rows;
+    Rows<NT, Sh::kVT, FINE> rows;
     rows.clear();
 
     const auto step = [&](int32_t k, auto more) {
@@ -260,7 +260,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArg
         hide<NT, 2>(arguments(), s, draft, base, there, bad, kg, sv);
       }
 
-      bf16x8_t p[NT][1];
+      Weights<NT, 2, FINE> p;
       rows.template weights<2>(sv, sc, p);
 
       // V into LDS, a row a position
@@ -277,7 +277,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArg
       }
       if (kMore) load_v(k + 1, next);
       __builtin_amdgcn_wave_barrier();
-      rows.template add_values<1, 1>(vt, Sh::kStride, p, 0, lane);
+      rows.template add_values<1, 2>(vt, Sh::kStride, p, 0, lane);
       __builtin_amdgcn_wave_barrier();
       found = next;
       next = after;

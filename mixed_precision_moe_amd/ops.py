@@ -415,8 +415,10 @@ class PagedCache:
         rows those up to itself, or with tree_mask (bool or uint8 [rows, W], rows may be strided) those j < W with
         tree_mask[row, j] set: j counts from the sequence's first row.  Positions without a page are not seen.  scale
         (None: k_dim ** -0.5) multiplies the scores.  Returns [rows, q_heads, v_dim] in out_dtype (bfloat16 or float32);
-        a row that sees nothing gets zeros, NaN in a query or in what it sees gives NaN.  Rows outside every sequence are undefined, or in `out` (strided like q)
-        left as they were; `out` and q must not overlap.  Forward only: a q that asks for a gradient is refused."""
+        bfloat16: the softmax's weights are rounded to it before they meet the values, float32: 2^-16 of them are lost;
+        a row that sees nothing gets zeros, NaN in a query or in what it sees gives NaN.  Rows outside every sequence are
+        undefined, or in `out` (strided like q) left as they were; `out` and q must not overlap.  Forward only: a q that
+        asks for a gradient is refused."""
         _gpu_of("the cache", self._storage[0], q, page_table, cu_rows, start, tree_mask, out)
         if torch.is_grad_enabled() and q.requires_grad:
             raise ValueError("attend has no backward pass: detach q, or call it under torch.no_grad()")
