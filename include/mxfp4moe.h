@@ -411,8 +411,10 @@ int mxfp4_cache_read(const mxfp4_cache_dims* d, const void* k_q, const void* k_s
  * Arithmetic: values are exact in bf16 (code * scale), products accumulate in fp32, the maximum and the sum of the
  * softmax are fp32, the weights p are rounded to bf16 before the second product (2^-8 of each; for results in fp32 to two
  * terms in bf16, 2^-16 of each); parts of a long context are joined in fp32 in a fixed order, and the result is rounded
- * once: repeated calls give the same bits.  Exponentials are the hardware's.  A NaN in a query or in a key that it sees makes the result NaN, one in a value that it sees at least the
- * element it is in.  A value of 2^128 and more and scores past fp32's range are outside the contract.
+ * once: repeated calls give the same bits.  Exponentials are the hardware's.  A NaN in a query or in a key that it sees
+ * makes the result NaN, one in a value that it sees at least the element it is in.  Outside the contract are keys of 2^128
+ * and more, scores past fp32's range, and values of 2^88 and more (NVFP4: before the division by the global scale, so
+ * none): their sums over up to 2^31 positions, with weights below 2^9, are formed before they are divided.
  * workspace device, 256-byte aligned, >= mxfp4_cache_attend_workspace_bytes (0: invalid sizes); nothing in it is kept
  * between calls. */
 size_t mxfp4_cache_attend_workspace_bytes(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows, int32_t n_seqs);

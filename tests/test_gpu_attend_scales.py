@@ -49,3 +49,15 @@ def test_scales_too_large_to_multiply_with():
     assert not small.attend(q, t, cu, scale=1.0).any()
     with pytest.raises(mx.Mxfp4Error):
         small.attend(q, t, cu, scale=10.0)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("have,new,group", [([9000, 40], [1, 2], 4), ([9000], [8], 3), ([3000], [60], 4)])
+def test_values_up_to_the_bound(fmt, have, new, group):
+    s = T.Setup(fmt, 32, 1, 64, 64, have, new, group)
+    s.cache.v_s.copy_((s.cache.v_s.int() + 84).clamp(max=254))
+    held = torch.from_numpy(s.values()[1][np.concatenate([32 * row[row >= 0] for row in s.table])])
+    assert 2.0 ** 84 < float(held.abs().max()) < 2.0 ** 88
+    got = s.cache.attend(s.q, *s.args(), out_dtype=torch.float32)
+    assert bool(torch.isfinite(got).all())
+    s.check(got, half_step=2.0 ** -24)
