@@ -54,6 +54,12 @@ _current_gpu = torch.cuda.current_device
 _changed = torch.autograd.graph.increment_version
 
 
+def _check_given(*tensors):
+    """Results that the caller gives: what they held before has no gradient through the call."""
+    _need(not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)),
+          "a result that is given must not ask for a gradient")
+
+
 def _no_tangent(what, *tensors):
     """Refuses forward-mode derivatives, which a kernel behind raw pointers would drop without a word."""
     # outside every dual level, where unpacking would cost a small call more than a microsecond, there are none
@@ -257,6 +263,7 @@ def fp4_expert_matvec(x, w_q, w_s, expert_offsets, sorted_pairs, bias=None, *, f
         y = torch.empty((P, width), dtype=out_dtype, device=x.device)
     else:
         out_fp32 = _check_out(y.dtype)
+        _check_given(y)
         _need(y.shape == (P, width) and y.is_contiguous(), "y: contiguous [P, N] (swiglu: [P, N/2])")
     _call(gpu, "fp4_expert_matvec", fmt, w_q.data_ptr(), w_s.data_ptr(), _ptr(global_scales), E, N, K, _ptr(bias),
           is_fp32, x.data_ptr(), ldx, top_k, expert_offsets.data_ptr(), sorted_pairs.data_ptr(), P, 1 if swiglu else 0,
@@ -398,6 +405,8 @@ class PagedCache:
             k_out = torch.empty((rows, self._heads, self._k_dim), dtype=torch.bfloat16, device=self._device)
             if self._v_dim:
                 v_out = torch.empty((rows, self._heads, self._v_dim), dtype=torch.bfloat16, device=self._device)
+        else:
+            _check_given(k_out, v_out)
         _gpu_of("the cache", self._storage[0], k_out, v_out, page_table, cu_rows, start)
         planes = self._planes(k_out, v_out)
         _need(rows is None or rows == k_out.shape[0], "rows must be the outputs' rows")
@@ -437,6 +446,7 @@ class PagedCache:
         else:
             out_fp32 = _check_out(out.dtype)
             _need(out.shape[0] == rows, "out must have q's rows")
+            _check_given(out)
         mask, ld_mask, W = None, 0, 0
         if tree_mask is not None:
             _need(tree_mask.dtype in (torch.bool, torch.uint8) and tree_mask.dim() == 2 and tree_mask.shape[0] == rows,

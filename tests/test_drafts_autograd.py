@@ -126,3 +126,18 @@ def test_one_memory_is_not_turned_twice_at_once(calls):  # noqa: F811
     rot(x[:, :1], x[:, 1:], p, inplace=True)
     rot(x[:0], x[:0], p[:0], inplace=True)
     assert len(calls) == 3
+
+
+def test_results_that_ask_for_a_gradient_are_refused(calls):  # noqa: F811
+    c = cache()
+    table, cu = torch.zeros(1, 2, dtype=torch.int32), i32(0, 3)
+    bf16 = lambda *s, grad=False: torch.zeros(*s, dtype=torch.bfloat16, requires_grad=grad)  # noqa: E731
+    q, out, k, v = bf16(3, 4, 64), bf16(3, 4, 32, grad=True), bf16(3, 2, 64, grad=True), bf16(3, 2, 32, grad=True)
+    for call in (lambda: c.attend(q, table, cu, out=out), lambda: c.read(table, cu, k_out=k, v_out=v.detach()),
+                 lambda: c.read(table, cu, k_out=k.detach(), v_out=v)):
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+        assert not calls
+        with torch.no_grad():
+            call()
+        calls.clear()
