@@ -409,8 +409,8 @@ int mxfp4_cache_read(const mxfp4_cache_dims* d, const void* k_q, const void* k_s
  *   of 8, 16-byte aligned; its vectors must not overlap each other or q.
  * tree_mask device uint8, row t of mask_cols entries at t * ld_mask, or NULL.
  * Arithmetic: values are exact in bf16 (code * scale), products accumulate in fp32, the maximum and the sum of the
- * softmax are fp32, the weights p are rounded to bf16 before the second product (2^-8 of each; for results in fp32 to two
- * terms in bf16, 2^-16 of each); parts of a long context are joined in fp32 in a fixed order, and the result is rounded
+ * softmax are fp32, the weights p are rounded to bf16 before the second product (2^-8 of each; for results in fp32, and
+ * where a sequence has up to 16 rows a key head on average, to two terms in bf16, 2^-16 of each); parts of a long context are joined in fp32 in a fixed order, and the result is rounded
  * once: repeated calls give the same bits.  Exponentials are the hardware's.  A NaN in a query or in a key that it sees
  * makes the result NaN, one in a value that it sees at least the element it is in.  Outside the contract are keys of 2^128
  * and more, scores past fp32's range, and values of 2^88 and more (NVFP4: before the division by the global scale, so

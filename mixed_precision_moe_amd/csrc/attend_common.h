@@ -13,11 +13,12 @@
 // one lane (and three others, which hold other positions), and S^T leaves the matrix instruction as P^T enters the next one.
 // Values are exact in bf16 (at most six significant bits), so both products are of what the cache holds; V is read back from
 // LDS transposed.  The weights are rounded to bf16, as the second product needs them, and their sum is of the rounded ones:
-// 2^-8 of each weight, as much as rounding the result to bf16 then costs.  FINE, for results in fp32: what that rounding
-// leaves is a second bf16 term, for another product with the values that are in registers then, and 2^-16 are lost.  A bf16
-// result would gain a third of a bit by it, for up to a tenth of the time with few rows and a quarter with many; with one term and
-// two, 32 sequences of up to 3900 positions, MXFP8: 53.5 and 53.3 us (4 rows a key head), 78.5 and 80.9 (24, pages of 16);
-// MXFP4, 24 rows: 46 and 50; 2 x 1024 rows: 164 and 206; 12 trees, NVFP4: 67 and 75; 130000 positions, MXFP4: 67 and 76.
+// 2^-8 of each weight, as much as rounding the result to bf16 then costs.  FINE: what that rounding leaves is a second bf16
+// term, for another product with the values that are in registers then, and 2^-16 are lost.  It is taken for results in fp32, and
+// for up to 16 rows a key head, where memory hides it (32 sequences of up to 3900 positions, 4 rows, MXFP8: 53.5 us without
+// and 53.3 with it; over formats, sizes and page sizes 0 to 4 % more).  With more rows it costs more than the third of a bit that
+// a bf16 result would gain: 24 rows MXFP8, pages of 16: 78.5 and 80.9 us, MXFP4: 46 and 50; 2 x 1024 rows MXFP8: 164 and 206;
+// 12 trees of up to 33 drafts, NVFP4: 67 and 75; 130000 positions, MXFP4: 67 and 76.
 // Few rows a key head (up to 32): attend_split.h; more: attend_shared.h.
 #pragma once
 

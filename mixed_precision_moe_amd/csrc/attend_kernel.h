@@ -118,9 +118,10 @@ template <int FMT, bool FINE, int DK, int DV>
 int launch_dims(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream) {
   const CacheArgs& c = a.cache;
   const bool paged = c.page_size % kTile == 0 && c.plane[0].dim == DK && c.plane[1].dim == DV;
-  if (p.nt == 1)
-    return launch_both<FMT, DV, 1>(a, p, ws, stream, paged ? attend_split_kernel<FMT, DK, DV, 1, attend_waves(DK, 1), true, FINE>
-                                                           : attend_split_kernel<FMT, DK, DV, 1, attend_waves(DK, 1), false, FINE>);
+  if constexpr (!FINE)  // with two terms of the weights whatever the result's type is
+    if (p.nt == 1)
+      return launch_both<FMT, DV, 1>(a, p, ws, stream, paged ? attend_split_kernel<FMT, DK, DV, 1, attend_waves(DK, 1), true, true>
+                                                             : attend_split_kernel<FMT, DK, DV, 1, attend_waves(DK, 1), false, true>);
   if (p.nt == 2)
     return launch_both<FMT, DV, 2>(a, p, ws, stream, paged ? attend_split_kernel<FMT, DK, DV, 2, attend_waves(DK, 2), true, FINE>
                                                            : attend_split_kernel<FMT, DK, DV, 2, attend_waves(DK, 2), false, FINE>);
@@ -134,7 +135,7 @@ int launch_dims(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream
   return launch_both<FMT, DV, 8>(a, p, ws, stream, attend_shared_kernel<FMT, DK, DV, NT, W8, 8 / NT, attend_waves(DK, 8), FINE>, 64 * W8);
 }
 
-// FINE: for results in fp32.
+// FINE: for results in fp32 and more than 16 rows a key head.
 template <int FMT, bool FINE>
 int launch_format(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream) {
   if (p.dk == 64) return launch_dims<FMT, FINE, 64, 64>(a, p, ws, stream);

@@ -1,7 +1,7 @@
-// Attention over the paged cache: the kernels for MXFP4, results in bf16.
+// Attention over the paged cache: the kernels for MXFP4, results in bf16, and all with up to 16 rows a key head.
 #include "attend_kernel.h"
 
 int launch_attend_mxfp4(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream) {
-  if (a.out_fp32) return launch_attend_mxfp4_fp32(a, p, ws, stream);
+  if (a.out_fp32 && p.nt > 1) return launch_attend_mxfp4_fp32(a, p, ws, stream);
   return launch_format<MXFP4_FMT_MXFP4, false>(a, p, ws, stream);
 }

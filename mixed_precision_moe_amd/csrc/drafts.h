@@ -54,7 +54,7 @@ constexpr int attend_columns(int dk) { return dk <= 128 ? 2 : 1; }
 int launch_attend_mxfp4(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream);
 int launch_attend_nvfp4(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream);
 int launch_attend_mxfp8(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream);
-// (what those call for results in fp32)
+// (what those call for results in fp32 with nt > 1)
 int launch_attend_mxfp4_fp32(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream);
 int launch_attend_nvfp4_fp32(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream);
 int launch_attend_mxfp8_fp32(const AttendArgs& a, const AttendPlan& p, uint8_t* ws, hipStream_t stream);

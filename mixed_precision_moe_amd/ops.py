@@ -424,7 +424,8 @@ class PagedCache:
         rows those up to itself, or with tree_mask (bool or uint8 [rows, W], rows may be strided) those j < W with
         tree_mask[row, j] set: j counts from the sequence's first row.  Positions without a page are not seen.  scale
         (None: k_dim ** -0.5) multiplies the scores.  Returns [rows, q_heads, v_dim] in out_dtype (bfloat16 or float32);
-        bfloat16: the softmax's weights are rounded to it before they meet the values, float32: 2^-16 of them are lost;
+        bfloat16: the softmax's weights are rounded to it before they meet the values where a sequence has more than 16 rows
+        a key head on average; float32, or fewer rows: 2^-16 of them are lost;
         a row that sees nothing gets zeros, NaN in a query or in what it sees gives NaN.  Rows outside every sequence are
         undefined, or in `out` (strided like q) left as they were; `out` and q must not overlap.  Forward only: a q that
         asks for a gradient is refused."""

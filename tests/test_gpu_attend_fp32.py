@@ -52,3 +52,15 @@ def test_trees_and_scales(fmt, new, group):
 @pytest.mark.parametrize("fmt", list(FMTS))
 def test_parts_that_are_joined(fmt):
     check(Setup(fmt, 64, 1, 64, 64, [2000, 3], [2, 1], 2))
+
+
+@pytest.mark.parametrize("fmt", list(FMTS))
+@pytest.mark.parametrize("page,heads,group,k_dim,v_dim,have,new", [
+    (16, 2, 4, 64, 64, [77], [1]), (32, 4, 2, 64, 64, [300, 5], [1, 3]), (64, 3, 5, 96, 160, [63, 64, 129], [1, 2, 3]),
+    (32, 2, 8, 192, 128, [300, 5], [1, 2]), (64, 1, 1, 256, 256, [500], [16])])
+def test_few_rows_in_bf16_lose_no_more_than_their_rounding(fmt, page, heads, group, k_dim, v_dim, have, new):
+    """Up to 16 rows a key head: the bf16 result is the fp32 one, rounded once."""
+    s = Setup(fmt, page, heads, k_dim, v_dim, have, new, group)
+    check(s)
+    fine = s.cache.attend(s.q, *s.args(), out_dtype=torch.float32)
+    assert torch.equal(s.cache.attend(s.q, *s.args()), fine.bfloat16())
