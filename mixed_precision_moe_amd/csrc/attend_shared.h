@@ -9,9 +9,10 @@
 // Bound, where rows are many, by the matrix cores beside the exponentials and conversions: two waves a matrix core overlap them
 // in part.  By LDS too (what a wave reads it uses for 16 NT rows: 32 took 66 us where 16, with twice the waves, took 92),
 // so NT is 2 where the registers of two waves hold it, and 1 for more than 128 elements (256: 726 us against 1427 with two
-// column tiles and one wave).  1024 rows a sequence of 8 query heads a key head, 4 sequences, 4096 positions before them,
-// MXFP8: 942 TFLOP/s (128 elements), 852 (256), MXFP4 1010 (192 and 128).  Few rows and long contexts by what a worker does
-// once: 12 sequences of 264 rows a key head and 5000 positions took 65 us, 23 of them for finding and loading what comes first.
+// column tiles and one wave).  4 sequences of 1024 rows of 8 query heads on each of 4 key heads, 4096 positions before them,
+// with the join: MXFP8 905 TFLOP/s (128 elements), 845 (256), MXFP4 935, 801 and 1020 (192 and 128), NVFP4 877, 768 and 945.
+// Few rows and long contexts by what a worker does once: 12 sequences of up to 264 rows a key head (208 on average) and up to
+// 5000 positions (3754) took 65 us, 23 of them for finding and loading what comes first.
 #pragma once
 
 #include "attend_common.h"

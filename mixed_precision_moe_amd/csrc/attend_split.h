@@ -7,8 +7,9 @@
 // during its softmax and second product, V's during the next tile's first product.
 //
 // Bound by memory once a worker is under way, and by the trips to memory before that (lengths, pages, codes: about 12 us with
-// the launch and the sums' way out).  32 sequences of 3900 positions, 8 key heads, 4 rows each, MXFP8: 48.5 us, 4.2 TB/s of
-// codes and scales with all of that, and 5.5 us for the join; one sequence of 78 positions: 7.8 us.
+// the launch and the sums' way out).  32 sequences of up to 3900 positions (3032 on average), 8 key heads, 4 rows each, MXFP8:
+// 49.0 us, 4.2 TB/s of codes and scales with all of that, and 5.1 us for the join; one sequence of 78 positions: 8.0 us.  The
+// 4-bit formats read half the bytes behind the same trips and conversions: 33 us (MXFP4) and 40 us (NVFP4), with the join.
 #pragma once
 
 #include "attend_common.h"
@@ -34,7 +35,10 @@ struct Shape {
 };
 
 // PAGED: pages of whole tiles, and dimensions that are DK and DV.  A tile's page is then looked up once, and a lane's part
-// of the addresses does not change from tile to tile: 49 us where the other form took 66 (32 sequences, MXFP8).
+// of the addresses does not change from tile to tile.  The same sequences, with the join, us with pages of 64 and of 16 tokens:
+// MXFP8 45, 59 (128 elements), 52, 81 (192 and 128), 95, 159 (256); MXFP4 33, 54; 41, 68; 59, 104; NVFP4 41, 64; 58, 85; 69,
+// 120.  Other sizes take the second form with any page, and the work of the size that they are padded to: 96 elements 55 (MXFP8),
+// 50, 57 us; 160 elements 135, 94, 108 us (floors 30, 15, 16 and 50, 26, 27).
 template <int FMT, int DK, int DV, int NT, int WAVES, bool PAGED, bool FINE>
 __global__ __launch_bounds__(kThreads, WAVES) void attend_split_kernel(AttendArgs given, float* __restrict__ part,
                                                                  float2* __restrict__ part_ml, Open* __restrict__ open,

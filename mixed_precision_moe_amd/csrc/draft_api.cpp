@@ -109,13 +109,13 @@ AttendPlan attend_plan(const mxfp4_cache_dims* d, int32_t q_heads, int64_t rows,
   p.nt = per_seq <= 16 ? 1 : per_seq <= 32 ? 2 : 8;
   if (p.nt == 8 && p.dk <= 192) {
     // Tiles of 256 rows read and dequantize for twice the rows, and leave twice as much to join.  4 sequences of 4096
-    // positions, MXFP4, us with tiles of 128 and 256 rows, by rows a key head; keys of 128: 256: 33, 42; 512: 44, 44;
-    // 8192: 337, 333; of 192: 35, 44; 49, 51; 499, 379; of 64: 29, 34; 36, 34; 287, 245.
+    // positions, MXFP4, us with tiles of 128 and 256 rows, by rows a key head; keys of 128: 256: 34, 42; 512: 44, 45;
+    // 8192: 342, 330; of 192: 35, 46; 48, 53; 511, 380; of 64: 29, 36; 36, 35; 285, 245.
     const int64_t wide = (per_seq + 255) / 256 * 256, narrow = (per_seq + 127) / 128 * 128;
     p.nt = per_seq <= 64 && p.dk <= 128 ? 4 : per_seq > 512 && wide * 8 <= narrow * 9 ? 16 : 8;
   }
   if (p.nt <= 2) {
-    // Heads side by side: 32 sequences of 3900 positions, 8 heads, MXFP8: 49 us and 5 to join, a head a workgroup 59 and 5.  Not
+    // Heads side by side: 32 sequences of up to 3900 positions, 8 heads, MXFP8: 49 us and 5 to join, a head a workgroup 59 and 5.  Not
     // where the positions are few: one unit of all four waves then needs no join (78 positions: 7.8 us; 7.2 and 4.2).
     p.heads_log = positions <= 128 ? 0 : d->heads % 4 == 0 ? 2 : d->heads % 2 == 0 ? 1 : 0;
     p.unit_log = 7 - p.heads_log;

@@ -42,7 +42,7 @@ struct AttendPlan {
   uint64_t part, ml, open, totals, total;
 };
 // Waves of a workgroup, workgroups of a compute unit (what their registers and LDS leave room for), waves of a matrix core.
-// With keys of 192 elements eight waves share a tile of 64 positions: 12 sequences with 264 rows a key head and 5000
+// With keys of 192 elements eight waves share a tile of 64 positions: 12 sequences with up to 264 rows a key head and 5000
 // positions, NVFP4, took 84 us with four waves, 32 positions and two workgroups, 75 us so; with keys of 128 the same change
 // took 2 x 1024 rows from 192 to 221 us.
 constexpr int attend_size(int dk, int nt) { return nt == 16 || (nt == 8 && dk >= 192) ? 8 : 4; }

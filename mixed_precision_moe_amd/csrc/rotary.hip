@@ -6,8 +6,9 @@
 // their angles in LDS first (one a thread, shared by all heads), then runs over the vectors of both tensors in the widest
 // accesses that everything divides by.  8192 x 40 heads of 128 elements, bf16: 31 us, 5.4 TB/s (4 tokens a workgroup; 2: 33,
 // 8: 35); 4099 x 32 heads of 192 with a third turned, fp32: 43 us, 4.7 TB/s (45, 52); 4096 x 32 heads of 128, bf16, with
-// accesses of 16, 8, 4 and 2 bytes: 5.2, 4.5, 3.6 and 2.8 TB/s.  The angle is formed in binary64 and loses its whole turns there (a far position times a frequency has
-// no place left for the fraction in binary32); what rounding the fraction to binary32 loses is put back to first order.
+// accesses of 16, 8, 4 and 2 bytes: 4.8, 4.7, 4.1 and 2.9 TB/s (passes of 14 to 23 us).  The angle is formed in binary64 and loses
+// its whole turns there (a far position times a frequency has no place left for the fraction in binary32); what rounding
+// the fraction to binary32 loses is put back to first order.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
